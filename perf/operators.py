@@ -333,7 +333,7 @@ def prepare(case, seed):
         score = SCALE * _columns(c, q.float()) @ _read(c, cache, True, c["T"], s["places"]).transpose(-1, -2)
         sees = _sees(c, count, s["lens"])[:, None, None]
         score = score.view(B, c["H_kv"], -1, n_q, c["T"]).masked_fill_(~sees, -math.inf)
-        lse = torch.logsumexp(score, -1).permute(0, 3, 1, 2).reshape(B, n_q, c["H_q"])
+        lse = torch.logsumexp(score, -1).permute(0, 3, 1, 2).reshape(B, n_q, c["H_q"]).contiguous()
         del score
         s["lse"] = lse
         if c["path"]:  # as the tree's tokens lie; the others' are finite and must not count
