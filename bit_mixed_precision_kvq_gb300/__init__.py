@@ -24,6 +24,9 @@ __all__ = [
     "kvq_decode_attention_mq", "decode_mq_workspace_bytes", "kvq_decode_mq_workspace_bytes",
     "KVQ_MAX_QUERY_TOKENS", "workspace_status", "kvq_workspace_status", "set_wait_limits",
     "kvq_set_wait_limits", "set_cache_preload", "kvq_set_cache_preload", "STATUS_TILE_WAIT", "STATUS_PEER_WAIT", "STATUS_COUNTER",
+    "decode_tree_workspace_bytes", "kvq_decode_tree_workspace_bytes", "decode_attention_tree",
+    "kvq_decode_attention_tree", "tree_commit", "kvq_tree_commit", "attention_mass", "kvq_attention_mass",
+    "cache_evict", "kvq_cache_evict",
     "SEG_K_CODES", "SEG_K_SZ", "SEG_V_CODES", "SEG_V_SZ", "SEG_PROT_K", "SEG_PROT_V",
     "SEG_TEXT_K", "SEG_TEXT_V", "EXPORTED_SYMBOLS",
 ]
@@ -40,7 +43,8 @@ EXPORTED_SYMBOLS = ["kvq_cache_layout", "kvq_quantize_append", "kvq_decode_atten
                     "kvq_sensitivity_probe", "kvq_probe_workspace_bytes", "kvq_decode_attention_mq",
                     "kvq_decode_mq_workspace_bytes",
                     "kvq_decode_attention_static_ws", "kvq_workspace_status", "kvq_set_wait_limits",
-                    "kvq_set_cache_preload",
+                    "kvq_set_cache_preload", "kvq_decode_tree_workspace_bytes", "kvq_decode_attention_tree",
+                    "kvq_tree_commit", "kvq_attention_mass", "kvq_cache_evict",
                     "kvq_last_cuda_error", "kvq_status_string"]
 STATUS_TILE_WAIT, STATUS_PEER_WAIT, STATUS_COUNTER = 1, 2, 4  # KVQ_STATUS_* bits
 STATIC_WS_BYTES = 16 * 1024 * 1024  # KVQ_STATIC_WS_BYTES
@@ -131,6 +135,17 @@ def load() -> ctypes.CDLL:
     lib.kvq_set_wait_limits.restype = None
     lib.kvq_set_cache_preload.argtypes = [ctypes.c_int32]
     lib.kvq_set_cache_preload.restype = None
+    LP = ctypes.POINTER(Layout)
+    lib.kvq_decode_tree_workspace_bytes.argtypes = [LP, i32]
+    lib.kvq_decode_tree_workspace_bytes.restype = sz
+    lib.kvq_decode_attention_tree.argtypes = [LP, P, P, P, P, i64, i64, i64, i32, P, i64, P, i32, f32, P, P, P, sz, P]
+    lib.kvq_decode_attention_tree.restype = ctypes.c_int
+    lib.kvq_tree_commit.argtypes = [LP, P, P, P, i64, i64, i64, i32, P, i32, P, P, i32, P, P]
+    lib.kvq_tree_commit.restype = ctypes.c_int
+    lib.kvq_attention_mass.argtypes = [LP, P, P, P, i32, P, i32, P, i32, P, f32, P, f32, P, P]
+    lib.kvq_attention_mass.restype = ctypes.c_int
+    lib.kvq_cache_evict.argtypes = [LP, P, P, P, i32, LP, P, i32, i32, P, P, P, P]
+    lib.kvq_cache_evict.restype = ctypes.c_int
     lib.kvq_last_cuda_error.argtypes = []
     lib.kvq_last_cuda_error.restype = ctypes.c_int
     lib.kvq_status_string.argtypes = [ctypes.c_int]
@@ -335,6 +350,153 @@ def decode_attention_static_ws(L: Layout, cache, q, T: int, out,
         raise KvqError(st, "kvq_decode_attention_static_ws")
 
 
+def _tensor(what: str, x, dtype: str, shape, contiguous: bool = True) -> None:
+    """Refuse a tensor (None and raw addresses pass) of another type or shape,
+    with holes, or on another device than the current one: the C call would
+    read it as something else."""
+    if x is None or isinstance(x, int):
+        return
+    import torch
+    if x.dtype != getattr(torch, dtype) or (shape is not None and tuple(x.shape) != shape):
+        raise ValueError(f"{what}: {dtype} of shape {shape} expected, got {x.dtype} {tuple(x.shape)}")
+    if contiguous and not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+
+
+def _cache_bytes(what: str, L: Layout, x) -> None:
+    _tensor(what, x, "uint8", None)
+    if not (x is None or isinstance(x, int)) and x.numel() < L.total_bytes:
+        raise ValueError(f"{what}: {L.total_bytes} bytes expected, got {x.numel()}")
+
+
+def _drafts(L: Layout, k, v, n_q: int):
+    """Strides of the drafted rows ([B, H_kv, n_q, D], last dimension contiguous)."""
+    shape = (L.d.B, L.d.H_kv, n_q, L.d.D)
+    _tensor("k_draft", k, "bfloat16", shape, False)
+    _tensor("v_draft", v, "bfloat16", shape, False)
+    s = k.stride()
+    if s != v.stride():
+        raise ValueError("k_draft and v_draft must share strides")
+    if s[3] != 1:
+        raise ValueError("last dim must be contiguous")
+    return [0 if shape[i] == 1 else s[i] for i in range(3)]
+
+
+def decode_tree_workspace_bytes(L: Layout, n_q: int) -> int:
+    """kvq_decode_tree_workspace_bytes: workspace bytes of decode_attention_tree."""
+    return int(load().kvq_decode_tree_workspace_bytes(ctypes.byref(L), int(n_q)))
+
+
+def decode_attention_tree(L: Layout, cache, q, k_draft, v_draft, tree_mask, T_ctx: int, out,
+                          softmax_scale: Optional[float] = None, lse=None, workspace=None,
+                          ws_bytes: Optional[int] = None, seq_len=None, stream=None) -> None:
+    """kvq_decode_attention_tree: q [B, n_q, H_q, D] bf16, drafted rows
+    k_draft, v_draft [B, H_kv, n_q, D] bf16 (any strides of the first three
+    dimensions that are multiples of 8), tree_mask int64 [B, n_q], or [n_q] or
+    [1, n_q] for one tree of the whole batch (bit j of entry i: token i sees
+    draft j).  Token i attends the cache positions [0, seq_len[b]) ([0, T_ctx)
+    without seq_len) and its drafts; out [B, n_q, H_q, D], lse [B, n_q, H_q]."""
+    d = L.d
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n_q, H_q, D]")
+    n_q = int(q.shape[1])
+    _cache_bytes("cache", L, cache)
+    _tensor("q", q, "bfloat16", (d.B, n_q, d.H_q, d.D))
+    sb, sh, st_ = _drafts(L, k_draft, v_draft, n_q)
+    shared = tree_mask.dim() == 1 or tree_mask.shape[0] != d.B
+    _tensor("tree_mask", tree_mask, "int64", ((n_q,) if tree_mask.dim() == 1 else (1, n_q)) if shared else (d.B, n_q))
+    _tensor("out", out, "bfloat16", (d.B, n_q, d.H_q, d.D))
+    _tensor("lse", lse, "float32", (d.B, n_q, d.H_q))
+    _tensor("seq_len", seq_len, "int32", (d.B,))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d.D)
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = load().kvq_decode_attention_tree(ctypes.byref(L), _addr(cache), _addr(q), _addr(k_draft), _addr(v_draft), sb, sh,
+                                          st_, n_q, _addr(tree_mask), 0 if shared else n_q, _addr(seq_len), int(T_ctx),
+                                          float(softmax_scale), _addr(out), _addr(lse), _addr(workspace), int(ws_bytes),
+                                          _stream(stream))
+    if st != 0:
+        raise KvqError(st, "kvq_decode_attention_tree")
+
+
+def tree_commit(L: Layout, cache, k_draft, v_draft, path, path_len, T_ctx: int, seq_len=None, new_len=None,
+                stream=None) -> None:
+    """kvq_tree_commit: cache position seq_len[b] + k (T_ctx + k without
+    seq_len) takes drafted row path[b, k] (int32 [B, max_path]) for
+    k < path_len[b] (int32 [B]); new_len (int32 [B], other memory than
+    seq_len) gets the new lengths, -1 for an inactive sequence."""
+    d = L.d
+    if k_draft.dim() != 4 or path.dim() != 2:
+        raise ValueError("k_draft must be [B, H_kv, n_q, D] and path [B, max_path]")
+    n_q, max_path = int(k_draft.shape[2]), int(path.shape[1])
+    _cache_bytes("cache", L, cache)
+    sb, sh, st_ = _drafts(L, k_draft, v_draft, n_q)
+    _tensor("path", path, "int32", (d.B, max_path))
+    _tensor("path_len", path_len, "int32", (d.B,))
+    _tensor("seq_len", seq_len, "int32", (d.B,))
+    _tensor("new_len", new_len, "int32", (d.B,))
+    st = load().kvq_tree_commit(ctypes.byref(L), _addr(cache), _addr(k_draft), _addr(v_draft), sb, sh, st_, n_q, _addr(path),
+                                max_path, _addr(path_len), _addr(seq_len), int(T_ctx), _addr(new_len), _stream(stream))
+    if st != 0:
+        raise KvqError(st, "kvq_tree_commit")
+
+
+def attention_mass(L: Layout, cache, q, lse, T: int, mass, mass_in=None, softmax_scale: Optional[float] = None,
+                   decay: float = 1.0, seq_len=None, path=None, path_len=None, stream=None) -> None:
+    """kvq_attention_mass: mass[b, h, t] = decay * mass_in[b, h, t] + the
+    attention weight that the tokens' query heads of h give position t.
+    q [B, n_q, H_q, D] bf16 and lse [B, n_q, H_q] (or [B, H_q, D] and
+    [B, H_q]) of one attention call; mass and mass_in float32
+    [B, H_kv, T_cap] (mass_in: None for zeros, or mass itself); path int32
+    [B, max_path] and path_len int32 [B] pick the tokens (all without)."""
+    d = L.d
+    n_q = int(q.shape[1]) if q.dim() == 4 else 1
+    rows = (d.B, n_q, d.H_q) if q.dim() == 4 else (d.B, d.H_q)
+    _cache_bytes("cache", L, cache)
+    _tensor("q", q, "bfloat16", rows + (d.D,))
+    _tensor("lse", lse, "float32", rows)
+    _tensor("mass", mass, "float32", (d.B, d.H_kv, d.T_cap))
+    _tensor("mass_in", mass_in, "float32", (d.B, d.H_kv, d.T_cap))
+    _tensor("seq_len", seq_len, "int32", (d.B,))
+    max_path = 0
+    if path is not None:
+        max_path = int(path.shape[1]) if path.dim() == 2 else 0
+        _tensor("path", path, "int32", (d.B, max_path))
+        _tensor("path_len", path_len, "int32", (d.B,))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d.D)
+    st = load().kvq_attention_mass(ctypes.byref(L), _addr(cache), _addr(q), _addr(lse), n_q, _addr(seq_len), int(T),
+                                   _addr(path), max_path, _addr(path_len), float(softmax_scale), _addr(mass_in),
+                                   float(decay), _addr(mass), _stream(stream))
+    if st != 0:
+        raise KvqError(st, "kvq_attention_mass")
+
+
+def cache_evict(L: Layout, cache, mass, T: int, L_dst: Layout, cache_dst, T_dst: int, keep, n_recent: int = 0,
+                mass_dst=None, seq_len=None, new_len=None, stream=None) -> None:
+    """kvq_cache_evict: the positions of largest mass (float32
+    [B, H_kv, T_cap]) copied from cache (lengths T, or seq_len) into
+    cache_dst, whose layout L_dst has a smaller visual block; keep int32
+    [B, H_kv, T_dst] gets their source positions, mass_dst float32
+    [B, H_kv, T_cap_dst] their masses, new_len int32 [B] the new lengths."""
+    d = L.d
+    _cache_bytes("cache", L, cache)
+    _cache_bytes("cache_dst", L_dst, cache_dst)
+    _tensor("mass", mass, "float32", (d.B, d.H_kv, d.T_cap))
+    _tensor("keep", keep, "int32", (d.B, d.H_kv, int(T_dst)))
+    _tensor("mass_dst", mass_dst, "float32", (d.B, d.H_kv, L_dst.d.T_cap))
+    _tensor("seq_len", seq_len, "int32", (d.B,))
+    _tensor("new_len", new_len, "int32", (d.B,))
+    st = load().kvq_cache_evict(ctypes.byref(L), _addr(cache), _addr(mass), _addr(seq_len), int(T), ctypes.byref(L_dst),
+                                _addr(cache_dst), int(T_dst), int(n_recent), _addr(keep), _addr(mass_dst), _addr(new_len),
+                                _stream(stream))
+    if st != 0:
+        raise KvqError(st, "kvq_cache_evict")
+
+
 def workspace_status(workspace, stream=None) -> int:
     """kvq_workspace_status: the KVQ_STATUS_* bits OR-ed into the
     workspace's status word (synchronises the stream to read them)."""
@@ -377,6 +539,11 @@ kvq_sensitivity_probe = sensitivity_probe
 kvq_decode_attention_mq = decode_attention_mq
 kvq_decode_mq_workspace_bytes = decode_mq_workspace_bytes
 kvq_probe_workspace_bytes = probe_workspace_bytes
+kvq_decode_tree_workspace_bytes = decode_tree_workspace_bytes
+kvq_decode_attention_tree = decode_attention_tree
+kvq_tree_commit = tree_commit
+kvq_attention_mass = attention_mass
+kvq_cache_evict = cache_evict
 kvq_workspace_status = workspace_status
 kvq_set_wait_limits = set_wait_limits
 kvq_set_cache_preload = set_cache_preload

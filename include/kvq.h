@@ -343,6 +343,131 @@ kvq_status kvq_sensitivity_probe(const kvq_layout* L, const void* cache, const v
                                  const float* readout, int32_t n_out, double* result, void* workspace,
                                  size_t ws_bytes, void* stream);
 
+/*
+ * Trees of drafted tokens (speculative decoding).  n_q drafted tokens per
+ * sequence follow a context of cached positions; their K/V rows are separate
+ * bf16 tensors, so a rejected draft never enters the cache.
+ *
+ * kvq_decode_attention_tree -- token i of sequence b attends the context
+ * [0, len_b) of the cache and the drafted rows j whose bit j is set in its
+ * mask (nothing is implied: a token that sees itself has its own bit set).
+ *   q_bf16    device bf16 [B][n_q][H_q][D], 16-byte aligned
+ *   k_draft_bf16, v_draft_bf16   device bf16, element (b, h, j, d) at index
+ *             b*stride_b + h*stride_h + j*stride_t + d (strides >= 0,
+ *             multiples of 8 elements; 16-byte aligned; outside the cache)
+ *   n_q       1 <= n_q <= KVQ_MAX_QUERY_TOKENS
+ *   tree_mask device uint64, entry (b, i) at index b*mask_stride_b + i,
+ *             8-byte aligned; mask_stride_b = 0 for one tree of the whole
+ *             batch, else >= n_q; bits n_q and above are ignored
+ *   seq_len   device int32 [B] of context lengths, or NULL: every len_b is
+ *             T_ctx.  An entry outside [0, T_ctx] marks an inactive sequence
+ *             (outputs zero, lse -inf)
+ *   T_ctx     0 <= T_ctx <= T_cap: the (largest) context length
+ *   out_bf16  device bf16 [B][n_q][H_q][D];  lse  fp32 [B][n_q][H_q] or NULL
+ *   workspace at least kvq_decode_tree_workspace_bytes(L, n_q) bytes,
+ *             256-byte aligned, first 4 bytes the status word; other contents
+ *             on entry are ignored; overlapping calls must not share it
+ * A token that attends nothing (empty context, empty mask) gets output zero
+ * and lse -inf.  Drafted rows that no token of their sequence attends may
+ * hold anything; all other values are finite, |x| <= 65504.
+ * kvq_decode_tree_workspace_bytes returns 0 for an invalid layout or n_q.
+ */
+size_t kvq_decode_tree_workspace_bytes(const kvq_layout* L, int32_t n_q);
+kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void* cache, const void* q_bf16,
+                                     const void* k_draft_bf16, const void* v_draft_bf16,
+                                     int64_t stride_b, int64_t stride_h, int64_t stride_t,
+                                     int32_t n_q, const uint64_t* tree_mask, int64_t mask_stride_b,
+                                     const int32_t* seq_len, int32_t T_ctx, float softmax_scale,
+                                     void* out_bf16, float* lse, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/*
+ * kvq_tree_commit -- store the accepted path of the tree: position len_b + k
+ * of every KV head takes drafted row path[b][k], for k < path_len[b]
+ * (verbatim bf16: the current tokens are never quantised).
+ *   k_draft_bf16, v_draft_bf16, strides, n_q   as above
+ *   path      device int32 [B][max_path], entries in [0, n_q); any order, the
+ *             same draft may appear twice; entries past path_len[b] are unread
+ *   max_path  1 <= max_path <= KVQ_MAX_QUERY_TOKENS
+ *   path_len  device int32 [B], entries in [0, max_path]
+ *   seq_len, T_ctx   as above (NULL: every len_b is T_ctx)
+ *   new_len   device int32 [B] or NULL: len_b + path_len[b]; it must not
+ *             share memory with seq_len, path_len or path
+ * A sequence whose length, path length or a path entry is outside its range,
+ * or whose new positions would pass T_cap or touch the visual range, is
+ * inactive: nothing is stored for it and its new_len is -1 (which every call
+ * of this library that reads lengths takes as inactive).
+ */
+kvq_status kvq_tree_commit(const kvq_layout* L, void* cache, const void* k_draft_bf16,
+                           const void* v_draft_bf16, int64_t stride_b, int64_t stride_h,
+                           int64_t stride_t, int32_t n_q, const int32_t* path, int32_t max_path,
+                           const int32_t* path_len, const int32_t* seq_len, int32_t T_ctx,
+                           int32_t* new_len, void* stream);
+
+/*
+ * kvq_attention_mass -- the attention weight each cache position has
+ * received, per KV head (what kvq_cache_evict goes by):
+ *   mass[b][h][t] = decay * mass_in[b][h][t] + sum over the tokens k taken
+ *   from sequence b and the query heads hq of h of
+ *   exp(softmax_scale * q[b][tok_k][hq] . khat[b][h][t] - lse[b][tok_k][hq])
+ * for t < len_b; token k of n reaches the positions t < len_b - n + 1 + k
+ * (causal at the end, as in kvq_decode_attention_mq and along a committed
+ * path).  Only K is read.
+ *   q_bf16    device bf16 [B][n_q][H_q][D], 16-byte aligned; n_q as above
+ *   lse       device fp32 [B][n_q][H_q], as the attention call of the same
+ *             tokens returned it; -inf or +inf: that row adds nothing
+ *   seq_len   device int32 [B] of lengths, the tokens' own positions
+ *             included, or NULL: every len_b is T
+ *   T         1 <= T <= T_cap: the (largest) length
+ *   path, max_path, path_len   the tokens taken, as in kvq_tree_commit (an
+ *             entry outside [0, n_q) adds nothing), or NULL, 0, NULL: all
+ *             n_q tokens in order (then n_q <= T without seq_len)
+ *   mass_in, mass   device fp32 [B][H_kv][T_cap]; mass_in may be mass itself,
+ *             or NULL (zeros); otherwise they must not overlap
+ *   decay     finite
+ * Positions t >= len_b are left as they were.  A sequence whose length is
+ * outside [1, T], or whose token count is outside [0, min(len_b, n_q or
+ * max_path)], is inactive: its rows are left as they were.
+ */
+kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache, const void* q_bf16,
+                              const float* lse, int32_t n_q, const int32_t* seq_len, int32_t T,
+                              const int32_t* path, int32_t max_path, const int32_t* path_len,
+                              float softmax_scale, const float* mass_in, float decay, float* mass,
+                              void* stream);
+
+/*
+ * kvq_cache_evict -- copy the positions of largest attention mass into the
+ * cache of a smaller layout.  Per sequence and KV head: the text prefix
+ * [0, vis_start) is kept whole; of the visual block the vis_end - vis_start
+ * positions of L_dst with the largest mass; of the text positions
+ * [vis_end, len_b) the last n_recent and, before them, those of largest mass,
+ * T_dst - vis_end_dst in all (every one when there are fewer).  NaN counts as
+ * less than every number; of equal masses the lowest position is kept.  Kept
+ * positions keep their order, and rows are copied as they are stored (packed
+ * rows bit for bit, never requantised).
+ *   mass      device fp32 [B][H_kv][T_cap]
+ *   seq_len, T   lengths as in kvq_attention_mass; T >= vis_end
+ *   L_dst, cache_dst   a layout that differs from L only in vis_end (a visual
+ *             block of at most L's size) and T_cap, and its buffer, which
+ *             must not overlap cache
+ *   T_dst     max(1, vis_end_dst) <= T_dst <= T_cap_dst
+ *   n_recent  0 <= n_recent <= T_dst - vis_end_dst
+ *   keep      device int32 [B][H_kv][T_dst]: the source position of each kept
+ *             one, -1 behind the last (written)
+ *   mass_dst  device fp32 [B][H_kv][T_cap_dst] or NULL: the kept masses, zeros
+ *             behind them; must not overlap mass
+ *   new_len   device int32 [B] or NULL: the new lengths; must not share memory
+ *             with seq_len
+ * Rows of cache_dst behind a sequence's new length are left as they were.  A
+ * sequence whose length is outside [vis_end, T] is inactive: its keep entries
+ * and new_len become -1 and its rows of cache_dst and mass_dst are left as
+ * they were.
+ */
+kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* mass,
+                           const int32_t* seq_len, int32_t T, const kvq_layout* L_dst,
+                           void* cache_dst, int32_t T_dst, int32_t n_recent, int32_t* keep,
+                           float* mass_dst, int32_t* new_len, void* stream);
+
 /* Size in bytes of the device scratch array used by
  * kvq_decode_attention_static_ws (16 MiB).  A layout fits when
  * L->workspace_bytes <= KVQ_STATIC_WS_BYTES, which holds for up to 3007
