@@ -565,6 +565,8 @@ extern "C" kvq_status kvq_decode_step_ragged(const kvq_layout* L, void* cache, c
   return launch_step(L, p, stream);
 }
 
+uint32_t kvq_tile_polls() { return tl_tile_polls ? tl_tile_polls : kvq::kDefaultTilePolls; }
+
 extern "C" void kvq_set_wait_limits(uint32_t tile_polls, uint32_t peer_polls) {
   tl_tile_polls = tile_polls;
   tl_peer_polls = peer_polls;

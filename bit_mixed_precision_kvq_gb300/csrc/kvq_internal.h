@@ -333,6 +333,8 @@ kvq::Plan kvq_make_plan(const kvq_layout* L, int32_t T, int32_t n_chunks_target,
 // the plan's per-unit chunk fields.
 void kvq_plan_cuts(kvq::Plan* P, kvq::Cut* cuts);
 int kvq_device_sm_count(int* n_sm);
+// The calling host thread's limit of a wait (kvq_set_wait_limits).
+uint32_t kvq_tile_polls();
 // Record a failed CUDA call for kvq_last_cuda_error(); returns KVQ_ERR_CUDA.
 kvq_status kvq_cuda_fail(int err);
 // Launch `fn(*p)` with programmatic stream serialisation allowed, so that its

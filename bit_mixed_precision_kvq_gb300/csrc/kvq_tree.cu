@@ -6,76 +6,151 @@
 //   s_t = scale q . k_hat_t   for t < len,
 //   s_j = scale q . k_draft_j for the drafts j with bit j of mask[b, i] set,
 //   out = sum softmax(s) v,  lse = ln sum e^s   (no position: out 0, lse -inf).
-#include "kvq_simple.cuh"
+#include "kvq_tree.cuh"
 
+#include <algorithm>
 #include <cmath>
+#include <mutex>
 
 namespace kvq {
+namespace tree {
 namespace {
 
-struct TreeArgs {
-  Geom c;
-  const uint16_t *q, *kd, *vd;
-  int64_t sb, sh, st;  // strides of the drafts, in elements
-  const uint64_t* mask;
-  int64_t mask_sb;
-  const int32_t* seq_len;
-  int32_t T, n_q;
-  float scale_log2;
-  uint16_t* out;
-  float* lse;
-};
-
-// The simple form: a CTA per output row, a warp per position at a time.
-constexpr int kWarps = 4;
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const __grid_constant__ TreeArgs a) {
-  __shared__ float sm_o[kWarps][kD], sm_ml[kWarps][2];
-  const Geom& p = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The outputs of units that are split over several CTAs: a CTA per output
+// row, thread = d.  Partials are o (relative to the reference m), m and l.
+__global__ void __launch_bounds__(kD) combine_kernel(const __grid_constant__ Args a) {
+  __shared__ float wgt[kMaxSplitCtas];
+  __shared__ float red[4][2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;  // (b * n_q + i) * Hq + hq
-  const int hq = static_cast<int>(row % p.Hq), h = hq / p.g;
-  const int bi = static_cast<int>(row / p.Hq), b = bi / a.n_q, i = bi - b * a.n_q;
+  const int hq = static_cast<int>(row % a.c.Hq), h = hq / a.c.g;
+  const int bi = static_cast<int>(row / a.c.Hq), b = bi / a.n_q, i = bi - b * a.n_q;
+  const int cg = i * a.c.g + (hq - h * a.c.g), cb = cg / a.nb, c = cg - cb * a.nb;
+  int S;
+  const int cta = first_cta(a, b, h, cb, &S);
   pdl_wait();
-  const int len = a.seq_len ? a.seq_len[b] : a.T;
-  const bool live = len >= 0 && len <= a.T;
-  const HeadRows r = head_rows(p, b, h);
-  const uint64_t mask = a.mask[b * a.mask_sb + i];
-  const float4 q = row4(reinterpret_cast<const uint8_t*>(a.q + row * kD), nullptr, 16, p.G, true, 4 * lane);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int t = warp; live && t < len + a.n_q; t += kWarps) {
-    const int j = t - len;
-    if (j >= 0 && !((mask >> j) & 1)) continue;
-    const int64_t dr = b * a.sb + h * a.sh + j * a.st;
-    const float4 k = j < 0 ? k_row4(p, r, t, 4 * lane)
-                           : row4(reinterpret_cast<const uint8_t*>(a.kd + dr), nullptr, 16, p.G, true, 4 * lane);
-    const float4 v = j < 0 ? v_row4(p, r, t, 4 * lane)
-                           : row4(reinterpret_cast<const uint8_t*>(a.vd + dr), nullptr, 16, p.G, false, 4 * lane);
-    const float s = a.scale_log2 * warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w);
-    const float mn = fmaxf(m, s), c = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * c + w;
-    o = make_float4(o.x * c + w * v.x, o.y * c + w * v.y, o.z * c + w * v.z, o.w * c + w * v.w);
+  pdl_launch_dependents();
+  if (S == 1) return;  // written by its CTA
+  const int64_t pitch = static_cast<int64_t>(a.N) * (kD + 2);
+  const float* slot = a.ws + cta * pitch;
+  const float* ml = slot + a.N * kD + 2 * c;
+  float M = -INFINITY;
+  bool bad = false;
+  for (int s = tid; s < S; s += kD) {
+    const float m = __ldcg(ml + s * pitch);
+    wgt[s] = m;
+    bad |= m != m;
+    M = fmaxf(M, m);
   }
-  *reinterpret_cast<float4*>(&sm_o[warp][4 * lane]) = o;
-  if (lane == 0) {
-    sm_ml[warp][0] = m;
-    sm_ml[warp][1] = l;
-  }
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) red[warp][0] = bad ? __int_as_float(0x7fffffff) : M;
   __syncthreads();
-  const int d = threadIdx.x;
-  float M = -INFINITY, L = 0.f, O = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_ml[w][0]);
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = sm_ml[w][0] == -INFINITY ? 0.f : exp2f(sm_ml[w][0] - M);
-    L += f * sm_ml[w][1];
-    O += f * sm_o[w][d];
+  M = -INFINITY;
+  bad = false;
+  for (int k = 0; k < 4; ++k) {
+    bad |= red[k][0] != red[k][0];
+    M = fmaxf(M, red[k][0]);
   }
-  a.out[row * kD + d] = f32_to_bf16_bits(L > 0.f ? O / L : 0.f);
-  if (d == 0 && a.lse) a.lse[row] = 0.69314718055994531f * (M + log2f(L));
+  float L = 0.f;
+  for (int s = tid; s < S; s += kD) {
+    const float m = wgt[s], f = m == -INFINITY || m != m ? 0.f : exp2f(m - M);
+    wgt[s] = f;
+    L = fmaf(f, __ldcg(ml + s * pitch + 1), L);
+  }
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) red[warp][1] = L;
+  __syncthreads();
+  L = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+  const float* o = slot + c * kD + tid;
+  float O = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < S; ++s) O = fmaf(wgt[s], wgt[s] > 0.f ? __ldcg(o + s * pitch) : 0.f, O);
+  const float nan = __int_as_float(0x7fffffff);
+  a.out[row * kD + tid] = f32_to_bf16_bits(bad ? nan : (L > 0.f ? O / L : 0.f));
+  if (tid == 0 && a.lse) a.lse[row] = bad ? nan : 0.69314718055994531f * (M + log2f(L));
+}
+
+// Columns of the widest unit, rounded to the MMA's granularity.
+struct Columns {
+  int nblk, nb, N;
+};
+Columns columns_of(const kvq_layout* L, int32_t n_q) {
+  const int cols = L->g * n_q;
+  Columns c;
+  c.nblk = (cols + kMaxCols - 1) / kMaxCols;
+  c.nb = (cols + c.nblk - 1) / c.nblk;
+  c.N = (c.nb + 15) / 16 * 16;
+  return c;
+}
+
+constexpr int64_t kWsHead = 256;
+int64_t ws_bytes_of(const kvq_layout* L, int32_t n_q) {
+  return kWsHead + static_cast<int64_t>(kMaxSplitCtas) * columns_of(L, n_q).N * (kD + 2) * 4;
+}
+
+const void* kernel_for(int kb, int vb) {
+  switch (kb) {
+    case 2: return tree_kernel_k2(vb);
+    case 4: return tree_kernel_k4(vb);
+    case 8: return tree_kernel_k8(vb);
+    case 16: return tree_kernel_k16(vb);
+  }
+  return nullptr;
+}
+
+// Once per kernel and device: more than 48 KB of shared memory.
+kvq_status prepare(const void* fn) {
+  static std::mutex mu;
+  static const void* done[64][16];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return kvq_cuda_fail(e);
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64)
+    for (const void* f : done[dev])
+      if (f == fn) return KVQ_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+  if (e != cudaSuccess) return kvq_cuda_fail(e);
+  if (dev < 64)
+    for (const void*& f : done[dev])
+      if (!f) {
+        f = fn;
+        break;
+      }
+  return KVQ_OK;
+}
+
+// How many CTAs share a unit of each class: one wave of CTAs on the GPU's
+// SMs (a CTA fills an SM), more of them for the classes whose tiles cost
+// more.  With more units than SMs every unit has one CTA, the dearest first.
+constexpr double kTileCost[3] = {2.0, 1.5, 1.0};  // protected, K-only, packed
+void plan_splits(const kvq_layout* L, int tiles, int n_sm, Args* a) {
+  const int n[3] = {L->n_prot, L->n_konly, L->n_packed};
+  const int cap = std::min(n_sm, kMaxSplitCtas);
+  int used = 0;
+  for (int k = 0, h = 0; k < 3; ++k) {
+    a->U[k] = L->d.B * n[k] * a->nblk;
+    a->S[k] = 1;
+    a->head0[k] = h;
+    h += n[k];
+    used += a->U[k];
+  }
+  for (;;) {  // the class whose CTAs take longest gets one more each, while they fit
+    int worst = -1;
+    double most = 0.0;
+    for (int k = 0; k < 3; ++k) {
+      const double t = a->U[k] ? kTileCost[k] * ((tiles + a->S[k] - 1) / a->S[k]) : 0.0;
+      if (t > most) most = t, worst = k;
+    }
+    if (worst < 0 || a->S[worst] >= tiles || used + a->U[worst] > cap) return;
+    ++a->S[worst];
+    used += a->U[worst];
+  }
 }
 
 }  // namespace
+}  // namespace tree
 }  // namespace kvq
 
 // Checks of the drafted rows shared by the tree's entry points: pointers,
@@ -98,7 +173,7 @@ kvq_status kvq_check_drafts(const kvq_layout* L, const void* cache, const void* 
 
 extern "C" size_t kvq_decode_tree_workspace_bytes(const kvq_layout* L, int32_t n_q) {
   if (kvq_check_layout(L) != KVQ_OK || n_q < 1 || n_q > KVQ_MAX_QUERY_TOKENS) return 0;
-  return 256;
+  return static_cast<size_t>(kvq::tree::ws_bytes_of(L, n_q));
 }
 
 extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void* cache, const void* q_bf16,
@@ -119,10 +194,18 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
     return KVQ_ERR_INVALID_ARG;
   if (mask_stride_b != 0 && mask_stride_b < n_q) return KVQ_ERR_INVALID_ARG;
   if (T_ctx < 0 || T_ctx > L->d.T_cap || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
-  if (ws_bytes < kvq_decode_tree_workspace_bytes(L, n_q)) return KVQ_ERR_CAPACITY;
+  if (ws_bytes < static_cast<size_t>(kvq::tree::ws_bytes_of(L, n_q))) return KVQ_ERR_CAPACITY;
   const int64_t rows = static_cast<int64_t>(L->d.B) * n_q * L->d.H_q;
-  if (rows > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  kvq::TreeArgs a;
+  const kvq::tree::Columns cols = kvq::tree::columns_of(L, n_q);
+  const int64_t units = static_cast<int64_t>(L->d.B) * L->d.H_kv * cols.nblk;
+  if (rows > 0x7fffffffLL || units > 0x7fffffffLL || static_cast<int64_t>(L->g) * n_q > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  const void* fn = kvq::tree::kernel_for(L->d.k_bits, L->d.v_bits);
+  if (!fn) return KVQ_ERR_UNSUPPORTED;
+  int n_sm = 0;
+  if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
+  st = kvq::tree::prepare(fn);
+  if (st != KVQ_OK) return st;
+  kvq::tree::Args a;
   kvq::fill_geom(L, cache, &a.c);
   a.q = static_cast<const uint16_t*>(q_bf16);
   a.kd = static_cast<const uint16_t*>(k_draft_bf16);
@@ -138,6 +221,20 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out_bf16);
   a.lse = lse;
-  return kvq::launch_dependent(reinterpret_cast<const void*>(&kvq::tree_kernel), dim3(static_cast<unsigned>(rows)),
-                               kvq::kWarps * 32, 0, stream, &a);
+  a.status = static_cast<uint32_t*>(workspace);
+  a.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kvq::tree::kWsHead);
+  a.polls = kvq_tile_polls();
+  a.nblk = cols.nblk;
+  a.nb = cols.nb;
+  a.N = cols.N;
+  int h = 0;
+  for (int k = 0; k < L->n_prot; ++k) a.head[h++] = L->prot_head[k];
+  for (int k = 0; k < L->n_konly; ++k) a.head[h++] = L->konly_head[k];
+  for (int k = 0; k < L->n_packed; ++k) a.head[h++] = L->packed_head[k];
+  kvq::tree::plan_splits(L, (T_ctx + n_q + kvq::tree::kTile - 1) / kvq::tree::kTile, n_sm, &a);
+  const int grid = a.U[0] * a.S[0] + a.U[1] * a.S[1] + a.U[2] * a.S[2];
+  st = kvq::launch_dependent(fn, dim3(grid), kvq::tree::kThreads, sizeof(kvq::tree::Smem), stream, &a);
+  if (st != KVQ_OK || (a.S[0] == 1 && a.S[1] == 1 && a.S[2] == 1)) return st;
+  return kvq::launch_dependent(reinterpret_cast<const void*>(&kvq::tree::combine_kernel), dim3(static_cast<unsigned>(rows)),
+                               kvq::kD, 0, stream, &a);
 }

@@ -1,0 +1,814 @@
+// kvq_tree.cuh -- attention of a tree of drafted tokens on the fifth-
+// generation tensor cores (tcgen05), for kvq_decode_attention_tree.
+//
+// A unit is one (sequence b, KV head h, block of up to 64 columns); a column
+// is a (token i, query head of h) pair.  The unit's positions -- the context
+// [0, len), then the drafts -- are taken in tiles of 128, one position per
+// TMEM lane, so that a tile's MMAs cost in proportion to the columns there
+// are:
+//   S^T[t][c]  = k_t . q_c           M = 128 positions, N = columns, K = d
+//   O^T[d][c] += sum_t v_t[d] P[t][c]  M = 128 d, N = columns, K = positions
+// K rows are unpacked into TMEM (A operand: the thread that unpacks a row owns
+// its lane), V rows into shared memory as fp16 (A operand, d contiguous), P
+// goes to shared memory (B operand), q stays there (B operand).  Shared-memory
+// bandwidth (128 B a clock, for the unpacking warps and the tensor cores
+// together) is what bounds a tile, and K and S never pass through it.
+//
+// Exactness of the scores (lse is an fp32 output): a packed K value
+// c s + z is held as c' s + z' with c' = c - 2^(b-1) (c - 1 for 2 bits) and
+// z' = z + (c - c') s.  c' s is exact in fp16 for 2 bits and an exact
+// (high, low) fp16 pair for 4 and 8 bits, two MMAs; z' goes in as one more
+// K step, an fp16 (high, low) pair against the (high, low) pair of the query's
+// group sums (22 bits).  bf16 rows are exact in fp16.  K operands carry a
+// factor 1/2 and queries 2^-7, so that values up to 65504 do not overflow;
+// both powers of two are undone by the softmax scale.  V is dequantised to
+// fp16 (one rounding, 2^-11 of the value, below the output's 2^-8), P is
+// fp16 (2^-11), O and the softmax sums are fp32.
+//
+// Softmax: a thread owns a position (a TMEM lane) and all columns, so the
+// maximum of a column would be a reduction over 128 lanes.  Instead every
+// column has a reference m (log2 units, shared memory) that only moves, for
+// all lanes at once, when a score of a tile exceeds it by more than 2^12
+// (P <= 4096 in fp16); the column sums stay in the threads until the end.
+//
+// CTA = 12 warps: 0-3 softmax (TMEM lanes 32 w ..), 4-11 unpack (warp w: lanes
+// 32 (w mod 4) .., half (w - 4) / 4 of the row).  An unpack thread issues the
+// QK of a tile, a softmax thread its PV.  TMEM: two K buffers (64 columns
+// high, 64 low, 8 zero points), two S buffers of 64, O of 64.
+#pragma once
+
+#include "kvq_geom.cuh"
+#include "kvq_umma.cuh"
+
+namespace kvq {
+namespace tree {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;              // positions per tile (TMEM lanes)
+constexpr int kMaxCols = 64;            // columns per unit (at most)
+constexpr int kMaxSplitCtas = 160;      // CTAs of a call whose units are split (workspace slots)
+constexpr float kMaxGrowth = 12.f;      // log2 of the largest P
+constexpr float kUnset = -1e30f;        // reference of a column that has attended nothing
+constexpr float kOperandScale = 256.f;  // undoes K / 2 and q / 2^7
+
+constexpr uint32_t kTmK = 0, kTmKStride = 136, kTmLo = 64, kTmZ = 128;
+constexpr uint32_t kTmS = 272, kTmSStride = 64;
+constexpr uint32_t kTmO = 400;
+constexpr uint32_t kTmCols = 512;
+
+struct Args {
+  Geom c;
+  const uint16_t *q, *kd, *vd;
+  int64_t sb, sh, st;  // strides of the drafts, in elements
+  const uint64_t* mask;
+  int64_t mask_sb;
+  const int32_t* seq_len;
+  int32_t T, n_q;
+  float scale_log2;  // softmax_scale * log2(e)
+  uint16_t* out;
+  float* lse;
+  uint32_t* status;
+  float* ws;          // partials: a slot per CTA, [cols][D] o, then [cols][2] (m, l)
+  uint32_t polls;     // limit of a wait
+  // units: class k (0 protected, 1 K-only, 2 packed heads) has U[k] of them,
+  // each split over S[k] CTAs; heads of the classes in order in head[]
+  int32_t U[3], S[3], head0[3];
+  int32_t nblk, nb, N;  // column blocks per KV head, columns per block, columns of the MMAs (16, 32, 48, 64)
+  uint8_t head[KVQ_MAX_HEADS];
+};
+
+struct Smem {
+  alignas(1024) uint8_t vt[2][kTile * 256];   // V: position (row of K = t), d contiguous
+  alignas(1024) uint8_t pt[2][kMaxCols * 256];  // P: position, columns contiguous
+  alignas(1024) uint8_t qt[kMaxCols * 256];   // q: column, d contiguous (permuted)
+  alignas(128) uint8_t qz[kMaxCols * 32];     // group sums of q: column, 16 K indexes
+  uint64_t colmask[kMaxCols];
+  float m[kMaxCols], fac[kMaxCols];
+  uint32_t top[kMaxCols];
+  float lsum[4][kMaxCols];
+  float qs[kMaxCols][4];
+  uint64_t k_free[2], v_full[2], s_full[2], s_free[2], pv_done[2], q_ready;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// The unit and split of a CTA.
+struct Work {
+  int cls, b, h, cb, s, S;
+};
+__device__ __forceinline__ Work work_of(const Args& a, int cta) {
+  Work w;
+  int i = cta, cls = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (cls == k && i >= a.U[k] * a.S[k]) {
+      i -= a.U[k] * a.S[k];
+      cls = k + 1;
+    }
+  w.cls = cls;
+  w.S = cls == 0 ? a.S[0] : (cls == 1 ? a.S[1] : a.S[2]);
+  const int v = i / w.S;
+  w.s = i - v * w.S;
+  const int nh = (cls == 0 ? a.c.n_prot : (cls == 1 ? a.c.n_konly : a.c.n_packed)) * a.nblk;
+  w.b = v / nh;
+  const int r = v - w.b * nh;
+  const int slot = r / a.nblk;
+  w.cb = r - slot * a.nblk;
+  w.h = a.head[(cls == 0 ? a.head0[0] : (cls == 1 ? a.head0[1] : a.head0[2])) + slot];
+  return w;
+}
+// First CTA of the unit (b, h, cb).
+__device__ __forceinline__ int first_cta(const Args& a, int b, int h, int cb, int* S) {
+  const int mode = a.c.mode[h], cls = mode == 1 ? 0 : (mode == 2 ? 1 : 2);
+  const int nh = cls == 0 ? a.c.n_prot : (cls == 1 ? a.c.n_konly : a.c.n_packed);
+  const int base = (cls > 0 ? a.U[0] * a.S[0] : 0) + (cls > 1 ? a.U[1] * a.S[1] : 0);
+  *S = cls == 0 ? a.S[0] : (cls == 1 ? a.S[1] : a.S[2]);
+  return base + ((b * nh + a.c.slot[h]) * a.nblk + cb) * *S;
+}
+// Context length of sequence b, -1 for an inactive one.
+__device__ __forceinline__ int context_len(const Args& a, int b) {
+  const int len = a.seq_len ? a.seq_len[b] : a.T;
+  return len >= 0 && len <= a.T ? len : -1;
+}
+
+// A wait that gives up marks the CTA (its outputs become NaN) and the status
+// word; every later wait of the CTA then polls once.
+__device__ __forceinline__ void wait_for(const Args& a, Smem& sm, uint64_t* bar, uint32_t parity) {
+  if (mbar_wait(bar, parity, a.polls)) return;
+  if (*static_cast<volatile int*>(&sm.abort)) return;
+  sm.abort = 1;
+  atomicOr(a.status, KVQ_STATUS_TILE_WAIT);
+}
+
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, "
+      "q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0;
+}
+
+// ---- unpacking -----------------------------------------------------------------
+// Half hf of a K row: lane slices t = 2 hf, 2 hf + 1 of the storage order
+// (kvq.h), 8 b bytes; output pair (t & 1) * 16 + 4 P + i = elements (d0 + i,
+// d0 + i + 4), d0 = 32 P + 8 t.  Half hf of a V row: elements 64 hf .. + 63 in
+// order, chunk kk = elements 64 hf + 8 kk .. + 7 in registers 4 kk .. + 3.
+// A masked code with the exponent of 1024 over it is the fp16 1024 + c 2^p
+// for a code at bit p; one fma takes it to c - off.
+
+__device__ __forceinline__ uint32_t h2(float x) {  // both halves
+  return pack_f16x2(x, x);
+}
+
+template <int P2>  // code at bit P2 of each half of x -> code - off
+__device__ __forceinline__ uint32_t code_at(uint32_t x, uint32_t mask, float off) {
+  const uint32_t v = and_or(x, mask << P2, 0x64006400u);
+  if constexpr (P2 == 0) return hsub2_u(v, h2(1024.f + off));
+  return hfma2_u(v, h2(1.f / (1 << P2)), h2(-(1024.f / (1 << P2) + off)));
+}
+
+template <int KB>
+__device__ __forceinline__ constexpr float k_center() {
+  return KB == 2 ? 1.f : (KB == 4 ? 8.f : 128.f);
+}
+
+// c' of the 32 pairs of a half K row.
+template <int KB>
+__device__ __forceinline__ void k_codes(const uint4 (&r)[8], uint32_t (&c)[32]) {
+  constexpr float off = k_center<KB>();
+  if constexpr (KB == 2) {
+    const uint32_t x[4] = {r[0].x, r[0].y, r[0].z, r[0].w};  // word 2 (t & 1) + i / 2
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = x[2 * t + h], y = w >> 6;
+        uint32_t* o = c + 16 * t + 2 * h;  // i = 2 h, 2 h + 1
+        o[0] = code_at<8>(w, 0x00030003u, off);
+        o[1] = code_at<8>(y, 0x00030003u, off);
+        o[4] = code_at<6>(w, 0x00030003u, off);
+        o[5] = code_at<6>(y, 0x00030003u, off);
+        o[8] = code_at<4>(w, 0x00030003u, off);
+        o[9] = code_at<4>(y, 0x00030003u, off);
+        o[12] = code_at<0>(w, 0x00030003u, off);
+        o[13] = code_at<2>(w, 0x00030003u, off);
+      }
+  } else if constexpr (KB == 4) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t x[4] = {r[t].x, r[t].y, r[t].z, r[t].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = x[i], y = w >> 8;
+        uint32_t* o = c + 16 * t + i;
+        o[0] = code_at<0>(w, 0x000F000Fu, off);
+        o[4] = code_at<4>(w, 0x000F000Fu, off);
+        o[8] = code_at<0>(y, 0x000F000Fu, off);
+        o[12] = code_at<4>(y, 0x000F000Fu, off);
+      }
+    }
+  } else if constexpr (KB == 8) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t x[8] = {r[2 * t].x,     r[2 * t].y,     r[2 * t].z,     r[2 * t].w,
+                             r[2 * t + 1].x, r[2 * t + 1].y, r[2 * t + 1].z, r[2 * t + 1].w};
+#pragma unroll
+      for (int P = 0; P < 4; ++P)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = x[2 * P + (i >> 1)];
+          c[16 * t + 4 * P + i] = code_at<0>((i & 1) ? w >> 8 : w, 0x00FF00FFu, off);
+        }
+    }
+  }
+}
+
+// Scale (fp16 bits) and zero of group g of a scale/zero row [z.., s..] of n groups.
+__device__ __forceinline__ uint32_t half_of(const uint4& r, int k) {
+  const uint32_t w = k < 4 ? (k < 2 ? r.x : r.y) : (k < 6 ? r.z : r.w);
+  return (k & 1) ? w >> 16 : w & 0xffffu;
+}
+__device__ __forceinline__ float f16_bits(uint32_t h) { return __half2float(__ushort_as_half(static_cast<uint16_t>(h))); }
+
+// A packed half V row, dequantised in order.
+template <int VB>
+__device__ __forceinline__ void v_values(const uint4 (&r)[8], const uint4& sz, int hf, int G, uint32_t (&o)[32]) {
+  const int ng = kD / G;
+  uint32_t s2[8], z2[8];  // of chunk kk
+#pragma unroll
+  for (int kk = 0; kk < 8; kk += 4) {  // a group is at least 4 chunks
+    const int g = (64 * hf + 8 * kk) / G;
+    const uint32_t s = half_of(sz, ng + g) * 0x10001u, z = half_of(sz, g) * 0x10001u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s2[kk + j] = s, z2[kk + j] = z;
+  }
+  auto put = [&](int kk, int j, uint32_t c) { o[4 * kk + j] = hfma2_u(c, s2[kk], z2[kk]); };
+  if constexpr (VB == 2) {
+    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = prmt(w[2 * j], w[2 * j + 1], hf ? 0x7632u : 0x5410u), y = x >> 6;
+      put(0, j, code_at<0>(x, 0x00030003u, 0.f));
+      put(1, j, code_at<2>(x, 0x00030003u, 0.f));
+      put(2, j, code_at<4>(x, 0x00030003u, 0.f));
+      put(3, j, code_at<6>(x, 0x00030003u, 0.f));
+      put(4, j, code_at<8>(x, 0x00030003u, 0.f));
+      put(5, j, code_at<4>(y, 0x00030003u, 0.f));
+      put(6, j, code_at<6>(y, 0x00030003u, 0.f));
+      put(7, j, code_at<8>(y, 0x00030003u, 0.f));
+    }
+  } else if constexpr (VB == 4) {
+    // word 2 n + hf
+    const uint32_t w[8] = {hf ? r[0].y : r[0].x, hf ? r[0].w : r[0].z, hf ? r[1].y : r[1].x, hf ? r[1].w : r[1].z,
+                           hf ? r[2].y : r[2].x, hf ? r[2].w : r[2].z, hf ? r[3].y : r[3].x, hf ? r[3].w : r[3].z};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = prmt(w[2 * j], w[2 * j + 1], e ? 0x7632u : 0x5410u), y = x >> 8;
+        put(4 * e, j, code_at<0>(x, 0x000F000Fu, 0.f));
+        put(4 * e + 1, j, code_at<4>(x, 0x000F000Fu, 0.f));
+        put(4 * e + 2, j, code_at<0>(y, 0x000F000Fu, 0.f));
+        put(4 * e + 3, j, code_at<4>(y, 0x000F000Fu, 0.f));
+      }
+  } else if constexpr (VB == 8) {
+    // words 4 n + 2 hf, + 1: r[n / 2] holds the pairs of n even and odd
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t wa[2] = {r[j].x, r[j].y}, wb[2] = {r[j].z, r[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // half-words: chunks 2 e, 2 e + 1
+        const uint32_t x = prmt(wa[e >> 1], wb[e >> 1], (e & 1) ? 0x7632u : 0x5410u);
+        put(2 * e, j, code_at<0>(x, 0x00FF00FFu, 0.f));
+        put(2 * e + 1, j, code_at<0>(x >> 8, 0x00FF00FFu, 0.f));
+      }
+    }
+  }
+}
+
+// Where a row's values come from.
+enum RowKind { kRowNone = 0, kRowPacked = 1, kRowBf16 = 2 };
+struct Row {
+  int kind;
+  const uint8_t *p, *sz;
+};
+
+struct Source {
+  HeadRows r;
+  const uint8_t *kd, *vd;  // drafts of (b, h)
+  int64_t dstep;           // bytes from draft to draft
+  uint64_t any;            // drafts that some token attends
+  int len, end;            // context length; + n_q
+};
+
+template <bool kKey>
+__device__ __forceinline__ Row row_of(const Args& a, const Source& s, int t) {
+  Row w;
+  w.kind = kRowNone;
+  w.p = w.sz = nullptr;
+  if (t < s.len) {
+    const Geom& c = a.c;
+    if (t >= c.vs && t < c.ve) {
+      const int64_t i = t - c.vs;
+      const bool packed = kKey ? s.r.k_packed : s.r.v_packed;
+      w.kind = packed ? kRowPacked : kRowBf16;
+      const int step = packed ? (kKey ? c.krow : c.vrow) : kRowBytes;
+      w.p = (kKey ? s.r.vis_k : s.r.vis_v) + i * step;
+      if (packed) w.sz = kKey ? s.r.vis_ksz + i * c.kszrow : s.r.vis_vsz + i * c.vszrow;
+    } else {
+      w.kind = kRowBf16;
+      w.p = (kKey ? s.r.text_k : s.r.text_v) + static_cast<int64_t>(t < c.vs ? t : t - c.Tv) * kRowBytes;
+    }
+  } else if (t < s.end && ((s.any >> (t - s.len)) & 1)) {
+    w.kind = kRowBf16;
+    w.p = (kKey ? s.kd : s.vd) + (t - s.len) * s.dstep;
+  }
+  return w;
+}
+
+// The raw bytes of half hf of a row (and its scale/zero row).
+template <int KB>
+__device__ __forceinline__ void load_k(const Row& w, int hf, int G, uint4 (&r)[8], uint4& sz) {
+  if (KB < 16 && w.kind == kRowPacked) {
+    const uint4* p = reinterpret_cast<const uint4*>(w.p + hf * 8 * KB);
+#pragma unroll
+    for (int i = 0; i < KB / 2; ++i) r[i] = p[i];
+    if (G == 32) sz = *reinterpret_cast<const uint4*>(w.sz);
+    else if (G == 64) { const uint2 x = *reinterpret_cast<const uint2*>(w.sz); sz.x = x.x; sz.y = x.y; }
+    else sz.x = *reinterpret_cast<const uint32_t*>(w.sz);
+  } else if (w.kind == kRowBf16) {  // d = 32 P + 16 hf .. + 15
+#pragma unroll
+    for (int P = 0; P < 4; ++P) {
+      const uint4* p = reinterpret_cast<const uint4*>(w.p + 64 * P + 32 * hf);
+      r[2 * P] = p[0];
+      r[2 * P + 1] = p[1];
+    }
+  }
+}
+template <int VB>
+__device__ __forceinline__ void load_v(const Row& w, int hf, int G, uint4 (&r)[8], uint4& sz) {
+  if (VB < 16 && w.kind == kRowPacked) {
+    if constexpr (VB == 8) {
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(w.p + 16 * n + 8 * hf);
+        const uint2 y = *reinterpret_cast<const uint2*>(w.p + 16 * n + 16 + 8 * hf);
+        r[n / 2] = make_uint4(x.x, x.y, y.x, y.y);
+      }
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(w.p);
+#pragma unroll
+      for (int i = 0; i < VB; ++i) r[i] = p[i];
+    }
+    if (G == 32) sz = *reinterpret_cast<const uint4*>(w.sz);
+    else if (G == 64) { const uint2 x = *reinterpret_cast<const uint2*>(w.sz); sz.x = x.x; sz.y = x.y; }
+    else sz.x = *reinterpret_cast<const uint32_t*>(w.sz);
+  } else if (w.kind == kRowBf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(w.p + 128 * hf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = p[i];
+  }
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Both operands' majors as bits 15 (A) and 16 (B): 0 K-major, 1 MN-major.
+__host__ __device__ constexpr uint32_t idesc(int n, bool a_mn, bool b_mn) {
+  return umma_idesc_f16(kTile, n, b_mn) | (static_cast<uint32_t>(a_mn) << 15);
+}
+
+// fp32 <-> uint32 of the same order (for integer maxima).
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_free[i], 1);
+      mbar_init(&sm.v_full[i], 8);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_free[i], 4);
+      mbar_init(&sm.pv_done[i], 1);
+    }
+    mbar_init(&sm.q_ready, 4);
+    sm.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem_base, kTmCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = sm.tmem_base;
+  const int N = a.N;
+  const Work w = work_of(a, blockIdx.x);
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();  // past the dependency wait; this kernel writes no cache row
+  const int len = context_len(a, w.b);
+  const int nt = len < 0 ? 0 : (len + a.n_q + kTile - 1) / kTile;
+  const int i0 = static_cast<int>(static_cast<int64_t>(nt) * w.s / w.S);
+  const int i1 = static_cast<int>(static_cast<int64_t>(nt) * (w.s + 1) / w.S);
+  const int hq0 = w.h * a.c.g, col0 = w.cb * a.nb;
+  const int ncols = min(a.nb, a.c.g * a.n_q - col0);
+  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  // packed K rows in a tile: their low parts and zero points are MMAs of their own
+  const bool k_packed = KB < 16 && a.c.mode[w.h] == 0;
+  auto has_packed = [&](int i) { return k_packed && i * kTile < min(a.c.ve, len) && (i + 1) * kTile > a.c.vs; };
+
+  if (warp >= 4) {
+    // ---------------- unpack ----------------
+    const int hf = (warp - 4) >> 2, pos = 32 * (warp & 3) + lane;
+    Source src;
+    src.r = head_rows(a.c, w.b, w.h);
+    const int64_t d0 = w.b * a.sb + w.h * a.sh;
+    src.kd = reinterpret_cast<const uint8_t*>(a.kd + d0);
+    src.vd = reinterpret_cast<const uint8_t*>(a.vd + d0);
+    src.dstep = 2 * a.st;
+    src.len = max(len, 0);
+    src.end = src.len + a.n_q;
+    {
+      const uint64_t* mk = a.mask + w.b * a.mask_sb;
+      const uint64_t x = (lane < a.n_q ? mk[lane] : 0) | (lane + 32 < a.n_q ? mk[lane + 32] : 0);
+      src.any = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x))) |
+                (static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x >> 32))) << 32);
+    }
+    const uint32_t id_qk = idesc(N, false, false);
+    uint4 kr[8], vr[8], ksz = make_uint4(0, 0, 0, 0), vsz = ksz;
+    Row kw, vw;
+    kw.kind = vw.kind = kRowNone;
+    if (i0 < i1) {
+      kw = row_of<true>(a, src, i0 * kTile + pos);
+      load_k<KB>(kw, hf, a.c.G, kr, ksz);
+      vw = row_of<false>(a, src, i0 * kTile + pos);
+      load_v<VB>(vw, hf, a.c.G, vr, vsz);
+    }
+    for (int i = i0; i < i1; ++i) {
+      const int n = i - i0, buf = n & 1;
+      const bool packed = has_packed(i);
+      const uint32_t kt = tm + lanes + kTmK + buf * kTmKStride;
+      // ---- K: registers -> TMEM ----
+      uint32_t hi[32], lo[32], zz[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) zz[j] = 0u;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) hi[j] = lo[j] = 0u;
+      if (KB < 16 && kw.kind == kRowPacked) {
+        if constexpr (KB < 16) {
+          k_codes<KB>(kr, hi);
+          const int ng = kD / a.c.G;
+#pragma unroll
+          for (int P = 0; P < 4; ++P) {
+            const uint32_t s = half_of(ksz, ng + 32 * P / a.c.G) * 0x10001u;
+            const uint32_t s2 = hmul2_u(s, 0x38003800u);  // s / 2
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int x = 16 * t + 4 * P + j;
+                const uint32_t c = hi[x];
+                hi[x] = hmul2_u(c, s2);
+                if constexpr (KB > 2) lo[x] = hfma2_u(c, s2, hi[x] ^ 0x80008000u);
+              }
+          }
+          if (hf == 0) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (g < ng) {
+                const float z = 0.5f * fmaf(k_center<KB>(), f16_bits(half_of(ksz, ng + g)), f16_bits(half_of(ksz, g)));
+                const __half zh = __float2half_rn(z);
+                const uint32_t h = __half_as_ushort(zh), l = __half_as_ushort(__float2half_rn(z - __half2float(zh)));
+                zz[g >> 1] |= h << (16 * (g & 1));
+                zz[2 + (g >> 1)] |= l << (16 * (g & 1));
+                zz[4 + (g >> 1)] |= h << (16 * (g & 1));
+              }
+          }
+        }
+      } else if (kw.kind == kRowBf16) {
+#pragma unroll
+        for (int P = 0; P < 4; ++P)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint4 x = kr[2 * P + t];
+            uint32_t* o = hi + 16 * t + 4 * P;
+            o[0] = pack_f16x2(0.5f * bf16_lo(x.x), 0.5f * bf16_lo(x.z));
+            o[1] = pack_f16x2(0.5f * bf16_hi(x.x), 0.5f * bf16_hi(x.z));
+            o[2] = pack_f16x2(0.5f * bf16_lo(x.y), 0.5f * bf16_lo(x.w));
+            o[3] = pack_f16x2(0.5f * bf16_hi(x.y), 0.5f * bf16_hi(x.w));
+          }
+      }
+      if (i + 1 < i1) {
+        kw = row_of<true>(a, src, (i + 1) * kTile + pos);
+        load_k<KB>(kw, hf, a.c.G, kr, ksz);
+      } else {
+        kw.kind = kRowNone;
+      }
+      if (n >= 2) {
+        wait_for(a, sm, &sm.k_free[buf], ((n - 2) >> 1) & 1);
+        tc_fence_after();
+      }
+      tmem_st32(kt + 32 * hf, hi);
+      if (packed) {
+        if constexpr (KB > 2) tmem_st32(kt + kTmLo + 32 * hf, lo);
+        if (hf == 0) tmem_st8(kt + kTmZ, zz);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      named_bar(2, 256);
+      if (warp == 4 && lane == 0) {  // ---- QK of tile i ----
+        if (n == 0) wait_for(a, sm, &sm.q_ready, 0);
+        if (n >= 2) wait_for(a, sm, &sm.s_free[buf], ((n - 2) >> 1) & 1);
+        tc_fence_after();
+        const uint32_t kb = tm + kTmK + buf * kTmKStride, sb = tm + kTmS + buf * kTmSStride;
+        const uint32_t qa = smem_u32(sm.qt), lbo = 16 * N;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          umma_ts(sb, kb + 8 * ks, umma_sdesc(qa + ks * 2 * lbo, lbo, 128), id_qk, ks > 0);
+        if (packed) {
+          if constexpr (KB > 2) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_ts(sb, kb + kTmLo + 8 * ks, umma_sdesc(qa + ks * 2 * lbo, lbo, 128), id_qk, true);
+          }
+          umma_ts(sb, kb + kTmZ, umma_sdesc(smem_u32(sm.qz), lbo, 128), id_qk, true);
+        }
+        umma_commit(&sm.s_full[buf]);
+        umma_commit(&sm.k_free[buf]);
+      }
+      __syncwarp();
+      // ---- V: registers -> shared memory ----
+      uint32_t o[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0u;
+      if (VB < 16 && vw.kind == kRowPacked) {
+        if constexpr (VB < 16) v_values<VB>(vr, vsz, hf, a.c.G, o);
+      } else if (vw.kind == kRowBf16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[4 * j] = pack_f16x2(bf16_lo(vr[j].x), bf16_hi(vr[j].x));
+          o[4 * j + 1] = pack_f16x2(bf16_lo(vr[j].y), bf16_hi(vr[j].y));
+          o[4 * j + 2] = pack_f16x2(bf16_lo(vr[j].z), bf16_hi(vr[j].z));
+          o[4 * j + 3] = pack_f16x2(bf16_lo(vr[j].w), bf16_hi(vr[j].w));
+        }
+      }
+      if (i + 1 < i1) {
+        vw = row_of<false>(a, src, (i + 1) * kTile + pos);
+        load_v<VB>(vw, hf, a.c.G, vr, vsz);
+      } else {
+        vw.kind = kRowNone;
+      }
+      if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);
+      uint8_t* vt = sm.vt[buf] + (pos >> 3) * 2048 + (pos & 7) * 16 + 1024 * hf;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        *reinterpret_cast<uint4*>(vt + 128 * kk) = make_uint4(o[4 * kk], o[4 * kk + 1], o[4 * kk + 2], o[4 * kk + 3]);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[buf]);
+    }
+  } else {
+    // ---------------- softmax ----------------
+    const int tid = threadIdx.x;
+    // q into shared memory: 16-byte chunk ch (8 d) of a column's row goes to
+    // chunk 4 t + P of the permuted order; the sums of the 32-element blocks
+    for (int x = tid; x < N * 4; x += 128) {
+      const int c = x >> 2, P = x & 3;
+      const bool ok = c < ncols;
+      const int cg = col0 + c, tok = cg / a.c.g;
+      const int64_t row = ok ? (static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g) : 0;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        uint4 r = make_uint4(0u, 0u, 0u, 0u);
+        if (ok) r = __ldcg(reinterpret_cast<const uint4*>(a.q + row * kD) + 4 * P + t);
+        constexpr float f = 1.f / 128.f;
+        const uint32_t y[4] = {pack_f16x2(f * bf16_lo(r.x), f * bf16_lo(r.z)), pack_f16x2(f * bf16_hi(r.x), f * bf16_hi(r.z)),
+                               pack_f16x2(f * bf16_lo(r.y), f * bf16_lo(r.w)), pack_f16x2(f * bf16_hi(r.y), f * bf16_hi(r.w))};
+        *reinterpret_cast<uint4*>(sm.qt + (4 * t + P) * (16 * N) + (c >> 3) * 128 + (c & 7) * 16) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += f16_bits(y[j] & 0xffffu) + f16_bits(y[j] >> 16);
+      }
+      sm.qs[c][P] = sum;
+    }
+    named_bar(1, 128);
+    if (tid < N) {
+      const int c = tid, ng = kD / a.c.G, per = 4 / ng;
+      uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      for (int g = 0; g < ng; ++g) {
+        float s = 0.f;
+        for (int j = 0; j < per; ++j) s += sm.qs[c][g * per + j];
+        const __half sh = __float2half_rn(s);
+        const uint32_t h = __half_as_ushort(sh), l = __half_as_ushort(__float2half_rn(s - __half2float(sh)));
+        const int sft = 16 * (g & 1);
+        if (g < 2) { z[0] |= h << sft; z[2] |= h << sft; z[4] |= l << sft; }
+        else { z[1] |= h << sft; z[3] |= h << sft; z[5] |= l << sft; }
+      }
+      uint8_t* d = sm.qz + (c >> 3) * 128 + (c & 7) * 16;
+      *reinterpret_cast<uint4*>(d) = make_uint4(z[0], z[1], z[2], z[3]);
+      *reinterpret_cast<uint4*>(d + 16 * N) = make_uint4(z[4], z[5], z[6], z[7]);
+      uint64_t mk = 0;
+      if (c < ncols) mk = a.mask[w.b * a.mask_sb + (col0 + c) / a.c.g];
+      sm.colmask[c] = mk;
+      sm.m[c] = kUnset;
+    }
+    fence_async_smem();  // the tensor cores read q
+    named_bar(1, 128);
+    if (lane == 0) mbar_arrive(&sm.q_ready);
+
+    const float sl2 = a.scale_log2 * kOperandScale;
+    const uint32_t id_pv = idesc(N, true, true);
+    float l[kMaxCols];
+#pragma unroll
+    for (int c = 0; c < kMaxCols; ++c) l[c] = 0.f;
+    for (int i = i0; i < i1; ++i) {
+      const int n = i - i0, buf = n & 1;
+      const int t = i * kTile + tid;          // this thread's position
+      const bool whole = (i + 1) * kTile <= len;  // every position is context
+      const bool ctx = t < len;
+      const int j = ctx || t >= len + a.n_q ? 0 : t - len;
+      const bool draft = !ctx && t < len + a.n_q;
+      const uint32_t sb = tm + lanes + kTmS + buf * kTmSStride;
+      wait_for(a, sm, &sm.s_full[buf], (n >> 1) & 1);
+      tc_fence_after();
+      float x[kMaxCols];
+      // x = score - reference, log2 units; -inf where this position is not attended
+      auto scores = [&](bool relative) {
+#pragma unroll
+        for (int c0 = 0; c0 < kMaxCols; c0 += 16)
+          if (c0 < N) {
+            uint32_t s[16];
+            tmem_ld16(sb + c0, s);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 mm = relative ? *reinterpret_cast<const float4*>(&sm.m[c0 + k]) : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[c0 + k] = fmaf(__uint_as_float(s[k]), sl2, -mm.x);
+              x[c0 + k + 1] = fmaf(__uint_as_float(s[k + 1]), sl2, -mm.y);
+              x[c0 + k + 2] = fmaf(__uint_as_float(s[k + 2]), sl2, -mm.z);
+              x[c0 + k + 3] = fmaf(__uint_as_float(s[k + 3]), sl2, -mm.w);
+            }
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (!(ctx || (draft && ((sm.colmask[c0 + k] >> j) & 1)))) x[c0 + k] = -INFINITY;
+            }
+          }
+      };
+      scores(true);
+      float top = -INFINITY;
+#pragma unroll
+      for (int c0 = 0; c0 < kMaxCols; c0 += 16)
+        if (c0 < N) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, x[c0 + k]);
+        }
+      if (bar_or(1, 128, top > kMaxGrowth)) {
+        // some column's reference is too low (or unset): move the references
+        // of the columns that need it to their maximum over this tile
+        if (tid < kMaxCols) sm.top[tid] = 0u;
+        named_bar(1, 128);
+        scores(false);
+#pragma unroll
+        for (int c = 0; c < kMaxCols; ++c)
+          if (c < N) {
+            const uint32_t k = __reduce_max_sync(0xffffffffu, order_of(x[c]));
+            if (lane == 0) atomicMax(&sm.top[c], k);
+          }
+        named_bar(1, 128);
+        if (tid < N) {
+          const float v = value_of(sm.top[tid]), old = sm.m[tid];
+          const bool move = v > old + kMaxGrowth;
+          sm.fac[tid] = move ? ex2(old - v) : 1.f;
+          if (move) sm.m[tid] = v;
+        }
+        named_bar(1, 128);
+        if (n > 0) {  // every earlier PV has landed before O is rescaled
+          wait_for(a, sm, &sm.pv_done[buf ^ 1], ((n - 1) >> 1) & 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < N; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(tm + lanes + kTmO + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.fac[c0 + k]);
+            tmem_st16(tm + lanes + kTmO + c0, o);
+          }
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCols; ++c)
+          if (c < N) l[c] *= sm.fac[c];
+        scores(true);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+      if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);  // P's buffer is free
+      uint8_t* pt = sm.pt[buf] + (tid >> 3) * (16 * N) + (tid & 7) * 16;
+#pragma unroll
+      for (int c0 = 0; c0 < kMaxCols; c0 += 8)
+        if (c0 < N) {
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const float p0 = ex2(x[c0 + k]), p1 = ex2(x[c0 + k + 1]);
+            l[c0 + k] += p0;
+            l[c0 + k + 1] += p1;
+            y[k >> 1] = pack_f16x2(p0, p1);
+          }
+          *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      fence_async_smem();
+      tc_fence_before();
+      named_bar(1, 128);
+      if (tid == 0) {  // ---- PV of tile i ----
+        wait_for(a, sm, &sm.v_full[buf], (n >> 1) & 1);
+        tc_fence_after();
+        const uint32_t va = smem_u32(sm.vt[buf]), pa = smem_u32(sm.pt[buf]), lbo = 16 * N;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          umma_ss(tm + kTmO, umma_sdesc(va + ks * 4096, 2048, 128), umma_sdesc(pa + ks * 2 * lbo, lbo, 128), id_pv,
+                  n > 0 || ks > 0);
+        umma_commit(&sm.pv_done[buf]);
+      }
+      __syncwarp();
+    }
+    // ---- the column sums over the lanes, then the outputs (thread = d) ----
+    const int nd = i1 - i0;
+    if (nd > 0) {
+      wait_for(a, sm, &sm.pv_done[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
+      tc_fence_after();
+    }
+#pragma unroll
+    for (int c = 0; c < kMaxCols; ++c)
+      if (c < N) {
+        float s = l[c];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) sm.lsum[warp][c] = s;
+      }
+    named_bar(1, 128);
+    const bool bad = sm.abort != 0;
+    const float nan = __int_as_float(0x7fffffff);
+    float* slot = a.ws + static_cast<int64_t>(blockIdx.x) * N * (kD + 2);
+#pragma unroll 1
+    for (int c0 = 0; c0 < N; c0 += 16) {
+      uint32_t o[16];
+      if (nd > 0) {
+        tmem_ld16(tm + lanes + kTmO + c0, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int c = c0 + k;
+        if (c >= ncols) break;
+        const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
+        const float M = bad ? nan : (L > 0.f ? sm.m[c] : -INFINITY);
+        if (w.S > 1) {
+          slot[c * kD + tid] = __uint_as_float(o[k]);
+          if (tid < 2) slot[N * kD + 2 * c + tid] = tid ? L : M;
+        } else {
+          const int cg = col0 + c, tok = cg / a.c.g;
+          const int64_t row = (static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g);
+          const float inv = bad ? nan : (L > 0.f ? 1.f / L : 0.f);
+          a.out[row * kD + tid] = f32_to_bf16_bits(__uint_as_float(o[k]) * inv);
+          if (tid == 0 && a.lse) a.lse[row] = bad ? nan : 0.69314718055994531f * (M + log2f(L));
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tm, kTmCols);
+  }
+}
+
+const void* tree_kernel_k2(int vb);
+const void* tree_kernel_k4(int vb);
+const void* tree_kernel_k8(int vb);
+const void* tree_kernel_k16(int vb);
+
+}  // namespace tree
+}  // namespace kvq
