@@ -31,10 +31,10 @@
 // all lanes at once, when a score of a tile exceeds it by more than 2^12
 // (P <= 4096 in fp16); the column sums stay in the threads until the end.
 //
-// CTA = 12 warps: 0-3 softmax (TMEM lanes 32 w ..), 4-11 unpack (warp w: lanes
-// 32 (w mod 4) .., half (w - 4) / 4 of the row).  An unpack thread issues the
-// QK of a tile, a softmax thread its PV.  TMEM: two K buffers (64 columns
-// high, 64 low, 8 zero points), two S buffers of 64, O of 64.
+// CTA = 13 warps: 0-3 softmax (TMEM lanes 32 w ..), 4-11 unpack (warp w: lanes
+// 32 (w mod 4) .., half (w - 4) / 4 of the row), 12 issues the MMAs.  TMEM: two
+// K buffers (64 columns high, 64 low, 8 zero points), two S buffers of 64, O
+// of 64.
 #pragma once
 
 #include "kvq_geom.cuh"
@@ -43,7 +43,9 @@
 namespace kvq {
 namespace tree {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
+constexpr int kMmaWarp = 12;
+constexpr int kAhead = 4;               // tiles that the L2 prefetch runs ahead
 constexpr int kTile = 128;              // positions per tile (TMEM lanes)
 constexpr int kMaxCols = 64;            // columns per unit (at most)
 constexpr int kMaxSplitCtas = 160;      // CTAs of a call whose units are split (workspace slots)
@@ -83,11 +85,11 @@ struct Smem {
   alignas(1024) uint8_t qt[kMaxCols * 256];   // q: column, d contiguous (permuted)
   alignas(128) uint8_t qz[kMaxCols * 32];     // group sums of q: column, 16 K indexes
   uint64_t colmask[kMaxCols];
-  float m[kMaxCols], fac[kMaxCols];
-  uint32_t top[kMaxCols];
-  float lsum[4][kMaxCols];
+  alignas(16) float m[kMaxCols];
+  alignas(16) float fac[kMaxCols];
+  float lsum[4][kMaxCols];  // per softmax warp: column maxima of a tile; at the end column sums
   float qs[kMaxCols][4];
-  uint64_t k_free[2], v_full[2], s_full[2], s_free[2], pv_done[2], q_ready;
+  uint64_t k_full[2], k_free[2], v_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready;
   uint32_t tmem_base;
   int abort;
 };
@@ -289,6 +291,8 @@ __device__ __forceinline__ void v_values(const uint4 (&r)[8], const uint4& sz, i
   }
 }
 
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x) { return pack_f16x2(bf16_lo(x), bf16_hi(x)); }
+
 // Where a row's values come from.
 enum RowKind { kRowNone = 0, kRowPacked = 1, kRowBf16 = 2 };
 struct Row {
@@ -329,47 +333,37 @@ __device__ __forceinline__ Row row_of(const Args& a, const Source& s, int t) {
   return w;
 }
 
-// The raw bytes of half hf of a row (and its scale/zero row).
-template <int KB>
-__device__ __forceinline__ void load_k(const Row& w, int hf, int G, uint4 (&r)[8], uint4& sz) {
-  if (KB < 16 && w.kind == kRowPacked) {
-    const uint4* p = reinterpret_cast<const uint4*>(w.p + hf * 8 * KB);
-#pragma unroll
-    for (int i = 0; i < KB / 2; ++i) r[i] = p[i];
-    if (G == 32) sz = *reinterpret_cast<const uint4*>(w.sz);
-    else if (G == 64) { const uint2 x = *reinterpret_cast<const uint2*>(w.sz); sz.x = x.x; sz.y = x.y; }
-    else sz.x = *reinterpret_cast<const uint32_t*>(w.sz);
-  } else if (w.kind == kRowBf16) {  // d = 32 P + 16 hf .. + 15
-#pragma unroll
-    for (int P = 0; P < 4; ++P) {
-      const uint4* p = reinterpret_cast<const uint4*>(w.p + 64 * P + 32 * hf);
-      r[2 * P] = p[0];
-      r[2 * P + 1] = p[1];
-    }
+// The raw bytes of half hf of a packed row and its scale/zero row.
+__device__ __forceinline__ void load_sz(const uint8_t* p, int G, uint4& sz) {
+  if (G == 32) {
+    sz = *reinterpret_cast<const uint4*>(p);
+  } else if (G == 64) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    sz.x = x.x;
+    sz.y = x.y;
+  } else {
+    sz.x = *reinterpret_cast<const uint32_t*>(p);
   }
 }
+template <int KB>
+__device__ __forceinline__ void load_k_packed(const uint8_t* row, int hf, uint4 (&r)[8]) {
+  const uint4* p = reinterpret_cast<const uint4*>(row + hf * 8 * KB);
+#pragma unroll
+  for (int i = 0; i < KB / 2; ++i) r[i] = p[i];
+}
 template <int VB>
-__device__ __forceinline__ void load_v(const Row& w, int hf, int G, uint4 (&r)[8], uint4& sz) {
-  if (VB < 16 && w.kind == kRowPacked) {
-    if constexpr (VB == 8) {
+__device__ __forceinline__ void load_v_packed(const uint8_t* row, int hf, uint4 (&r)[8]) {
+  if constexpr (VB == 8) {
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(w.p + 16 * n + 8 * hf);
-        const uint2 y = *reinterpret_cast<const uint2*>(w.p + 16 * n + 16 + 8 * hf);
-        r[n / 2] = make_uint4(x.x, x.y, y.x, y.y);
-      }
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(w.p);
-#pragma unroll
-      for (int i = 0; i < VB; ++i) r[i] = p[i];
+    for (int n = 0; n < 8; n += 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(row + 16 * n + 8 * hf);
+      const uint2 y = *reinterpret_cast<const uint2*>(row + 16 * n + 16 + 8 * hf);
+      r[n / 2] = make_uint4(x.x, x.y, y.x, y.y);
     }
-    if (G == 32) sz = *reinterpret_cast<const uint4*>(w.sz);
-    else if (G == 64) { const uint2 x = *reinterpret_cast<const uint2*>(w.sz); sz.x = x.x; sz.y = x.y; }
-    else sz.x = *reinterpret_cast<const uint32_t*>(w.sz);
-  } else if (w.kind == kRowBf16) {
-    const uint4* p = reinterpret_cast<const uint4*>(w.p + 128 * hf);
+  } else {
+    const uint4* p = reinterpret_cast<const uint4*>(row);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = p[i];
+    for (int i = 0; i < VB; ++i) r[i] = p[i];
   }
 }
 
@@ -384,13 +378,70 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool a_mn, bool b_mn) {
   return umma_idesc_f16(kTile, n, b_mn) | (static_cast<uint32_t>(a_mn) << 15);
 }
 
-// fp32 <-> uint32 of the same order (for integer maxima).
-__device__ __forceinline__ uint32_t order_of(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+// One lane of a converged warp; what it issues stays in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+
+// c' -> the high (and low) fp16 parts of c' s / 2 for 16 pairs of slice t of a
+// half K row (c holds both slices' c').
+template <int KB>
+__device__ __forceinline__ void k_parts(const uint32_t (&c)[32], int t, const uint32_t (&s2)[4], uint32_t (&hi)[16],
+                                        uint32_t (&lo)[16]) {
+#pragma unroll
+  for (int P = 0; P < 4; ++P)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = c[16 * t + 4 * P + j], h = hmul2_u(x, s2[P]);
+      hi[4 * P + j] = h;
+      if constexpr (KB > 2) lo[4 * P + j] = hfma2_u(x, s2[P], h ^ 0x80008000u);
+    }
+}
+
+// The zero points' A row: z' / 2 as (high, low, high) of each group.
+template <int KB>
+__device__ __forceinline__ void z_parts(const uint4& sz, int G, uint32_t (&zz)[8]) {
+  const int ng = kD / G;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) zz[j] = 0u;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if (g < ng) {
+      const float z = 0.5f * fmaf(k_center<KB>(), f16_bits(half_of(sz, ng + g)), f16_bits(half_of(sz, g)));
+      const __half zh = __float2half_rn(z);
+      const uint32_t h = __half_as_ushort(zh), l = __half_as_ushort(__float2half_rn(z - __half2float(zh)));
+      zz[g >> 1] |= h << (16 * (g & 1));
+      zz[2 + (g >> 1)] |= l << (16 * (g & 1));
+      zz[4 + (g >> 1)] |= h << (16 * (g & 1));
+    }
+}
+
+// s / 2 of the four 32-element blocks.
+__device__ __forceinline__ void k_scales(const uint4& sz, int G, uint32_t (&s2)[4]) {
+  const int ng = kD / G;
+#pragma unroll
+  for (int P = 0; P < 4; ++P) s2[P] = hmul2_u(half_of(sz, ng + 32 * P / G) * 0x10001u, 0x38003800u);
+}
+
+// Bulk prefetch into L2 of rows [i, i + n) of w bytes (16-byte granules).
+__device__ __forceinline__ void prefetch_rows(const uint8_t* base, int64_t i, int n, int w) {
+  const uint64_t p0 = reinterpret_cast<uint64_t>(base + i * w) & ~15ull;
+  const uint64_t p1 = (reinterpret_cast<uint64_t>(base + (i + n) * w) + 15) & ~15ull;
+  prefetch_l2(reinterpret_cast<const void*>(p0), static_cast<uint32_t>(p1 - p0));
+}
+// The visual rows of tile i, K (key) or V: the bulk of a unit's bytes.
+__device__ __forceinline__ void prefetch_tile(const Geom& c, const HeadRows& r, int i, int len, bool key) {
+  const int t0 = max(i * kTile, c.vs), t1 = min(min((i + 1) * kTile, c.ve), len);
+  if (t0 >= t1) return;
+  if (key) {
+    prefetch_rows(r.vis_k, t0 - c.vs, t1 - t0, r.k_packed ? c.krow : kRowBytes);
+    if (r.k_packed) prefetch_rows(r.vis_ksz, t0 - c.vs, t1 - t0, c.kszrow);
+  } else {
+    prefetch_rows(r.vis_v, t0 - c.vs, t1 - t0, r.v_packed ? c.vrow : kRowBytes);
+    if (r.v_packed) prefetch_rows(r.vis_vsz, t0 - c.vs, t1 - t0, c.vszrow);
+  }
 }
 
 template <int KB, int VB>
@@ -400,17 +451,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_full[i], 8);
       mbar_init(&sm.k_free[i], 1);
       mbar_init(&sm.v_full[i], 8);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.s_free[i], 4);
+      mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.pv_done[i], 1);
     }
     mbar_init(&sm.q_ready, 4);
     sm.abort = 0;
     fence_barrier_init();
   }
-  if (warp == 0) tmem_alloc(&sm.tmem_base, kTmCols);
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem_base, kTmCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -430,111 +483,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const bool k_packed = KB < 16 && a.c.mode[w.h] == 0;
   auto has_packed = [&](int i) { return k_packed && i * kTile < min(a.c.ve, len) && (i + 1) * kTile > a.c.vs; };
 
-  if (warp >= 4) {
-    // ---------------- unpack ----------------
-    const int hf = (warp - 4) >> 2, pos = 32 * (warp & 3) + lane;
-    Source src;
-    src.r = head_rows(a.c, w.b, w.h);
-    const int64_t d0 = w.b * a.sb + w.h * a.sh;
-    src.kd = reinterpret_cast<const uint8_t*>(a.kd + d0);
-    src.vd = reinterpret_cast<const uint8_t*>(a.vd + d0);
-    src.dstep = 2 * a.st;
-    src.len = max(len, 0);
-    src.end = src.len + a.n_q;
-    {
-      const uint64_t* mk = a.mask + w.b * a.mask_sb;
-      const uint64_t x = (lane < a.n_q ? mk[lane] : 0) | (lane + 32 < a.n_q ? mk[lane + 32] : 0);
-      src.any = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x))) |
-                (static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x >> 32))) << 32);
-    }
-    const uint32_t id_qk = idesc(N, false, false);
-    uint4 kr[8], vr[8], ksz = make_uint4(0, 0, 0, 0), vsz = ksz;
-    Row kw, vw;
-    kw.kind = vw.kind = kRowNone;
-    if (i0 < i1) {
-      kw = row_of<true>(a, src, i0 * kTile + pos);
-      load_k<KB>(kw, hf, a.c.G, kr, ksz);
-      vw = row_of<false>(a, src, i0 * kTile + pos);
-      load_v<VB>(vw, hf, a.c.G, vr, vsz);
-    }
+  if (warp == kMmaWarp) {
+    // ---------------- MMAs ----------------
+    const uint32_t id_qk = idesc(N, false, false), id_pv = idesc(N, true, true);
+    const uint32_t lbo = 16 * N;
+    const uint32_t qa = smem_u32(sm.qt), qz = smem_u32(sm.qz);
+    auto issue_pv = [&](int n) {
+      const int buf = n & 1;
+      wait_for(a, sm, &sm.v_full[buf], (n >> 1) & 1);
+      wait_for(a, sm, &sm.p_full[buf], (n >> 1) & 1);
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t va = smem_u32(sm.vt[buf]), pa = smem_u32(sm.pt[buf]);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          umma_ss(tm + kTmO, umma_sdesc(va + ks * 4096, 2048, 128), umma_sdesc(pa + ks * 2 * lbo, lbo, 128), id_pv,
+                  n > 0 || ks > 0);
+        umma_commit(&sm.pv_done[buf]);
+      }
+      __syncwarp();
+    };
+    if (i0 < i1) wait_for(a, sm, &sm.q_ready, 0);
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
+      wait_for(a, sm, &sm.k_full[buf], (n >> 1) & 1);
+      if (n >= 2) wait_for(a, sm, &sm.s_free[buf], ((n - 2) >> 1) & 1);
+      tc_fence_after();
       const bool packed = has_packed(i);
-      const uint32_t kt = tm + lanes + kTmK + buf * kTmKStride;
-      // ---- K: registers -> TMEM ----
-      uint32_t hi[32], lo[32], zz[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) zz[j] = 0u;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) hi[j] = lo[j] = 0u;
-      if (KB < 16 && kw.kind == kRowPacked) {
-        if constexpr (KB < 16) {
-          k_codes<KB>(kr, hi);
-          const int ng = kD / a.c.G;
-#pragma unroll
-          for (int P = 0; P < 4; ++P) {
-            const uint32_t s = half_of(ksz, ng + 32 * P / a.c.G) * 0x10001u;
-            const uint32_t s2 = hmul2_u(s, 0x38003800u);  // s / 2
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int x = 16 * t + 4 * P + j;
-                const uint32_t c = hi[x];
-                hi[x] = hmul2_u(c, s2);
-                if constexpr (KB > 2) lo[x] = hfma2_u(c, s2, hi[x] ^ 0x80008000u);
-              }
-          }
-          if (hf == 0) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (g < ng) {
-                const float z = 0.5f * fmaf(k_center<KB>(), f16_bits(half_of(ksz, ng + g)), f16_bits(half_of(ksz, g)));
-                const __half zh = __float2half_rn(z);
-                const uint32_t h = __half_as_ushort(zh), l = __half_as_ushort(__float2half_rn(z - __half2float(zh)));
-                zz[g >> 1] |= h << (16 * (g & 1));
-                zz[2 + (g >> 1)] |= l << (16 * (g & 1));
-                zz[4 + (g >> 1)] |= h << (16 * (g & 1));
-              }
-          }
-        }
-      } else if (kw.kind == kRowBf16) {
-#pragma unroll
-        for (int P = 0; P < 4; ++P)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint4 x = kr[2 * P + t];
-            uint32_t* o = hi + 16 * t + 4 * P;
-            o[0] = pack_f16x2(0.5f * bf16_lo(x.x), 0.5f * bf16_lo(x.z));
-            o[1] = pack_f16x2(0.5f * bf16_hi(x.x), 0.5f * bf16_hi(x.z));
-            o[2] = pack_f16x2(0.5f * bf16_lo(x.y), 0.5f * bf16_lo(x.w));
-            o[3] = pack_f16x2(0.5f * bf16_hi(x.y), 0.5f * bf16_hi(x.w));
-          }
-      }
-      if (i + 1 < i1) {
-        kw = row_of<true>(a, src, (i + 1) * kTile + pos);
-        load_k<KB>(kw, hf, a.c.G, kr, ksz);
-      } else {
-        kw.kind = kRowNone;
-      }
-      if (n >= 2) {
-        wait_for(a, sm, &sm.k_free[buf], ((n - 2) >> 1) & 1);
-        tc_fence_after();
-      }
-      tmem_st32(kt + 32 * hf, hi);
-      if (packed) {
-        if constexpr (KB > 2) tmem_st32(kt + kTmLo + 32 * hf, lo);
-        if (hf == 0) tmem_st8(kt + kTmZ, zz);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      named_bar(2, 256);
-      if (warp == 4 && lane == 0) {  // ---- QK of tile i ----
-        if (n == 0) wait_for(a, sm, &sm.q_ready, 0);
-        if (n >= 2) wait_for(a, sm, &sm.s_free[buf], ((n - 2) >> 1) & 1);
-        tc_fence_after();
+      if (elect_one()) {
         const uint32_t kb = tm + kTmK + buf * kTmKStride, sb = tm + kTmS + buf * kTmSStride;
-        const uint32_t qa = smem_u32(sm.qt), lbo = 16 * N;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           umma_ts(sb, kb + 8 * ks, umma_sdesc(qa + ks * 2 * lbo, lbo, 128), id_qk, ks > 0);
@@ -544,32 +521,184 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int ks = 0; ks < 8; ++ks)
               umma_ts(sb, kb + kTmLo + 8 * ks, umma_sdesc(qa + ks * 2 * lbo, lbo, 128), id_qk, true);
           }
-          umma_ts(sb, kb + kTmZ, umma_sdesc(smem_u32(sm.qz), lbo, 128), id_qk, true);
+          umma_ts(sb, kb + kTmZ, umma_sdesc(qz, lbo, 128), id_qk, true);
         }
         umma_commit(&sm.s_full[buf]);
         umma_commit(&sm.k_free[buf]);
       }
       __syncwarp();
+      if (n > 0) issue_pv(n - 1);
+    }
+    if (i0 < i1) issue_pv(i1 - i0 - 1);
+  } else if (warp >= 4) {
+    // ---------------- unpack ----------------
+    const int hf = (warp - 4) >> 2, pos = 32 * (warp & 3) + lane;
+    const Geom& c = a.c;
+    Source src;
+    src.r = head_rows(c, w.b, w.h);
+    src.len = max(len, 0);
+    const bool fetch = (warp & 3) == 0 && lane == 0;  // of K (hf = 0) or V (hf = 1)
+    if (fetch)
+      for (int k = 0; k < kAhead && i0 + k < i1; ++k) prefetch_tile(c, src.r, i0 + k, src.len, hf == 0);
+    const int64_t d0 = w.b * a.sb + w.h * a.sh;
+    src.kd = reinterpret_cast<const uint8_t*>(a.kd + d0);
+    src.vd = reinterpret_cast<const uint8_t*>(a.vd + d0);
+    src.dstep = 2 * a.st;
+    src.end = src.len + a.n_q;
+    {
+      const uint64_t* mk = a.mask + w.b * a.mask_sb;
+      const uint64_t x = (lane < a.n_q ? mk[lane] : 0) | (lane + 32 < a.n_q ? mk[lane + 32] : 0);
+      src.any = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x))) |
+                (static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x >> 32))) << 32);
+    }
+    // All 32 rows of this warp in tile i are packed ones (the same for K and
+    // V of the head: a K-only head has packed V rows alone).
+    const int first = 32 * (warp & 3), vend = min(c.ve, src.len);
+    auto all_visual = [&](int i) { return i * kTile + first >= c.vs && i * kTile + first + 32 <= vend; };
+    const bool kp = KB < 16 && src.r.k_packed, vp = VB < 16 && src.r.v_packed;
+    uint4 kr[8], vr[8], ksz = make_uint4(0, 0, 0, 0), vsz = ksz;
+    auto load_k = [&](int i) {
+      if constexpr (KB < 16) {
+        const int64_t x = i * kTile + pos - c.vs;
+        load_k_packed<KB>(src.r.vis_k + x * c.krow, hf, kr);
+        load_sz(src.r.vis_ksz + x * c.kszrow, c.G, ksz);
+      }
+    };
+    auto load_v = [&](int i) {
+      if constexpr (VB < 16) {
+        const int64_t x = i * kTile + pos - c.vs;
+        load_v_packed<VB>(src.r.vis_v + x * c.vrow, hf, vr);
+        load_sz(src.r.vis_vsz + x * c.vszrow, c.G, vsz);
+      }
+    };
+    if (i0 < i1 && all_visual(i0)) {
+      if (kp) load_k(i0);
+      if (vp) load_v(i0);
+    }
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const int n = i - i0, buf = n & 1;
+      const bool vis = all_visual(i), next = i + 1 < i1 && all_visual(i + 1);
+      if (fetch && i + kAhead < i1) prefetch_tile(c, src.r, i + kAhead, src.len, hf == 0);
+      // ---- K: registers -> TMEM ----
+      const uint32_t kt = tm + lanes + kTmK + buf * kTmKStride + 32 * hf;
+      auto k_buffer = [&]() {
+        if (n >= 2) {
+          wait_for(a, sm, &sm.k_free[buf], ((n - 2) >> 1) & 1);
+          tc_fence_after();
+        }
+      };
+      uint32_t hi[16], lo[16];
+      if (kp && vis) {
+        if constexpr (KB < 16) {
+          uint32_t cc[32], s2[4];
+          k_codes<KB>(kr, cc);
+          k_scales(ksz, c.G, s2);
+          uint32_t zz[8];
+          if (hf == 0) z_parts<KB>(ksz, c.G, zz);
+          if (next) load_k(i + 1);
+          k_buffer();
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            k_parts<KB>(cc, t, s2, hi, lo);
+            tmem_st16(kt + 16 * t, hi);
+            if constexpr (KB > 2) tmem_st16(kt + kTmLo + 16 * t, lo);
+          }
+          if (hf == 0) tmem_st8(kt + kTmZ, zz);
+        }
+      } else {
+        const Row row = row_of<true>(a, src, i * kTile + pos);
+        const bool packed = has_packed(i);
+        uint32_t zz[8], s2[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) zz[j] = 0u;
+        uint32_t cc[32];
+        uint4 raw[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row.kind == kRowBf16) {  // d = 32 P + 16 hf .. + 15
+#pragma unroll
+          for (int P = 0; P < 4; ++P) {
+            const uint4* p = reinterpret_cast<const uint4*>(row.p + 64 * P + 32 * hf);
+            raw[2 * P] = p[0];
+            raw[2 * P + 1] = p[1];
+          }
+        }
+        if constexpr (KB < 16) {
+          if (row.kind == kRowPacked) {
+            uint4 sz = make_uint4(0u, 0u, 0u, 0u);
+            load_k_packed<KB>(row.p, hf, raw);
+            load_sz(row.sz, c.G, sz);
+            k_codes<KB>(raw, cc);
+            k_scales(sz, c.G, s2);
+            if (hf == 0) z_parts<KB>(sz, c.G, zz);
+          }
+        }
+        if (kp && next) load_k(i + 1);
+        k_buffer();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) lo[j] = 0u;
+          if (KB < 16 && row.kind == kRowPacked) {
+            if constexpr (KB < 16) k_parts<KB>(cc, t, s2, hi, lo);
+          } else {
+#pragma unroll
+            for (int P = 0; P < 4; ++P) {
+              const uint4 x = raw[2 * P + t];
+              hi[4 * P] = pack_f16x2(0.5f * bf16_lo(x.x), 0.5f * bf16_lo(x.z));
+              hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(x.x), 0.5f * bf16_hi(x.z));
+              hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(x.y), 0.5f * bf16_lo(x.w));
+              hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(x.y), 0.5f * bf16_hi(x.w));
+            }
+          }
+          __syncwarp();
+          tmem_st16(kt + 16 * t, hi);
+          if (KB > 2 && packed) tmem_st16(kt + kTmLo + 16 * t, lo);
+        }
+        if (packed && hf == 0) tmem_st8(kt + kTmZ, zz);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[buf]);
       // ---- V: registers -> shared memory ----
       uint32_t o[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = 0u;
-      if (VB < 16 && vw.kind == kRowPacked) {
-        if constexpr (VB < 16) v_values<VB>(vr, vsz, hf, a.c.G, o);
-      } else if (vw.kind == kRowBf16) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[4 * j] = pack_f16x2(bf16_lo(vr[j].x), bf16_hi(vr[j].x));
-          o[4 * j + 1] = pack_f16x2(bf16_lo(vr[j].y), bf16_hi(vr[j].y));
-          o[4 * j + 2] = pack_f16x2(bf16_lo(vr[j].z), bf16_hi(vr[j].z));
-          o[4 * j + 3] = pack_f16x2(bf16_lo(vr[j].w), bf16_hi(vr[j].w));
+      if (vp && vis) {
+        if constexpr (VB < 16) {
+          v_values<VB>(vr, vsz, hf, c.G, o);
+          if (next) load_v(i + 1);
         }
-      }
-      if (i + 1 < i1) {
-        vw = row_of<false>(a, src, (i + 1) * kTile + pos);
-        load_v<VB>(vw, hf, a.c.G, vr, vsz);
       } else {
-        vw.kind = kRowNone;
+        const Row row = row_of<false>(a, src, i * kTile + pos);
+        uint4 raw[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row.kind == kRowBf16) {
+          const uint4* p = reinterpret_cast<const uint4*>(row.p + 128 * hf);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) raw[j] = p[j];
+        }
+        bool done = false;
+        if constexpr (VB < 16) {
+          if (row.kind == kRowPacked) {
+            uint4 sz = make_uint4(0u, 0u, 0u, 0u);
+            load_v_packed<VB>(row.p, hf, raw);
+            load_sz(row.sz, c.G, sz);
+            v_values<VB>(raw, sz, hf, c.G, o);
+            done = true;
+          }
+        }
+        if (!done) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[4 * j] = bf16x2_to_f16x2(raw[j].x);
+            o[4 * j + 1] = bf16x2_to_f16x2(raw[j].y);
+            o[4 * j + 2] = bf16x2_to_f16x2(raw[j].z);
+            o[4 * j + 3] = bf16x2_to_f16x2(raw[j].w);
+          }
+        }
+        if (vp && next) load_v(i + 1);
       }
       if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);
       uint8_t* vt = sm.vt[buf] + (pos >> 3) * 2048 + (pos & 7) * 16 + 1024 * hf;
@@ -590,14 +719,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const bool ok = c < ncols;
       const int cg = col0 + c, tok = cg / a.c.g;
       const int64_t row = ok ? (static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g) : 0;
+      uint4 r[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        r[t] = ok ? __ldcg(reinterpret_cast<const uint4*>(a.q + row * kD) + 4 * P + t) : make_uint4(0u, 0u, 0u, 0u);
       float sum = 0.f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        uint4 r = make_uint4(0u, 0u, 0u, 0u);
-        if (ok) r = __ldcg(reinterpret_cast<const uint4*>(a.q + row * kD) + 4 * P + t);
         constexpr float f = 1.f / 128.f;
-        const uint32_t y[4] = {pack_f16x2(f * bf16_lo(r.x), f * bf16_lo(r.z)), pack_f16x2(f * bf16_hi(r.x), f * bf16_hi(r.z)),
-                               pack_f16x2(f * bf16_lo(r.y), f * bf16_lo(r.w)), pack_f16x2(f * bf16_hi(r.y), f * bf16_hi(r.w))};
+        const uint32_t y[4] = {
+            pack_f16x2(f * bf16_lo(r[t].x), f * bf16_lo(r[t].z)), pack_f16x2(f * bf16_hi(r[t].x), f * bf16_hi(r[t].z)),
+            pack_f16x2(f * bf16_lo(r[t].y), f * bf16_lo(r[t].w)), pack_f16x2(f * bf16_hi(r[t].y), f * bf16_hi(r[t].w))};
         *reinterpret_cast<uint4*>(sm.qt + (4 * t + P) * (16 * N) + (c >> 3) * 128 + (c & 7) * 16) =
             make_uint4(y[0], y[1], y[2], y[3]);
 #pragma unroll
@@ -609,21 +741,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (tid < N) {
       const int c = tid, ng = kD / a.c.G, per = 4 / ng;
       uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      for (int g = 0; g < ng; ++g) {
-        float s = 0.f;
-        for (int j = 0; j < per; ++j) s += sm.qs[c][g * per + j];
-        const __half sh = __float2half_rn(s);
-        const uint32_t h = __half_as_ushort(sh), l = __half_as_ushort(__float2half_rn(s - __half2float(sh)));
-        const int sft = 16 * (g & 1);
-        if (g < 2) { z[0] |= h << sft; z[2] |= h << sft; z[4] |= l << sft; }
-        else { z[1] |= h << sft; z[3] |= h << sft; z[5] |= l << sft; }
-      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g < ng) {
+          float s = 0.f;
+          for (int j = 0; j < per; ++j) s += sm.qs[c][g * per + j];
+          const __half sh = __float2half_rn(s);
+          const uint32_t h = __half_as_ushort(sh), l = __half_as_ushort(__float2half_rn(s - __half2float(sh)));
+          z[g >> 1] |= h << (16 * (g & 1));
+          z[2 + (g >> 1)] |= h << (16 * (g & 1));
+          z[4 + (g >> 1)] |= l << (16 * (g & 1));
+        }
       uint8_t* d = sm.qz + (c >> 3) * 128 + (c & 7) * 16;
       *reinterpret_cast<uint4*>(d) = make_uint4(z[0], z[1], z[2], z[3]);
       *reinterpret_cast<uint4*>(d + 16 * N) = make_uint4(z[4], z[5], z[6], z[7]);
-      uint64_t mk = 0;
-      if (c < ncols) mk = a.mask[w.b * a.mask_sb + (col0 + c) / a.c.g];
-      sm.colmask[c] = mk;
+      sm.colmask[c] = c < ncols ? a.mask[w.b * a.mask_sb + (col0 + c) / a.c.g] : 0;
       sm.m[c] = kUnset;
     }
     fence_async_smem();  // the tensor cores read q
@@ -631,67 +763,83 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (lane == 0) mbar_arrive(&sm.q_ready);
 
     const float sl2 = a.scale_log2 * kOperandScale;
-    const uint32_t id_pv = idesc(N, true, true);
     float l[kMaxCols];
 #pragma unroll
     for (int c = 0; c < kMaxCols; ++c) l[c] = 0.f;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
-      const int t = i * kTile + tid;          // this thread's position
-      const bool whole = (i + 1) * kTile <= len;  // every position is context
-      const bool ctx = t < len;
-      const int j = ctx || t >= len + a.n_q ? 0 : t - len;
-      const bool draft = !ctx && t < len + a.n_q;
+      const int t = i * kTile + tid;  // this thread's position
+      // bit c: column c attends it
+      uint64_t sees = t < len ? ~0ull : 0ull;
+      const bool whole = (i + 1) * kTile <= len;
+      if (t >= len && t < len + a.n_q) {
+#pragma unroll 1
+        for (int c = 0; c < N; ++c) sees |= ((sm.colmask[c] >> (t - len)) & 1) << c;
+      }
       const uint32_t sb = tm + lanes + kTmS + buf * kTmSStride;
       wait_for(a, sm, &sm.s_full[buf], (n >> 1) & 1);
       tc_fence_after();
-      float x[kMaxCols];
-      // x = score - reference, log2 units; -inf where this position is not attended
-      auto scores = [&](bool relative) {
+      // scores (log2 units, relative to the references if rel) of 16 columns
+      auto rel16 = [&](const uint32_t (&s)[16], int c0, float (&x)[16]) {
 #pragma unroll
-        for (int c0 = 0; c0 < kMaxCols; c0 += 16)
-          if (c0 < N) {
-            uint32_t s[16];
-            tmem_ld16(sb + c0, s);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 mm = relative ? *reinterpret_cast<const float4*>(&sm.m[c0 + k]) : make_float4(0.f, 0.f, 0.f, 0.f);
-              x[c0 + k] = fmaf(__uint_as_float(s[k]), sl2, -mm.x);
-              x[c0 + k + 1] = fmaf(__uint_as_float(s[k + 1]), sl2, -mm.y);
-              x[c0 + k + 2] = fmaf(__uint_as_float(s[k + 2]), sl2, -mm.z);
-              x[c0 + k + 3] = fmaf(__uint_as_float(s[k + 3]), sl2, -mm.w);
-            }
-            if (!whole) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (!(ctx || (draft && ((sm.colmask[c0 + k] >> j) & 1)))) x[c0 + k] = -INFINITY;
-            }
-          }
-      };
-      scores(true);
-      float top = -INFINITY;
-#pragma unroll
-      for (int c0 = 0; c0 < kMaxCols; c0 += 16)
-        if (c0 < N) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) top = fmaxf(top, x[c0 + k]);
+        for (int k = 0; k < 16; k += 4) {
+          const float4 mm = *reinterpret_cast<const float4*>(&sm.m[c0 + k]);
+          x[k] = fmaf(__uint_as_float(s[k]), sl2, -mm.x);
+          x[k + 1] = fmaf(__uint_as_float(s[k + 1]), sl2, -mm.y);
+          x[k + 2] = fmaf(__uint_as_float(s[k + 2]), sl2, -mm.z);
+          x[k + 3] = fmaf(__uint_as_float(s[k + 3]), sl2, -mm.w);
         }
-      if (bar_or(1, 128, top > kMaxGrowth)) {
-        // some column's reference is too low (or unset): move the references
-        // of the columns that need it to their maximum over this tile
-        if (tid < kMaxCols) sm.top[tid] = 0u;
-        named_bar(1, 128);
-        scores(false);
+      };
+      auto hide16 = [&](int c0, float (&x)[16]) {
+        const uint32_t b = static_cast<uint32_t>(sees >> c0);
 #pragma unroll
-        for (int c = 0; c < kMaxCols; ++c)
-          if (c < N) {
-            const uint32_t k = __reduce_max_sync(0xffffffffu, order_of(x[c]));
-            if (lane == 0) atomicMax(&sm.top[c], k);
+        for (int k = 0; k < 16; ++k)
+          if (!((b >> k) & 1)) x[k] = -INFINITY;
+      };
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c0 = 0; c0 < N; c0 += 16) {
+        uint32_t s[16];
+        float x[16];
+        tmem_ld16(sb + c0, s);
+        tmem_ld_wait();
+        rel16(s, c0, x);
+        if (!whole) hide16(c0, x);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, x[k]);
+      }
+      if (bar_or(1, 128, top > kMaxGrowth)) {
+        // Some column's reference is too low (or unset): the columns that
+        // need it take their maximum over this tile.
+#pragma unroll 1
+        for (int c0 = 0; c0 < N; c0 += 16) {
+          uint32_t s[16];
+          float x[16];
+          tmem_ld16(sb + c0, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]) * sl2;
+          if (!whole) hide16(c0, x);
+          // maxima over the lanes of 16 columns: halve the columns a lane
+          // holds four times; lane bits 4 .. 1 end up naming the column
+#pragma unroll
+          for (int h = 8; h > 0; h >>= 1) {
+            const bool up = lane & (2 * h);
+#pragma unroll
+            for (int k = 0; k < h; ++k) {
+              const float give = up ? x[k] : x[k + h];
+              const float got = __shfl_xor_sync(0xffffffffu, give, 2 * h);
+              x[k] = fmaxf(up ? x[k + h] : x[k], got);
+            }
           }
+          x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
+          if (!(lane & 1)) sm.lsum[warp][c0 + (lane >> 1)] = x[0];
+        }
         named_bar(1, 128);
         if (tid < N) {
-          const float v = value_of(sm.top[tid]), old = sm.m[tid];
+          const float v = fmaxf(fmaxf(sm.lsum[0][tid], sm.lsum[1][tid]), fmaxf(sm.lsum[2][tid], sm.lsum[3][tid]));
+          const float old = sm.m[tid];
           const bool move = v > old + kMaxGrowth;
           sm.fac[tid] = move ? ex2(old - v) : 1.f;
           if (move) sm.m[tid] = v;
@@ -710,44 +858,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             tmem_st16(tm + lanes + kTmO + c0, o);
           }
           tmem_st_wait();
-        }
 #pragma unroll
-        for (int c = 0; c < kMaxCols; ++c)
-          if (c < N) l[c] *= sm.fac[c];
-        scores(true);
+          for (int c = 0; c < kMaxCols; ++c)
+            if (c < N) l[c] *= sm.fac[c];
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_free[buf]);
       if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);  // P's buffer is free
       uint8_t* pt = sm.pt[buf] + (tid >> 3) * (16 * N) + (tid & 7) * 16;
+      uint32_t s[2][16];
+      tmem_ld16(sb, s[0]);
 #pragma unroll
-      for (int c0 = 0; c0 < kMaxCols; c0 += 8)
+      for (int c0 = 0; c0 < kMaxCols; c0 += 16)
         if (c0 < N) {
-          uint32_t y[4];
+          const int cur = (c0 >> 4) & 1;
+          float x[16];
+          tmem_ld_wait();
+          if (c0 + 16 < N) {
+            tmem_ld16(sb + c0 + 16, s[cur ^ 1]);
+          } else {  // S is read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+          }
+          rel16(s[cur], c0, x);
+          if (!whole) hide16(c0, x);
+          uint32_t y[8];
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
-            const float p0 = ex2(x[c0 + k]), p1 = ex2(x[c0 + k + 1]);
+          for (int k = 0; k < 16; k += 2) {
+            const float p0 = ex2(x[k]), p1 = ex2(x[k + 1]);
             l[c0 + k] += p0;
             l[c0 + k + 1] += p1;
             y[k >> 1] = pack_f16x2(p0, p1);
           }
           *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128 + 128) = make_uint4(y[4], y[5], y[6], y[7]);
         }
       fence_async_smem();
       tc_fence_before();
-      named_bar(1, 128);
-      if (tid == 0) {  // ---- PV of tile i ----
-        wait_for(a, sm, &sm.v_full[buf], (n >> 1) & 1);
-        tc_fence_after();
-        const uint32_t va = smem_u32(sm.vt[buf]), pa = smem_u32(sm.pt[buf]), lbo = 16 * N;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_ss(tm + kTmO, umma_sdesc(va + ks * 4096, 2048, 128), umma_sdesc(pa + ks * 2 * lbo, lbo, 128), id_pv,
-                  n > 0 || ks > 0);
-        umma_commit(&sm.pv_done[buf]);
-      }
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[buf]);
     }
     // ---- the column sums over the lanes, then the outputs (thread = d) ----
     const int nd = i1 - i0;
@@ -755,13 +904,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       wait_for(a, sm, &sm.pv_done[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
       tc_fence_after();
     }
+    named_bar(1, 128);  // lsum's last readers are done
 #pragma unroll
-    for (int c = 0; c < kMaxCols; ++c)
-      if (c < N) {
-        float s = l[c];
+    for (int c0 = 0; c0 < kMaxCols; c0 += 16)
+      if (c0 < N) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) sm.lsum[warp][c] = s;
+        for (int h = 8; h > 0; h >>= 1) {
+          const bool up = lane & (2 * h);
+#pragma unroll
+          for (int k = 0; k < h; ++k) {
+            const float give = up ? l[c0 + k] : l[c0 + k + h];
+            const float got = __shfl_xor_sync(0xffffffffu, give, 2 * h);
+            l[c0 + k] = (up ? l[c0 + k + h] : l[c0 + k]) + got;
+          }
+        }
+        const float s = l[c0] + __shfl_xor_sync(0xffffffffu, l[c0], 1);
+        if (!(lane & 1)) sm.lsum[warp][c0 + (lane >> 1)] = s;
       }
     named_bar(1, 128);
     const bool bad = sm.abort != 0;
@@ -781,25 +939,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       for (int k = 0; k < 16; ++k) {
         const int c = c0 + k;
         if (c >= ncols) break;
-        const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
-        const float M = bad ? nan : (L > 0.f ? sm.m[c] : -INFINITY);
         if (w.S > 1) {
           slot[c * kD + tid] = __uint_as_float(o[k]);
-          if (tid < 2) slot[N * kD + 2 * c + tid] = tid ? L : M;
         } else {
+          const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
           const int cg = col0 + c, tok = cg / a.c.g;
           const int64_t row = (static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g);
           const float inv = bad ? nan : (L > 0.f ? 1.f / L : 0.f);
           a.out[row * kD + tid] = f32_to_bf16_bits(__uint_as_float(o[k]) * inv);
-          if (tid == 0 && a.lse) a.lse[row] = bad ? nan : 0.69314718055994531f * (M + log2f(L));
         }
+      }
+    }
+    if (tid < ncols) {
+      const int c = tid, cg = col0 + c, tok = cg / a.c.g;
+      const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
+      const float M = bad ? nan : (L > 0.f ? sm.m[c] : -INFINITY);
+      if (w.S > 1) {
+        *reinterpret_cast<float2*>(slot + N * kD + 2 * c) = make_float2(M, L);
+      } else if (a.lse) {
+        a.lse[(static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g)] =
+            bad ? nan : 0.69314718055994531f * (M + log2f(L));
       }
     }
     tc_fence_before();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tm, kTmCols);
   }
