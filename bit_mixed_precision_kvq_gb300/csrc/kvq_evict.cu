@@ -43,6 +43,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 struct SelectSmem {
   uint32_t hist[256];
   uint32_t scan[kSelWarps][2];
+  uint32_t count[kSelThreads];  // (round, warp): kept above the threshold | equal to it << 16
+  uint2 start[kSelThreads];
   uint32_t prefix, want, equal;  // threshold so far; how many of its bin are wanted
 };
 
@@ -131,6 +133,127 @@ __device__ void write_kept(SelectSmem& sm, const float* x, int n, int pos0, uint
   }
 }
 
+// Selection with the keys in registers: thread k holds x[k + 1024 r], r < R.
+// The threshold is found bit by bit from the highest bit in which the keys
+// differ; a step counts the keys at or above a candidate (two instructions a
+// key, a warp sum, one barrier) and stops once exactly `want` are.  Against
+// the histogram form above this has no atomics, which a few crowded exponents
+// serialise, and reads the masses once.
+template <int R>
+__device__ void select_in_registers(SelectSmem& sm, const float* x, int n, int want, int pos0, int32_t* out, float* xout) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t key[R];
+  uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = tid + kSelThreads * r;
+    // a slot past the end is never counted: 0 is below every candidate
+    key[r] = i < n ? order_key(__ldcg(x + i)) : 0u;
+    if (i < n) {
+      lo = min(lo, key[r]);
+      hi = max(hi, key[r]);
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    sm.scan[warp][0] = lo;
+    sm.scan[warp][1] = hi;
+  }
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, sm.scan[lane][0]);
+  hi = __reduce_max_sync(0xffffffffu, sm.scan[lane][1]);
+  // T: the largest value that at least `want` keys reach; above: keys past T
+  uint32_t T = lo, above = 0;
+  bool exact = false;
+  if (lo != hi) {
+    const int top = 31 - __clz(lo ^ hi);
+    T = top == 31 ? 0u : (lo >> (top + 1)) << (top + 1);
+#pragma unroll 1
+    for (int bit = top; bit >= 0 && !exact; --bit) {
+      const uint32_t cand = T | (1u << bit);
+      uint32_t c = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) c += key[r] >= cand;
+      c = __reduce_add_sync(0xffffffffu, c);
+      uint32_t* row = sm.hist + 32 * (bit & 1);  // two rows: one barrier a step
+      if (lane == 0) row[warp] = c;
+      __syncthreads();
+      c = __reduce_add_sync(0xffffffffu, row[lane]);
+      if (c >= static_cast<uint32_t>(want)) {
+        T = cand;
+        exact = c == static_cast<uint32_t>(want);
+      } else {
+        above = c;
+      }
+    }
+  }
+  const uint32_t ties = exact ? 0xffffffffu : want - above;  // keys equal to T that stay
+  // kept positions in order: counts of (round, warp), their scan, the writes
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool in = tid + kSelThreads * r < n;
+    const uint32_t gt = __ballot_sync(0xffffffffu, in && key[r] > T), eq = __ballot_sync(0xffffffffu, in && key[r] == T);
+    if (lane == 0) sm.count[r * kSelWarps + warp] = __popc(gt) | (__popc(eq) << 16);
+  }
+  __syncthreads();
+  {
+    // exclusive scan of R * 32 pairs (both counts stay below 2^16 for R <= 32)
+    const uint32_t own = tid < R * kSelWarps ? sm.count[tid] : 0u;
+    uint32_t g = own & 0xffffu, e = own >> 16;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t pg = __shfl_up_sync(0xffffffffu, g, o), pe = __shfl_up_sync(0xffffffffu, e, o);
+      if (lane >= o) {
+        g += pg;
+        e += pe;
+      }
+    }
+    if (lane == 31) {
+      sm.scan[warp][0] = g;
+      sm.scan[warp][1] = e;
+    }
+    __syncthreads();
+    const uint32_t g0 = __reduce_add_sync(0xffffffffu, lane < warp ? sm.scan[lane][0] : 0u);
+    const uint32_t e0 = __reduce_add_sync(0xffffffffu, lane < warp ? sm.scan[lane][1] : 0u);
+    if (tid < R * kSelWarps) sm.start[tid] = make_uint2(g0 + g - (own & 0xffffu), e0 + e - (own >> 16));
+  }
+  __syncthreads();
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = tid + kSelThreads * r;
+    const bool in = i < n;
+    const uint32_t gt = __ballot_sync(0xffffffffu, in && key[r] > T), eq = __ballot_sync(0xffffffffu, in && key[r] == T);
+    const uint2 at = sm.start[r * kSelWarps + warp];
+    const uint32_t e = at.y + __popc(eq & below);
+    if (in && (key[r] > T || (key[r] == T && e < ties))) {
+      const uint32_t o = at.x + __popc(gt & below) + min(e, ties);
+      out[o] = pos0 + i;
+      if (xout) xout[o] = __ldcg(x + i);
+    }
+  }
+}
+
+// The `want` largest of x[0, n), in order of position: out[i] = pos0 + index,
+// xout[i] = value (xout may be null).  Registers hold up to 32 keys a thread;
+// longer ranges are read anew in every pass.
+__device__ __forceinline__ void select_range(SelectSmem& sm, const float* x, int n, int want, int pos0, int32_t* out,
+                                             float* xout) {
+  if (n <= kSelThreads) {
+    select_in_registers<1>(sm, x, n, want, pos0, out, xout);
+  } else if (n <= 8 * kSelThreads) {
+    select_in_registers<8>(sm, x, n, want, pos0, out, xout);
+  } else if (n <= 32 * kSelThreads) {
+    select_in_registers<32>(sm, x, n, want, pos0, out, xout);
+  } else {
+    uint32_t ties;
+    const uint32_t thr = select_key(sm, x, n, want, &ties);
+    write_kept(sm, x, n, pos0, thr, ties, out, xout);
+  }
+}
+
 // CTA (b, h, part): part 0 the text prefix and the visual block, part 1 the
 // text behind it and the tails of keep and mass_dst.
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictArgs a) {
@@ -157,19 +280,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       if (y) y[i] = x[i];
     }
     if (d.Tv == 0) return;
-    uint32_t ties;
-    const uint32_t thr = select_key(sm, x + c.vs, c.Tv, d.Tv, &ties);
-    write_kept(sm, x + c.vs, c.Tv, c.vs, thr, ties, keep + c.vs, y ? y + c.vs : nullptr);
+    select_range(sm, x + c.vs, c.Tv, d.Tv, c.vs, keep + c.vs, y ? y + c.vs : nullptr);
     return;
   }
   const int n_suf = len - c.ve, room = min(n_suf, a.T_dst - d.ve);
   const int last = min(a.n_recent, n_suf);           // always kept
   const int pick = room - last, n_old = n_suf - last;  // pick of the n_old before them
-  if (pick > 0) {
-    uint32_t ties;
-    const uint32_t thr = select_key(sm, x + c.ve, n_old, pick, &ties);
-    write_kept(sm, x + c.ve, n_old, c.ve, thr, ties, keep + d.ve, y ? y + d.ve : nullptr);
-  }
+  if (pick > 0) select_range(sm, x + c.ve, n_old, pick, c.ve, keep + d.ve, y ? y + d.ve : nullptr);
   for (int i = threadIdx.x; i < last; i += kSelThreads) {
     const int t = len - last + i;
     keep[d.ve + pick + i] = t;
@@ -182,41 +299,72 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   if (h == 0 && threadIdx.x == 0 && a.new_len) a.new_len[b] = end;
 }
 
-// Copy w bytes (a multiple of 4) with the warp's lanes, 16 bytes at a time
-// where the row size allows.
-__device__ __forceinline__ void copy_row(uint8_t* dst, const uint8_t* src, int w, int lane) {
-  if (w % 16 == 0) {
-    if (lane < w / 16) reinterpret_cast<uint4*>(dst)[lane] = __ldcg(reinterpret_cast<const uint4*>(src) + lane);
-  } else if (lane < w / 4) {
-    reinterpret_cast<uint32_t*>(dst)[lane] = __ldcg(reinterpret_cast<const uint32_t*>(src) + lane);
+// The kept rows: a CTA per (sequence, KV head, 64 rows of the new cache).
+// Consecutive threads copy consecutive granules of the destination, so the
+// stores are whole lines and the loads are whole rows; a thread has up to
+// eight granules in flight.
+constexpr int kMoveRows = 64;
+constexpr int kMoveThreads = 128;
+constexpr int kMoveBatch = 8;
+
+// Rows [0, n) of w bytes at dst from the rows at[i] >= 0 of src, in granules
+// of T (w a multiple of its size).
+template <typename T>
+__device__ __forceinline__ void move_rows(uint8_t* dst, const uint8_t* src, int w, int n, const int32_t* at) {
+  const int per = w / static_cast<int>(sizeof(T));  // a power of two
+  const int sh = 31 - __clz(per), total = n << sh;
+  for (int x0 = threadIdx.x; x0 < total; x0 += kMoveThreads * kMoveBatch) {
+    T v[kMoveBatch];
+    bool ok[kMoveBatch];
+#pragma unroll
+    for (int k = 0; k < kMoveBatch; ++k) {
+      const int x = x0 + kMoveThreads * k;
+      const int row = x < total ? at[x >> sh] : -1;
+      ok[k] = row >= 0;
+      if (ok[k]) v[k] = __ldcg(reinterpret_cast<const T*>(src + static_cast<int64_t>(row) * w) + (x & (per - 1)));
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveBatch; ++k)
+      if (ok[k]) reinterpret_cast<T*>(dst)[x0 + kMoveThreads * k] = v[k];
   }
 }
+__device__ __forceinline__ void move_sz(uint8_t* dst, const uint8_t* src, int w, int n, const int32_t* at) {
+  if (w == 16) move_rows<uint4>(dst, src, w, n, at);
+  else if (w == 8) move_rows<uint2>(dst, src, w, n, at);
+  else move_rows<uint32_t>(dst, src, w, n, at);
+}
 
-// A warp per kept row.
-constexpr int kMoveWarps = 8;
-__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ int32_t at[2][kMoveRows];  // source rows: visual, text (-1: none)
   const Geom &c = a.c, &d = a.d;
-  const int lane = threadIdx.x & 31;
-  pdl_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(c.B) * c.Hkv * a.T_dst) return;
-  const int t = a.keep[row];
-  if (t < 0) return;
-  const int64_t bh = row / a.T_dst;
-  const int i = static_cast<int>(row - bh * a.T_dst);
+  const int chunks = (a.T_dst + kMoveRows - 1) / kMoveRows;
+  const int64_t bh = blockIdx.x / chunks;
+  const int i0 = static_cast<int>(blockIdx.x - bh * chunks) * kMoveRows, n = min(kMoveRows, a.T_dst - i0);
   const int b = static_cast<int>(bh / c.Hkv), h = static_cast<int>(bh - static_cast<int64_t>(b) * c.Hkv);
+  // Rows [i0, i0 + n) of the new cache: text rows [t0, t1) (the prefix and
+  // the text behind the visual block are neighbours) and visual rows [v0, v1).
+  const int v0 = max(0, min(i0, d.ve) - d.vs), v1 = max(0, min(i0 + n, d.ve) - d.vs);
+  const int t0 = i0 <= d.vs ? i0 : max(d.vs, i0 - d.Tv), t1 = i0 + n <= d.vs ? i0 + n : max(d.vs, i0 + n - d.Tv);
+  pdl_wait();
+  if (threadIdx.x < static_cast<unsigned>(n)) {
+    const int i = i0 + threadIdx.x, t = a.keep[bh * a.T_dst + i];
+    if (i >= d.vs && i < d.ve) at[0][i - d.vs - v0] = t < 0 ? -1 : t - c.vs;
+    else at[1][(i < d.vs ? i : i - d.Tv) - t0] = t < c.ve ? t : t - c.Tv;  // -1 stays -1
+  }
+  __syncthreads();
   const HeadRows s = head_rows(c, b, h), r = head_rows(d, b, h);
-  if (i >= d.vs && i < d.ve) {
-    const int64_t x = t - c.vs, y = i - d.vs;
-    const int kw = s.k_packed ? c.krow : kRowBytes, vw = s.v_packed ? c.vrow : kRowBytes;
-    copy_row(r.vis_k + y * kw, s.vis_k + x * kw, kw, lane);
-    copy_row(r.vis_v + y * vw, s.vis_v + x * vw, vw, lane);
-    if (s.k_packed) copy_row(r.vis_ksz + y * c.kszrow, s.vis_ksz + x * c.kszrow, c.kszrow, lane);
-    if (s.v_packed) copy_row(r.vis_vsz + y * c.vszrow, s.vis_vsz + x * c.vszrow, c.vszrow, lane);
-  } else {
-    const int64_t x = t < c.vs ? t : t - c.Tv, y = i < d.vs ? i : i - d.Tv;
-    copy_row(r.text_k + y * kRowBytes, s.text_k + x * kRowBytes, kRowBytes, lane);
-    copy_row(r.text_v + y * kRowBytes, s.text_v + x * kRowBytes, kRowBytes, lane);
+  if (v1 > v0) {
+    const int kw = s.k_packed ? c.krow : kRowBytes, vw = s.v_packed ? c.vrow : kRowBytes, m = v1 - v0;
+    const int64_t o = v0;
+    move_rows<uint4>(r.vis_k + o * kw, s.vis_k, kw, m, at[0]);
+    move_rows<uint4>(r.vis_v + o * vw, s.vis_v, vw, m, at[0]);
+    if (s.k_packed) move_sz(r.vis_ksz + o * c.kszrow, s.vis_ksz, c.kszrow, m, at[0]);
+    if (s.v_packed) move_sz(r.vis_vsz + o * c.vszrow, s.vis_vsz, c.vszrow, m, at[0]);
+  }
+  if (t1 > t0) {
+    const int64_t o = static_cast<int64_t>(t0) * kRowBytes;
+    move_rows<uint4>(r.text_k + o, s.text_k, kRowBytes, t1 - t0, at[1]);
+    move_rows<uint4>(r.text_v + o, s.text_v, kRowBytes, t1 - t0, at[1]);
   }
 }
 
@@ -251,7 +399,7 @@ extern "C" kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, co
       kvq::ranges_meet(mass, 4 * bh * s.T_cap, mass_dst, 4 * bh * d.T_cap) ||
       kvq::ranges_meet(new_len, 4 * static_cast<int64_t>(s.B), seq_len, 4 * static_cast<int64_t>(s.B)))
     return KVQ_ERR_INVALID_ARG;
-  const int64_t blocks = (bh * T_dst + kvq::kMoveWarps - 1) / kvq::kMoveWarps;
+  const int64_t blocks = bh * ((T_dst + kvq::kMoveRows - 1) / kvq::kMoveRows);
   if (blocks > 0x7fffffffLL || 2 * bh > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   kvq::EvictArgs a;
   kvq::fill_geom(L, cache, &a.c);
@@ -268,5 +416,5 @@ extern "C" kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, co
                              kvq::kSelThreads, 0, stream, &a);
   if (st != KVQ_OK) return st;
   return kvq::launch_dependent(reinterpret_cast<const void*>(&kvq::move_kernel), dim3(static_cast<unsigned>(blocks)),
-                               kvq::kMoveWarps * 32, 0, stream, &a);
+                               kvq::kMoveThreads, 0, stream, &a);
 }

@@ -118,4 +118,11 @@ __device__ __forceinline__ HeadRows head_rows(const Geom& p, int b, int h) {
   return r;
 }
 
+// Bulk prefetch into L2 of the bytes at p, in whole 16-byte granules.
+__device__ __forceinline__ void prefetch_bytes(const void* p, uint32_t bytes) {
+  const uint64_t p0 = reinterpret_cast<uint64_t>(p) & ~15ull;
+  const uint64_t p1 = (reinterpret_cast<uint64_t>(p) + bytes + 15) & ~15ull;
+  prefetch_l2(reinterpret_cast<const void*>(p0), static_cast<uint32_t>(p1 - p0));
+}
+
 }  // namespace kvq

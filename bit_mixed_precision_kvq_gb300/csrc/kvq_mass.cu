@@ -33,7 +33,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRows = 16;        // positions of a block
 constexpr int kMaxTiles = 8;     // 8-column tiles handled in one pass over the rows
-constexpr int kCtasPerSm = 3;    // resident CTAs (registers)
+constexpr int kCtasPerSm = 2;    // resident CTAs (registers)
+constexpr int kAhead = 4;        // blocks of a warp that its L2 prefetch runs ahead
 
 struct MassArgs {
   Geom c;
@@ -252,6 +253,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
   };
   const int64_t base = (static_cast<int64_t>(b) * p.Hkv + h) * p.T_cap;
   const int cols = p.g * n;
+  // a block's rows into L2, ahead of the loads (one lane)
+  auto prefetch = [&](int i) {
+    if (i >= last) return;
+    const Block x = block(i);
+    prefetch_bytes(x.row, x.n * (x.packed ? p.krow : kRowBytes));
+    if (x.packed) prefetch_bytes(x.sz, x.n * p.kszrow);
+    if (a.mass_in) prefetch_bytes(a.mass_in + base + x.t0, 4 * x.n);
+  };
+  if (lane == 0)
+    for (int k = 0; k < kAhead; ++k) prefetch(first + warp + k * kWarps);
   // one pass over the rows for every 64 columns (at least one: the decay)
   for (int col0 = 0; col0 == 0 || col0 < cols; col0 += 8 * kMaxTiles) {
     const int tiles = min(kMaxTiles, (cols - col0 + 7) / 8);
@@ -267,22 +278,25 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
         }
       }
     };
+    // the mass that the block's sum is added to: lanes tig 0 have row gid, tig 1 row gid + 8
+    const int my = tig == 0 ? gid : gid + 8;
+    auto fetch_mass = [&](const Block& x) {
+      if (tig >= 2 || my >= x.n) return 0.f;
+      if (col0 > 0) return a.mass[base + x.t0 + my];
+      return a.mass_in ? a.decay * a.mass_in[base + x.t0 + my] : 0.f;
+    };
     Block cur;
+    float cur_mass = 0.f;
     if (first + warp < last) {
       cur = block(first + warp);
+      cur_mass = fetch_mass(cur);
       fetch(cur);
     }
 #pragma unroll 1
     for (int i = first + warp; i < last; i += kWarps) {
       const Block x = cur;
-      // the row whose mass this lane writes (tig 0: gid, tig 1: gid + 8)
-      const int my = tig == 0 ? gid : gid + 8;
-      const bool writes = tig < 2 && my < x.n;
-      float m_in = 0.f;
-      if (writes) {
-        if (col0 > 0) m_in = a.mass[base + x.t0 + my];
-        else if (a.mass_in) m_in = a.decay * a.mass_in[base + x.t0 + my];
-      }
+      const float m_in = cur_mass;
+      if (lane == 0 && col0 == 0) prefetch(i + kAhead * kWarps);
       const bool late = x.t0 + x.n > len - n + 1;  // some column does not reach the last rows
       float w0 = 0.f, w1 = 0.f;                    // weights of rows gid, gid + 8
       auto add = [&](int t, float (&S)[4]) {
@@ -307,6 +321,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
           const uint4 sz0 = r0.sz, sz1 = r1.sz;
           if (i + kWarps < last) {
             cur = block(i + kWarps);
+            cur_mass = fetch_mass(cur);
             fetch(cur);
           }
           uint32_t za = 0u, zc = 0u;  // z halves 2 (tig & 1), + 1
@@ -374,6 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
         }
         if (i + kWarps < last) {
           cur = block(i + kWarps);
+          cur_mass = fetch_mass(cur);
           fetch(cur);
         }
 #pragma unroll 1
@@ -397,7 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
       w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
       w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
       w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-      if (writes) a.mass[base + x.t0 + my] = m_in + (tig == 0 ? w0 : w1);
+      if (tig < 2 && my < x.n) a.mass[base + x.t0 + my] = m_in + (tig == 0 ? w0 : w1);
     }
   }
 }

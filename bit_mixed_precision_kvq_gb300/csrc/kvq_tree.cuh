@@ -425,22 +425,19 @@ __device__ __forceinline__ void k_scales(const uint4& sz, int G, uint32_t (&s2)[
   for (int P = 0; P < 4; ++P) s2[P] = hmul2_u(half_of(sz, ng + 32 * P / G) * 0x10001u, 0x38003800u);
 }
 
-// Bulk prefetch into L2 of rows [i, i + n) of w bytes (16-byte granules).
-__device__ __forceinline__ void prefetch_rows(const uint8_t* base, int64_t i, int n, int w) {
-  const uint64_t p0 = reinterpret_cast<uint64_t>(base + i * w) & ~15ull;
-  const uint64_t p1 = (reinterpret_cast<uint64_t>(base + (i + n) * w) + 15) & ~15ull;
-  prefetch_l2(reinterpret_cast<const void*>(p0), static_cast<uint32_t>(p1 - p0));
-}
 // The visual rows of tile i, K (key) or V: the bulk of a unit's bytes.
 __device__ __forceinline__ void prefetch_tile(const Geom& c, const HeadRows& r, int i, int len, bool key) {
   const int t0 = max(i * kTile, c.vs), t1 = min(min((i + 1) * kTile, c.ve), len);
   if (t0 >= t1) return;
+  const int64_t i0 = t0 - c.vs;
   if (key) {
-    prefetch_rows(r.vis_k, t0 - c.vs, t1 - t0, r.k_packed ? c.krow : kRowBytes);
-    if (r.k_packed) prefetch_rows(r.vis_ksz, t0 - c.vs, t1 - t0, c.kszrow);
+    const int w = r.k_packed ? c.krow : kRowBytes;
+    prefetch_bytes(r.vis_k + i0 * w, (t1 - t0) * w);
+    if (r.k_packed) prefetch_bytes(r.vis_ksz + i0 * c.kszrow, (t1 - t0) * c.kszrow);
   } else {
-    prefetch_rows(r.vis_v, t0 - c.vs, t1 - t0, r.v_packed ? c.vrow : kRowBytes);
-    if (r.v_packed) prefetch_rows(r.vis_vsz, t0 - c.vs, t1 - t0, c.vszrow);
+    const int w = r.v_packed ? c.vrow : kRowBytes;
+    prefetch_bytes(r.vis_v + i0 * w, (t1 - t0) * w);
+    if (r.v_packed) prefetch_bytes(r.vis_vsz + i0 * c.vszrow, (t1 - t0) * c.vszrow);
   }
 }
 
