@@ -11,6 +11,8 @@
 // copied as they are stored (codes, scales and zeros bit for bit).
 #include "kvq_geom.cuh"
 
+#include <algorithm>
+
 namespace kvq {
 namespace {
 
@@ -37,227 +39,231 @@ __device__ __forceinline__ int evict_len(const EvictArgs& a, int b) {
   return len >= a.c.ve && len <= a.T ? len : -1;
 }
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
+// ---- selection ------------------------------------------------------------------
+// A CTA per range of masses (the visual block, or the text behind it, of one
+// sequence and KV head).  The threshold -- the want-th largest key -- is
+// found in three passes of 11, 11 and 10 bits: a histogram in shared memory of
+// the keys that share the digits found so far, and the bin in which the count
+// from above reaches `want`.  11 bits spread the exponents of real masses over
+// enough bins that the shared-memory atomics do not queue; a warp whose keys
+// all fall into one bin (ties, zeros) adds once.
+constexpr int kBins = 2048;
 
+template <int NT>
 struct SelectSmem {
-  uint32_t hist[256];
-  uint32_t scan[kSelWarps][2];
-  uint32_t count[kSelThreads];  // (round, warp): kept above the threshold | equal to it << 16
-  uint2 start[kSelThreads];
-  uint32_t prefix, want, equal;  // threshold so far; how many of its bin are wanted
+  uint32_t hist[kBins];
+  uint32_t scan[NT / 32][2];
+  uint32_t count[1024];  // (round, warp): kept above the threshold | equal to it << 16
+  uint2 start[1024];
+  uint32_t digit, want;
 };
 
-// The want-th largest key of x[0, n) (1 <= want <= n), 8 bits a pass: the
-// histogram of the keys that share the prefix found so far, and the bin in
-// which the count from above reaches `want`.  Returns the key; *ties gets how
-// many keys equal to it belong to the want largest.
-__device__ uint32_t select_key(SelectSmem& sm, const float* x, int n, int want, uint32_t* ties) {
-  if (threadIdx.x == 0) {
-    sm.prefix = 0;
-    sm.want = want;
-  }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) sm.hist[threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t prefix = sm.prefix, high = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
-      const uint32_t k = order_key(x[i]);
-      if ((k & high) == prefix) atomicAdd(&sm.hist[(k >> shift) & 255], 1u);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {  // lane l: bins 255 - 8l .. 248 - 8l, counted from above
-      uint32_t own = 0;
-      for (int k = 0; k < 8; ++k) own += sm.hist[255 - 8 * threadIdx.x - k];
-      uint32_t incl = own;
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (threadIdx.x >= static_cast<unsigned>(o)) incl += y;
-      }
-      const uint32_t w = sm.want, above = incl - own;
-      __syncwarp();
-      if (above < w && w <= incl) {
-        uint32_t left = w - above;
-        int bin = 255 - 8 * threadIdx.x;
-        while (left > sm.hist[bin]) left -= sm.hist[bin--];
-        sm.prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-        sm.want = left;
-      }
-    }
-    __syncthreads();
-  }
-  *ties = sm.want;
-  return sm.prefix;
-}
-
-// Positions of x[0, n) with key above `thr`, and the first `ties` equal to
-// it, in order: out[i] = pos0 + index, xout[i] = value (xout may be null).
-// A warp takes a span of n / 32 values, counts, and after a scan over the
-// warps writes.
-__device__ void write_kept(SelectSmem& sm, const float* x, int n, int pos0, uint32_t thr, uint32_t ties, int32_t* out,
-                           float* xout) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int span = (n + kSelWarps - 1) / kSelWarps;
-  const int i0 = min(n, warp * span), i1 = min(n, i0 + span);
-  uint32_t gt = 0, eq = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t k = order_key(x[i]);
-    gt += k > thr;
-    eq += k == thr;
-  }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  __syncthreads();
-  if (lane == 0) {
-    sm.scan[warp][0] = gt;
-    sm.scan[warp][1] = eq;
-  }
-  __syncthreads();
-  uint32_t g0 = lane < warp ? sm.scan[lane][0] : 0, e0 = lane < warp ? sm.scan[lane][1] : 0;
-  g0 = __reduce_add_sync(0xffffffffu, g0);
-  e0 = __reduce_add_sync(0xffffffffu, e0);
-  const uint32_t below = (1u << lane) - 1u;
-  for (int base = i0; base < i1; base += 32) {
-    const int i = base + lane;
-    const float v = i < i1 ? x[i] : 0.f;
-    const uint32_t k = order_key(v);
-    const uint32_t mg = __ballot_sync(0xffffffffu, i < i1 && k > thr), me = __ballot_sync(0xffffffffu, i < i1 && k == thr);
-    const uint32_t e = e0 + __popc(me & below);
-    if (i < i1 && (k > thr || (k == thr && e < ties))) {
-      const uint32_t at = g0 + __popc(mg & below) + min(e, ties);
-      out[at] = pos0 + i;
-      if (xout) xout[at] = v;
-    }
-    g0 += __popc(mg);
-    e0 += __popc(me);
+__device__ __forceinline__ void hist_add(uint32_t* hist, uint32_t bin, bool in) {
+  const uint32_t who = __ballot_sync(0xffffffffu, in);
+  if (who == 0) return;
+  const int leader = __ffs(who) - 1;
+  const uint32_t b0 = __shfl_sync(0xffffffffu, bin, leader);
+  if (__all_sync(0xffffffffu, !in || bin == b0)) {
+    if ((threadIdx.x & 31) == leader) atomicAdd(&hist[b0], __popc(who));
+  } else if (in) {
+    atomicAdd(&hist[bin], 1u);
   }
 }
 
-// Selection with the keys in registers: thread k holds x[k + 1024 r], r < R.
-// The threshold is found bit by bit from the highest bit in which the keys
-// differ; a step counts the keys at or above a candidate (two instructions a
-// key, a warp sum, one barrier) and stops once exactly `want` are.  Against
-// the histogram form above this has no atomics, which a few crowded exponents
-// serialise, and reads the masses once.
-template <int R>
-__device__ void select_in_registers(SelectSmem& sm, const float* x, int n, int want, int pos0, int32_t* out, float* xout) {
+// The bin in which the count from the highest one down reaches sm.want;
+// sm.want becomes what is wanted of that bin.  Thread k has the kBins / NT
+// bins below kBins - k (kBins / NT).
+template <int NT>
+__device__ __forceinline__ void find_bin(SelectSmem<NT>& sm) {
+  constexpr int PER = kBins / NT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t own = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) own += sm.hist[kBins - 1 - tid * PER - k];
+  uint32_t incl = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sm.scan[warp][0] = incl;
+  const uint32_t want = sm.want;
+  __syncthreads();
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp && lane < NT / 32 ? sm.scan[lane][0] : 0u);
+  uint32_t above = before + incl - own;
+  if (above < want && want <= above + own) {
+    int bin = kBins - 1 - tid * PER;
+    while (above + sm.hist[bin] < want) above += sm.hist[bin--];
+    sm.digit = bin;
+    sm.want = want - above;
+  }
+  __syncthreads();
+}
+
+// load(f) calls f(key, there is one) for every key of the thread, all threads
+// the same number of times.
+template <int NT, typename F>
+__device__ __forceinline__ uint32_t find_threshold(SelectSmem<NT>& sm, int want, F&& load) {
+  const int tid = threadIdx.x;
+  if (tid == 0) sm.want = want;
+  uint32_t prefix = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    const uint32_t high = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
+    for (int k = tid; k < kBins; k += NT) sm.hist[k] = 0;
+    __syncthreads();
+    load([&](uint32_t key, bool in) { hist_add(sm.hist, (key >> shift) & mask, in && (key & high) == prefix); });
+    __syncthreads();
+    find_bin(sm);
+    prefix |= sm.digit << shift;
+  }
+  return prefix;
+}
+
+// Kept: keys above T and the first sm.want equal to it.  Counts of (round,
+// warp) pairs, their exclusive scan, and the writes, in order of position.
+template <int NT, int R>
+__device__ void select_in_registers(SelectSmem<NT>& sm, const float* x, int n, int want, int pos0, int32_t* out,
+                                    float* xout) {
+  static_assert(NT / 32 * R <= 1024, "one count per (round, warp)");
+  constexpr int NW = NT / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t key[R];
-  uint32_t lo = 0xffffffffu, hi = 0u;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = tid + kSelThreads * r;
-    // a slot past the end is never counted: 0 is below every candidate
+    const int i = tid + NT * r;
     key[r] = i < n ? order_key(__ldcg(x + i)) : 0u;
-    if (i < n) {
-      lo = min(lo, key[r]);
-      hi = max(hi, key[r]);
-    }
   }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    sm.scan[warp][0] = lo;
-    sm.scan[warp][1] = hi;
-  }
-  __syncthreads();
-  lo = __reduce_min_sync(0xffffffffu, sm.scan[lane][0]);
-  hi = __reduce_max_sync(0xffffffffu, sm.scan[lane][1]);
-  // T: the largest value that at least `want` keys reach; above: keys past T
-  uint32_t T = lo, above = 0;
-  bool exact = false;
-  if (lo != hi) {
-    const int top = 31 - __clz(lo ^ hi);
-    T = top == 31 ? 0u : (lo >> (top + 1)) << (top + 1);
-#pragma unroll 1
-    for (int bit = top; bit >= 0 && !exact; --bit) {
-      const uint32_t cand = T | (1u << bit);
-      uint32_t c = 0;
+  const uint32_t T = find_threshold<NT>(sm, want, [&](auto&& f) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) c += key[r] >= cand;
-      c = __reduce_add_sync(0xffffffffu, c);
-      uint32_t* row = sm.hist + 32 * (bit & 1);  // two rows: one barrier a step
-      if (lane == 0) row[warp] = c;
-      __syncthreads();
-      c = __reduce_add_sync(0xffffffffu, row[lane]);
-      if (c >= static_cast<uint32_t>(want)) {
-        T = cand;
-        exact = c == static_cast<uint32_t>(want);
-      } else {
-        above = c;
-      }
-    }
-  }
-  const uint32_t ties = exact ? 0xffffffffu : want - above;  // keys equal to T that stay
-  // kept positions in order: counts of (round, warp), their scan, the writes
-  __syncthreads();
+    for (int r = 0; r < R; ++r)
+      if (NT * r < n) f(key[r], tid + NT * r < n);
+  });
+  const uint32_t ties = sm.want;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const bool in = tid + kSelThreads * r < n;
+    const bool in = tid + NT * r < n;
     const uint32_t gt = __ballot_sync(0xffffffffu, in && key[r] > T), eq = __ballot_sync(0xffffffffu, in && key[r] == T);
-    if (lane == 0) sm.count[r * kSelWarps + warp] = __popc(gt) | (__popc(eq) << 16);
+    if (lane == 0) sm.count[r * NW + warp] = __popc(gt) | (__popc(eq) << 16);
   }
   __syncthreads();
-  {
-    // exclusive scan of R * 32 pairs (both counts stay below 2^16 for R <= 32)
-    const uint32_t own = tid < R * kSelWarps ? sm.count[tid] : 0u;
-    uint32_t g = own & 0xffffu, e = own >> 16;
+  // exclusive scan of the NW * R pairs, PER of them a thread
+  constexpr int PER = (NW * R + NT - 1) / NT;
+  uint32_t g = 0, e = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t pg = __shfl_up_sync(0xffffffffu, g, o), pe = __shfl_up_sync(0xffffffffu, e, o);
-      if (lane >= o) {
-        g += pg;
-        e += pe;
-      }
-    }
-    if (lane == 31) {
-      sm.scan[warp][0] = g;
-      sm.scan[warp][1] = e;
-    }
-    __syncthreads();
-    const uint32_t g0 = __reduce_add_sync(0xffffffffu, lane < warp ? sm.scan[lane][0] : 0u);
-    const uint32_t e0 = __reduce_add_sync(0xffffffffu, lane < warp ? sm.scan[lane][1] : 0u);
-    if (tid < R * kSelWarps) sm.start[tid] = make_uint2(g0 + g - (own & 0xffffu), e0 + e - (own >> 16));
+  for (int k = 0; k < PER; ++k) {
+    const uint32_t c = tid * PER + k < NW * R ? sm.count[tid * PER + k] : 0u;
+    g += c & 0xffffu;
+    e += c >> 16;
   }
+  uint32_t ig = g, ie = e;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t pg = __shfl_up_sync(0xffffffffu, ig, o), pe = __shfl_up_sync(0xffffffffu, ie, o);
+    if (lane >= o) {
+      ig += pg;
+      ie += pe;
+    }
+  }
+  if (lane == 31) {
+    sm.scan[warp][0] = ig;
+    sm.scan[warp][1] = ie;
+  }
+  __syncthreads();
+  const bool wl = lane < warp && lane < NW;
+  uint32_t g0 = __reduce_add_sync(0xffffffffu, wl ? sm.scan[lane][0] : 0u) + ig - g;
+  uint32_t e0 = __reduce_add_sync(0xffffffffu, wl ? sm.scan[lane][1] : 0u) + ie - e;
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+    if (tid * PER + k < NW * R) {
+      const uint32_t c = sm.count[tid * PER + k];
+      sm.start[tid * PER + k] = make_uint2(g0, e0);
+      g0 += c & 0xffffu;
+      e0 += c >> 16;
+    }
   __syncthreads();
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = tid + kSelThreads * r;
+    const int i = tid + NT * r;
     const bool in = i < n;
     const uint32_t gt = __ballot_sync(0xffffffffu, in && key[r] > T), eq = __ballot_sync(0xffffffffu, in && key[r] == T);
-    const uint2 at = sm.start[r * kSelWarps + warp];
-    const uint32_t e = at.y + __popc(eq & below);
-    if (in && (key[r] > T || (key[r] == T && e < ties))) {
-      const uint32_t o = at.x + __popc(gt & below) + min(e, ties);
+    const uint2 at = sm.start[r * NW + warp];
+    const uint32_t q = at.y + __popc(eq & below);
+    if (in && (key[r] > T || (key[r] == T && q < ties))) {
+      const uint32_t o = at.x + __popc(gt & below) + min(q, ties);
       out[o] = pos0 + i;
       if (xout) xout[o] = __ldcg(x + i);
     }
   }
 }
 
-// The `want` largest of x[0, n), in order of position: out[i] = pos0 + index,
-// xout[i] = value (xout may be null).  Registers hold up to 32 keys a thread;
-// longer ranges are read anew in every pass.
-__device__ __forceinline__ void select_range(SelectSmem& sm, const float* x, int n, int want, int pos0, int32_t* out,
-                                             float* xout) {
-  if (n <= kSelThreads) {
-    select_in_registers<1>(sm, x, n, want, pos0, out, xout);
-  } else if (n <= 8 * kSelThreads) {
-    select_in_registers<8>(sm, x, n, want, pos0, out, xout);
-  } else if (n <= 32 * kSelThreads) {
-    select_in_registers<32>(sm, x, n, want, pos0, out, xout);
-  } else {
-    uint32_t ties;
-    const uint32_t thr = select_key(sm, x, n, want, &ties);
-    write_kept(sm, x, n, pos0, thr, ties, out, xout);
+// Ranges that do not fit the registers: the masses are read anew in every
+// pass; a warp takes a contiguous span for the writes.
+template <int NT>
+__device__ void select_from_memory(SelectSmem<NT>& sm, const float* x, int n, int want, int pos0, int32_t* out,
+                                   float* xout) {
+  constexpr int NW = NT / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t T = find_threshold<NT>(sm, want, [&](auto&& f) {
+    for (int i0 = 0; i0 < n; i0 += NT) {
+      const int i = i0 + tid;
+      f(i < n ? order_key(__ldcg(x + i)) : 0u, i < n);
+    }
+  });
+  const uint32_t ties = sm.want;
+  const int span = (n + NW - 1) / NW;
+  const int i0 = min(n, warp * span), i1 = min(n, i0 + span);
+  uint32_t gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t k = order_key(__ldcg(x + i));
+    gt += k > T;
+    eq += k == T;
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    sm.scan[warp][0] = gt;
+    sm.scan[warp][1] = eq;
+  }
+  __syncthreads();
+  const bool wl = lane < warp && lane < NW;
+  uint32_t g0 = __reduce_add_sync(0xffffffffu, wl ? sm.scan[lane][0] : 0u);
+  uint32_t e0 = __reduce_add_sync(0xffffffffu, wl ? sm.scan[lane][1] : 0u);
+  const uint32_t below = (1u << lane) - 1u;
+  for (int base = i0; base < i1; base += 32) {
+    const int i = base + lane;
+    const float v = i < i1 ? __ldcg(x + i) : 0.f;
+    const uint32_t k = order_key(v);
+    const uint32_t mg = __ballot_sync(0xffffffffu, i < i1 && k > T), me = __ballot_sync(0xffffffffu, i < i1 && k == T);
+    const uint32_t q = e0 + __popc(me & below);
+    if (i < i1 && (k > T || (k == T && q < ties))) {
+      const uint32_t o = g0 + __popc(mg & below) + min(q, ties);
+      out[o] = pos0 + i;
+      if (xout) xout[o] = v;
+    }
+    g0 += __popc(mg);
+    e0 += __popc(me);
+  }
+}
+
+// The `want` largest of x[0, n), 1 <= want <= n, in order of position:
+// out[i] = pos0 + index, xout[i] = value (xout may be null).
+template <int NT>
+__device__ __forceinline__ void select_range(SelectSmem<NT>& sm, const float* x, int n, int want, int pos0, int32_t* out,
+                                             float* xout) {
+  if (n <= 4 * NT) select_in_registers<NT, 4>(sm, x, n, want, pos0, out, xout);
+  else if (n <= 32 * NT) select_in_registers<NT, 32>(sm, x, n, want, pos0, out, xout);
+  else select_from_memory(sm, x, n, want, pos0, out, xout);
 }
 
 // CTA (b, h, part): part 0 the text prefix and the visual block, part 1 the
 // text behind it and the tails of keep and mass_dst.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ SelectSmem sm;
+template <int NT>
+__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ SelectSmem<NT> sm;
   const Geom &c = a.c, &d = a.d;
   const int part = blockIdx.x & 1;
   const int64_t bh = blockIdx.x >> 1;
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   int32_t* keep = a.keep + bh * a.T_dst;
   if (len < 0) {
     if (part == 1) {
-      for (int i = threadIdx.x; i < a.T_dst; i += kSelThreads) keep[i] = -1;
+      for (int i = threadIdx.x; i < a.T_dst; i += NT) keep[i] = -1;
       if (h == 0 && threadIdx.x == 0 && a.new_len) a.new_len[b] = -1;
     }
     return;
@@ -275,27 +281,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   const float* x = a.mass + bh * c.T_cap;
   float* y = a.mass_dst ? a.mass_dst + bh * d.T_cap : nullptr;
   if (part == 0) {
-    for (int i = threadIdx.x; i < c.vs; i += kSelThreads) {
+    for (int i = threadIdx.x; i < c.vs; i += NT) {
       keep[i] = i;
       if (y) y[i] = x[i];
     }
-    if (d.Tv == 0) return;
-    select_range(sm, x + c.vs, c.Tv, d.Tv, c.vs, keep + c.vs, y ? y + c.vs : nullptr);
+    if (d.Tv > 0) select_range(sm, x + c.vs, c.Tv, d.Tv, c.vs, keep + c.vs, y ? y + c.vs : nullptr);
     return;
   }
   const int n_suf = len - c.ve, room = min(n_suf, a.T_dst - d.ve);
-  const int last = min(a.n_recent, n_suf);           // always kept
+  const int last = min(a.n_recent, n_suf);             // always kept
   const int pick = room - last, n_old = n_suf - last;  // pick of the n_old before them
   if (pick > 0) select_range(sm, x + c.ve, n_old, pick, c.ve, keep + d.ve, y ? y + d.ve : nullptr);
-  for (int i = threadIdx.x; i < last; i += kSelThreads) {
+  for (int i = threadIdx.x; i < last; i += NT) {
     const int t = len - last + i;
     keep[d.ve + pick + i] = t;
     if (y) y[d.ve + pick + i] = x[t];
   }
   const int end = d.ve + room;
-  for (int i = end + threadIdx.x; i < a.T_dst; i += kSelThreads) keep[i] = -1;
+  for (int i = end + threadIdx.x; i < a.T_dst; i += NT) keep[i] = -1;
   if (y)
-    for (int i = end + threadIdx.x; i < d.T_cap; i += kSelThreads) y[i] = 0.f;
+    for (int i = end + threadIdx.x; i < d.T_cap; i += NT) y[i] = 0.f;
   if (h == 0 && threadIdx.x == 0 && a.new_len) a.new_len[b] = end;
 }
 
@@ -412,8 +417,13 @@ extern "C" kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, co
   a.keep = keep;
   a.mass_dst = mass_dst;
   a.new_len = new_len;
-  st = kvq::launch_dependent(reinterpret_cast<const void*>(&kvq::select_kernel), dim3(static_cast<unsigned>(2 * bh)),
-                             kvq::kSelThreads, 0, stream, &a);
+  // Long ranges, or few of them: 1024 threads each; else 256, so that several
+  // share an SM.
+  const int longest = std::max(L->Tv, T - s.vis_end);
+  const bool wide = longest > 4 * 256;
+  st = kvq::launch_dependent(wide ? reinterpret_cast<const void*>(&kvq::select_kernel<1024>)
+                                  : reinterpret_cast<const void*>(&kvq::select_kernel<256>),
+                             dim3(static_cast<unsigned>(2 * bh)), wide ? 1024 : 256, 0, stream, &a);
   if (st != KVQ_OK) return st;
   return kvq::launch_dependent(reinterpret_cast<const void*>(&kvq::move_kernel), dim3(static_cast<unsigned>(blocks)),
                                kvq::kMoveThreads, 0, stream, &a);

@@ -45,12 +45,14 @@ struct MassArgs {
   float scale_log2, decay;
   const float* mass_in;  // [B][Hkv][T_cap] or null
   float* mass;
-  int32_t strips;                // CTAs per (sequence, KV head)
-  uint8_t head[KVQ_MAX_HEADS];   // heads, those with the longest rows first
+  // (sequence, KV head) pairs of class k (0 bf16 K rows, 1 packed) number U[k]
+  // and are split over S[k] CTAs each; heads of the classes in order in head[]
+  int32_t U[2], S[2], n_bf16;
+  uint8_t head[KVQ_MAX_HEADS];
 };
 
 struct MassSmem {
-  uint4 qh[kMaxTiles][4][32];   // fp16 operand: [tile][32-element block][lane]
+  uint4 qh[kMaxTiles][4][32];   // fp16 operand: [tile][32-element block][lane], see q_factor
   uint4 qb[kMaxTiles][4][32];   // bf16 operand
   uint32_t zb[kMaxTiles][32];   // group sums, high then low
   float2 lse2[kMaxTiles][4];    // lse in log2 units of columns 2 tig, 2 tig + 1
@@ -64,9 +66,35 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A code of block P sits at bit kKShift(P) of its half, i.e. is 2^(p - 24) c;
+// the fp16 query elements of the block carry 2^(p0 - p), p0 the smallest p, so
+// that the blocks of a group share one accumulator.  (|q| below 2^-8 may lose
+// bits of fp16's subnormal range: 2^-19 at most, 3e-7 of a score of unit keys.)
+template <int KB>
+__device__ __forceinline__ constexpr int k_first_shift() {
+  return KB == 2 ? 2 : 0;
+}
+template <int KB>
+__device__ __forceinline__ float q_factor(int P) {
+  const int p = KB == 2 ? 8 - 2 * P : (KB == 4 ? 4 * (P & 1) : 0);
+  return __int_as_float((127 + k_first_shift<KB>() - p) << 23);
+}
+
+// D = A * B (a fresh accumulator).
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // The columns [col0, col0 + 8 tiles) of (b, h): token k of the n taken is
 // column k g + j.  Columns that add nothing get q = 0 and lse = +inf.
-template <int G>
+template <int KB, int G>
 __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, int b, int h, int len, int n, int col0,
                                              int tiles) {
   const Geom& p = a.c;
@@ -89,7 +117,9 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
     sm.qb[t][P][lane] = r;
     const uint32_t y[4] = {bf16pair_f16(r.x, false, r.z, false), bf16pair_f16(r.x, true, r.z, true),
                            bf16pair_f16(r.y, false, r.w, false), bf16pair_f16(r.y, true, r.w, true)};
-    sm.qh[t][P][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+    const float f = q_factor<KB>(P);
+    const uint32_t f2 = pack_f16x2(f, f);
+    sm.qh[t][P][lane] = make_uint4(hmul2_u(y[0], f2), hmul2_u(y[1], f2), hmul2_u(y[2], f2), hmul2_u(y[3], f2));
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -133,13 +163,6 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
   }
   __syncthreads();
 }
-
-// A block of up to 16 positions of one kind.
-struct Block {
-  const uint8_t *row, *sz;  // first row
-  int t0, n;
-  bool packed;
-};
 
 template <int KB>
 struct RawRow {
@@ -218,8 +241,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
   constexpr int NG = kD / G;
   constexpr int PPG = G / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const int unit = blockIdx.x / a.strips, strip = blockIdx.x - unit * a.strips;
-  const int h = a.head[unit / p.B], b = unit - (unit / p.B) * p.B;
+  // the CTA's (sequence, KV head) and strip of its rows
+  int v = blockIdx.x, cls = 0;
+  if (v >= a.U[0] * a.S[0]) {
+    v -= a.U[0] * a.S[0];
+    cls = 1;
+  }
+  const int S = cls ? a.S[1] : a.S[0];
+  const int unit = v / S, strip = v - unit * S;
+  const int h = a.head[(cls ? a.n_bf16 : 0) + unit / p.B], b = unit - (unit / p.B) * p.B;
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();  // past the dependency wait; this kernel writes no cache row
   const int len = a.seq_len ? a.seq_len[b] : a.T;
@@ -230,191 +260,190 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
   const int n_pre = min(len, p.vs), n_vis = max(0, min(len, p.ve) - p.vs), n_suf = max(0, len - p.ve);
   const int b1 = (n_pre + kRows - 1) / kRows, b2 = b1 + (n_vis + kRows - 1) / kRows;
   const int nb = b2 + (n_suf + kRows - 1) / kRows;
-  const int first = static_cast<int>(static_cast<int64_t>(nb) * strip / a.strips);
-  const int last = static_cast<int>(static_cast<int64_t>(nb) * (strip + 1) / a.strips);
-  auto block = [&](int i) {
-    Block x;
-    x.sz = nullptr;
-    x.packed = false;
-    if (i >= b1 && i < b2) {
-      const int r = (i - b1) * kRows;
-      x.t0 = p.vs + r;
-      x.n = min(kRows, n_vis - r);
-      x.packed = hr.k_packed;
-      x.row = hr.vis_k + static_cast<int64_t>(r) * (hr.k_packed ? p.krow : kRowBytes);
-      if (hr.k_packed) x.sz = hr.vis_ksz + static_cast<int64_t>(r) * p.kszrow;
-    } else {
-      const int r = (i < b1 ? i : i - b2) * kRows;
-      x.t0 = i < b1 ? r : p.ve + r;
-      x.n = min(kRows, (i < b1 ? n_pre : n_suf) - r);
-      x.row = hr.text_k + static_cast<int64_t>(i < b1 ? r : p.vs + r) * kRowBytes;
-    }
-    return x;
-  };
+  const int first = static_cast<int>(static_cast<int64_t>(nb) * strip / S);
+  const int last = static_cast<int>(static_cast<int64_t>(nb) * (strip + 1) / S);
   const int64_t base = (static_cast<int64_t>(b) * p.Hkv + h) * p.T_cap;
   const int cols = p.g * n;
-  // a block's rows into L2, ahead of the loads (one lane)
-  auto prefetch = [&](int i) {
-    if (i >= last) return;
-    const Block x = block(i);
-    prefetch_bytes(x.row, x.n * (x.packed ? p.krow : kRowBytes));
-    if (x.packed) prefetch_bytes(x.sz, x.n * p.kszrow);
-    if (a.mass_in) prefetch_bytes(a.mass_in + base + x.t0, 4 * x.n);
-  };
-  if (lane == 0)
-    for (int k = 0; k < kAhead; ++k) prefetch(first + warp + k * kWarps);
+  const int reach = len - n + 1;  // every column sees the positions below
   // one pass over the rows for every 64 columns (at least one: the decay)
   for (int col0 = 0; col0 == 0 || col0 < cols; col0 += 8 * kMaxTiles) {
     const int tiles = min(kMaxTiles, (cols - col0 + 7) / 8);
     if (col0 > 0) __syncthreads();
-    load_columns<G>(a, sm, b, h, len, n, col0, tiles);
-    RawRow<KB> r0, r1;
-    auto fetch = [&](const Block& x) {
-      if constexpr (KB < 16) {
-        if (x.packed) {  // rows past the last are read from it
-          const int i0 = min(gid, x.n - 1), i1 = min(gid + 8, x.n - 1);
-          load_packed<KB, G>(x.row + i0 * p.krow, x.sz + i0 * p.kszrow, tig, r0);
-          load_packed<KB, G>(x.row + i1 * p.krow, x.sz + i1 * p.kszrow, tig, r1);
-        }
-      }
-    };
-    // the mass that the block's sum is added to: lanes tig 0 have row gid, tig 1 row gid + 8
+    load_columns<KB, G>(a, sm, b, h, len, n, col0, tiles);
+    // what the sums are added to: lanes tig 0 have row gid, tig 1 row gid + 8
     const int my = tig == 0 ? gid : gid + 8;
-    auto fetch_mass = [&](const Block& x) {
-      if (tig >= 2 || my >= x.n) return 0.f;
-      if (col0 > 0) return a.mass[base + x.t0 + my];
-      return a.mass_in ? a.decay * a.mass_in[base + x.t0 + my] : 0.f;
+    auto fetch_mass = [&](int t0, int m) {
+      if (tig >= 2 || my >= m) return 0.f;
+      if (col0 > 0) return a.mass[base + t0 + my];
+      return a.mass_in ? a.decay * a.mass_in[base + t0 + my] : 0.f;
     };
-    Block cur;
-    float cur_mass = 0.f;
-    if (first + warp < last) {
-      cur = block(first + warp);
-      cur_mass = fetch_mass(cur);
-      fetch(cur);
-    }
-#pragma unroll 1
-    for (int i = first + warp; i < last; i += kWarps) {
-      const Block x = cur;
-      const float m_in = cur_mass;
-      if (lane == 0 && col0 == 0) prefetch(i + kAhead * kWarps);
-      const bool late = x.t0 + x.n > len - n + 1;  // some column does not reach the last rows
-      float w0 = 0.f, w1 = 0.f;                    // weights of rows gid, gid + 8
-      auto add = [&](int t, float (&S)[4]) {
-        const float2 l2 = sm.lse2[t][tig];
-        float e0 = ex2(S[0] - l2.x), e1 = ex2(S[1] - l2.y), e2 = ex2(S[2] - l2.x), e3 = ex2(S[3] - l2.y);
-        if (late) {
-          const int2 lim = sm.lim[t][tig];
-          const int ta = x.t0 + gid, tb = ta + 8;
-          if (ta >= lim.x) e0 = 0.f;
-          if (ta >= lim.y) e1 = 0.f;
-          if (tb >= lim.x) e2 = 0.f;
-          if (tb >= lim.y) e3 = 0.f;
-        }
-        w0 += e0 + e1;
-        w1 += e2 + e3;
+    float w0 = 0.f, w1 = 0.f;  // weights of rows gid, gid + 8 of the block
+    auto add = [&](int t, const float (&x)[4], int t0, bool late) {
+      float e0 = ex2(x[0]), e1 = ex2(x[1]), e2 = ex2(x[2]), e3 = ex2(x[3]);
+      if (late) {
+        const int2 lim = sm.lim[t][tig];
+        const int ta = t0 + gid, tb = ta + 8;
+        if (ta >= lim.x) e0 = 0.f;
+        if (ta >= lim.y) e1 = 0.f;
+        if (tb >= lim.x) e2 = 0.f;
+        if (tb >= lim.y) e3 = 0.f;
+      }
+      w0 += e0 + e1;
+      w1 += e2 + e3;
+    };
+    auto store = [&](int t0, int m, float m_in) {
+      w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+      w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+      w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+      w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+      if (tig < 2 && my < m) a.mass[base + t0 + my] = m_in + (tig == 0 ? w0 : w1);
+    };
+    // A warp's blocks of a run of `rows` rows from position t_base on: the
+    // blocks lo + warp, lo + warp + 8, .. below hi.  Rows past the last are
+    // read from it and not stored.
+    auto run_bf16 = [&](const uint8_t* rows_at, int rows, int t_base, int lo, int hi) {
+      auto prefetch = [&](int i) {
+        if (i >= hi) return;
+        const int m = min(kRows, rows - i * kRows);
+        prefetch_bytes(rows_at + static_cast<int64_t>(i) * kRows * kRowBytes, m * kRowBytes);
+        if (a.mass_in) prefetch_bytes(a.mass_in + base + t_base + i * kRows, 4 * m);
       };
-      if (KB < 16 && x.packed) {
-        if constexpr (KB < 16) {
-          uint32_t f0[4][4], f1[4][4];
-          slice_regs<KB>(r0, f0);
-          slice_regs<KB>(r1, f1);
-          const uint4 sz0 = r0.sz, sz1 = r1.sz;
-          if (i + kWarps < last) {
-            cur = block(i + kWarps);
-            cur_mass = fetch_mass(cur);
-            fetch(cur);
-          }
-          uint32_t za = 0u, zc = 0u;  // z halves 2 (tig & 1), + 1
-          float s0[NG], s1[NG];
-          if constexpr (NG == 4) {
-            za = (tig & 1) ? sz0.y : sz0.x;
-            zc = (tig & 1) ? sz1.y : sz1.x;
-            h2_to_f2(sz0.z, s0[0], s0[1]);
-            h2_to_f2(sz0.w, s0[2], s0[3]);
-            h2_to_f2(sz1.z, s1[0], s1[1]);
-            h2_to_f2(sz1.w, s1[2], s1[3]);
-          } else if constexpr (NG == 2) {
-            if (!(tig & 1)) za = sz0.x, zc = sz1.x;
-            h2_to_f2(sz0.y, s0[0], s0[1]);
-            h2_to_f2(sz1.y, s1[0], s1[1]);
-          } else {
-            if (!(tig & 1)) za = sz0.x & 0xffffu, zc = sz1.x & 0xffffu;
-            float z;
-            h2_to_f2(sz0.x, z, s0[0]);
-            h2_to_f2(sz1.x, z, s1[0]);
-          }
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float kf = a.scale_log2 * kKFactor<KB>(g * PPG);
-            s0[g] *= kf;
-            s1[g] *= kf;
-          }
+      if (lane == 0 && col0 == 0)
+        for (int k = 0; k < kAhead; ++k) prefetch(lo + warp + k * kWarps);
 #pragma unroll 1
-          for (int t = 0; t < tiles; ++t) {
-            float C[4][4];
-#pragma unroll
-            for (int P = 0; P < 4; ++P) {
-              C[P][0] = C[P][1] = C[P][2] = C[P][3] = 0.f;
-              const uint4 q = sm.qh[t][P][lane];
-              const uint32_t A0[4] = {f0[P][0], f1[P][0], f0[P][1], f1[P][1]};
-              const uint32_t A1[4] = {f0[P][2], f1[P][2], f0[P][3], f1[P][3]};
-              mma_f16(C[P], A0, q.x, q.y);
-              mma_f16(C[P], A1, q.z, q.w);
-            }
-            float S[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t Z[4] = {za, zc, 0u, 0u};
-            mma_f16(S, Z, sm.zb[t][lane], 0u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) S[k] *= kZbScale;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float v = C[g * PPG][k];
-#pragma unroll
-                for (int e = 1; e < PPG; ++e)
-                  v = fmaf(C[g * PPG + e][k], kKFactor<KB>(g * PPG + e) / kKFactor<KB>(g * PPG), v);
-                S[k] = fmaf(k < 2 ? s0[g] : s1[g], v, S[k]);
-              }
-            add(t, S);
-          }
-        }
-      } else {
+      for (int i = lo + warp; i < hi; i += kWarps) {
+        const int m = min(kRows, rows - i * kRows), t0 = t_base + i * kRows;
+        const uint8_t* at = rows_at + static_cast<int64_t>(i) * kRows * kRowBytes + 16 * tig;
         uint4 f0[4], f1[4];
 #pragma unroll
         for (int P = 0; P < 4; ++P) {
-          const int off = 64 * P + 16 * tig;
-          f0[P] = *reinterpret_cast<const uint4*>(x.row + min(gid, x.n - 1) * kRowBytes + off);
-          f1[P] = *reinterpret_cast<const uint4*>(x.row + min(gid + 8, x.n - 1) * kRowBytes + off);
+          f0[P] = *reinterpret_cast<const uint4*>(at + min(gid, m - 1) * kRowBytes + 64 * P);
+          f1[P] = *reinterpret_cast<const uint4*>(at + min(gid + 8, m - 1) * kRowBytes + 64 * P);
         }
-        if (i + kWarps < last) {
-          cur = block(i + kWarps);
-          cur_mass = fetch_mass(cur);
-          fetch(cur);
-        }
-#pragma unroll 1
+        const float m_in = fetch_mass(t0, m);
+        if (lane == 0 && col0 == 0) prefetch(i + kAhead * kWarps);
+        const bool late = t0 + m > reach;
+        w0 = w1 = 0.f;
+#pragma unroll 2
         for (int t = 0; t < tiles; ++t) {
-          float C[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          float C[2][4], x[4];
 #pragma unroll
           for (int P = 0; P < 4; ++P) {
             const uint4 q = sm.qb[t][P][lane];
             const uint32_t A0[4] = {f0[P].x, f1[P].x, f0[P].y, f1[P].y};
             const uint32_t A1[4] = {f0[P].z, f1[P].z, f0[P].w, f1[P].w};
-            mma_bf16(C[0], A0, q.x, q.y);
-            mma_bf16(C[1], A1, q.z, q.w);
+            if (P == 0) {
+              mma_bf16_new(C[0], A0, q.x, q.y);
+              mma_bf16_new(C[1], A1, q.z, q.w);
+            } else {
+              mma_bf16(C[0], A0, q.x, q.y);
+              mma_bf16(C[1], A1, q.z, q.w);
+            }
           }
-          float S[4];
+          const float2 l2 = sm.lse2[t][tig];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) S[k] = (C[0][k] + C[1][k]) * a.scale_log2;
-          add(t, S);
+          for (int k = 0; k < 4; ++k) x[k] = fmaf(C[0][k] + C[1][k], a.scale_log2, (k & 1) ? -l2.y : -l2.x);
+          add(t, x, t0, late);
+        }
+        store(t0, m, m_in);
+      }
+    };
+    auto run_packed = [&](int lo, int hi) {
+      if constexpr (KB < 16) {
+        auto prefetch = [&](int i) {
+          if (i >= hi) return;
+          const int m = min(kRows, n_vis - i * kRows);
+          const int64_t r = static_cast<int64_t>(i) * kRows;
+          prefetch_bytes(hr.vis_k + r * p.krow, m * p.krow);
+          prefetch_bytes(hr.vis_ksz + r * p.kszrow, m * p.kszrow);
+          if (a.mass_in) prefetch_bytes(a.mass_in + base + p.vs + r, 4 * m);
+        };
+        RawRow<KB> r0, r1;
+        float next_mass = 0.f;
+        auto fetch = [&](int i) {
+          const int m = min(kRows, n_vis - i * kRows);
+          const int64_t r = static_cast<int64_t>(i) * kRows;
+          const uint8_t *row = hr.vis_k + r * p.krow, *sz = hr.vis_ksz + r * p.kszrow;
+          const int i0 = min(gid, m - 1), i1 = min(gid + 8, m - 1);
+          load_packed<KB, G>(row + i0 * p.krow, sz + i0 * p.kszrow, tig, r0);
+          load_packed<KB, G>(row + i1 * p.krow, sz + i1 * p.kszrow, tig, r1);
+          next_mass = fetch_mass(p.vs + i * kRows, m);
+        };
+        if (lane == 0 && col0 == 0)
+          for (int k = 1; k < kAhead; ++k) prefetch(lo + warp + k * kWarps);
+        if (lo + warp < hi) fetch(lo + warp);
+#pragma unroll 1
+        for (int i = lo + warp; i < hi; i += kWarps) {
+          const int m = min(kRows, n_vis - i * kRows), t0 = p.vs + i * kRows;
+          const float m_in = next_mass;
+          uint32_t f0[4][4], f1[4][4];
+          slice_regs<KB>(r0, f0);
+          slice_regs<KB>(r1, f1);
+          // the zero points (halves 2 (tig & 1), + 1) and the scales
+          uint32_t za = 0u, zc = 0u;
+          float s0[NG], s1[NG];
+          if constexpr (NG == 4) {
+            za = (tig & 1) ? r0.sz.y : r0.sz.x;
+            zc = (tig & 1) ? r1.sz.y : r1.sz.x;
+            h2_to_f2(r0.sz.z, s0[0], s0[1]);
+            h2_to_f2(r0.sz.w, s0[2], s0[3]);
+            h2_to_f2(r1.sz.z, s1[0], s1[1]);
+            h2_to_f2(r1.sz.w, s1[2], s1[3]);
+          } else if constexpr (NG == 2) {
+            if (!(tig & 1)) za = r0.sz.x, zc = r1.sz.x;
+            h2_to_f2(r0.sz.y, s0[0], s0[1]);
+            h2_to_f2(r1.sz.y, s1[0], s1[1]);
+          } else {
+            if (!(tig & 1)) za = r0.sz.x & 0xffffu, zc = r1.sz.x & 0xffffu;
+            float z;
+            h2_to_f2(r0.sz.x, z, s0[0]);
+            h2_to_f2(r1.sz.x, z, s1[0]);
+          }
+          const float kf = a.scale_log2 * (pow2i(24 - k_first_shift<KB>()) / kZbScale);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            s0[g] *= kf;
+            s1[g] *= kf;
+          }
+          if (i + kWarps < hi) fetch(i + kWarps);
+          if (lane == 0 && col0 == 0) prefetch(i + kAhead * kWarps);
+          const bool late = t0 + m > reach;
+          w0 = w1 = 0.f;
+#pragma unroll 2
+          for (int t = 0; t < tiles; ++t) {
+            float C[NG][4], x[4];
+#pragma unroll
+            for (int P = 0; P < 4; ++P) {
+              const uint4 q = sm.qh[t][P][lane];
+              const uint32_t A0[4] = {f0[P][0], f1[P][0], f0[P][1], f1[P][1]};
+              const uint32_t A1[4] = {f0[P][2], f1[P][2], f0[P][3], f1[P][3]};
+              if (P % PPG == 0) mma_f16_new(C[P / PPG], A0, q.x, q.y);
+              else mma_f16(C[P / PPG], A0, q.x, q.y);
+              mma_f16(C[P / PPG], A1, q.z, q.w);
+            }
+            const uint32_t Z[4] = {za, zc, 0u, 0u};
+            mma_f16_new(x, Z, sm.zb[t][lane], 0u);
+            const float2 l2 = sm.lse2[t][tig];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+              for (int g = 0; g < NG; ++g) x[k] = fmaf(k < 2 ? s0[g] : s1[g], C[g][k], x[k]);
+              x[k] = fmaf(x[k], kZbScale, (k & 1) ? -l2.y : -l2.x);
+            }
+            add(t, x, t0, late);
+          }
+          store(t0, m, m_in);
         }
       }
-      w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-      w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-      if (tig < 2 && my < x.n) a.mass[base + x.t0 + my] = m_in + (tig == 0 ? w0 : w1);
+    };
+    const int e0 = min(last, b1), s1_ = max(first, b1), e1 = min(last, b2), s2_ = max(first, b2);
+    if (first < e0) run_bf16(hr.text_k, n_pre, 0, first, e0);
+    if (s1_ < e1) {
+      if (KB < 16 && hr.k_packed) run_packed(s1_ - b1, e1 - b1);
+      else run_bf16(hr.vis_k, n_vis, p.vs, s1_ - b1, e1 - b1);
     }
+    if (s2_ < last)
+      run_bf16(hr.text_k + static_cast<int64_t>(p.vs) * kRowBytes, n_suf, p.ve, s2_ - b2, last - b2);
   }
 }
 
@@ -451,16 +480,9 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
   const int64_t bytes = 4 * static_cast<int64_t>(L->d.B) * L->d.H_kv * L->d.T_cap;
   if (mass_in != mass && kvq::ranges_meet(mass_in, bytes, mass, bytes)) return KVQ_ERR_INVALID_ARG;
   const int64_t units = static_cast<int64_t>(L->d.B) * L->d.H_kv;
-  // CTAs per (sequence, KV head): enough for several waves of resident CTAs,
-  // so that heads with bf16 rows (up to 10 times the bytes) even out, but at
-  // least a block for every warp of a CTA.
+  if (units > 0x3fffffffLL || static_cast<int64_t>(L->g) * KVQ_MAX_QUERY_TOKENS > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
-  const int64_t want = (4 * kvq::kCtasPerSm * static_cast<int64_t>(n_sm) + units - 1) / units;
-  const int64_t most = std::max<int64_t>(1, T / (kvq::kRows * kvq::kWarps));
-  const int64_t strips = std::max<int64_t>(1, std::min(want, most));
-  if (units * strips > 0x7fffffffLL || static_cast<int64_t>(L->g) * KVQ_MAX_QUERY_TOKENS > 0x7fffffffLL)
-    return KVQ_ERR_UNSUPPORTED;
   const void* fn = L->d.k_bits == 2   ? kvq::mass_kernel_for<2>(L->d.group_size)
                    : L->d.k_bits == 4 ? kvq::mass_kernel_for<4>(L->d.group_size)
                    : L->d.k_bits == 8 ? kvq::mass_kernel_for<8>(L->d.group_size)
@@ -480,10 +502,27 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
   a.decay = decay;
   a.mass_in = mass_in;
   a.mass = mass;
-  a.strips = static_cast<int32_t>(strips);
+  // CTAs per (sequence, KV head): one wave of resident CTAs, the pairs with
+  // bf16 K rows split finer (a bf16 block takes about twice as long), but no
+  // CTA below a block for each of its warps.
   int h = 0;
   for (int k = 0; k < L->n_prot; ++k) a.head[h++] = L->prot_head[k];
   for (int k = 0; k < L->n_konly; ++k) a.head[h++] = L->konly_head[k];
+  a.n_bf16 = h;
   for (int k = 0; k < L->n_packed; ++k) a.head[h++] = L->packed_head[k];
-  return kvq::launch_dependent(fn, dim3(static_cast<unsigned>(units * strips)), kvq::kWarps * 32, 0, stream, &a);
+  a.U[0] = L->d.B * a.n_bf16;
+  a.U[1] = L->d.B * L->n_packed;
+  const double cost[2] = {2.0, 1.0};
+  const int64_t cap = static_cast<int64_t>(kvq::kCtasPerSm) * n_sm;
+  const int most = std::max(1, T / (kvq::kRows * kvq::kWarps));
+  a.S[0] = a.S[1] = 1;
+  for (;;) {
+    int worst = -1;
+    for (int k = 0; k < 2; ++k)
+      if (a.U[k] && (worst < 0 || cost[k] / a.S[k] > cost[worst] / a.S[worst])) worst = k;
+    const int64_t used = static_cast<int64_t>(a.U[0]) * a.S[0] + static_cast<int64_t>(a.U[1]) * a.S[1];
+    if (a.S[worst] >= most || used + a.U[worst] > cap) break;
+    ++a.S[worst];
+  }
+  return kvq::launch_dependent(fn, dim3(a.U[0] * a.S[0] + a.U[1] * a.S[1]), kvq::kWarps * 32, 0, stream, &a);
 }
