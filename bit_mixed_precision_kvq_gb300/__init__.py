@@ -350,38 +350,70 @@ def decode_attention_static_ws(L: Layout, cache, q, T: int, out,
         raise KvqError(st, "kvq_decode_attention_static_ws")
 
 
-def _tensor(what: str, x, dtype: str, shape, contiguous: bool = True) -> None:
-    """Refuse a tensor (None and raw addresses pass) of another type or shape,
-    with holes, or on another device than the current one: the C call would
-    read it as something else."""
-    if x is None or isinstance(x, int):
-        return
+def _refuse(what: str, x, dtype: str, shape, dev: int) -> None:
+    """Why a tensor is not what a call needs."""
     import torch
     if x.dtype != getattr(torch, dtype) or (shape is not None and tuple(x.shape) != shape):
         raise ValueError(f"{what}: {dtype} of shape {shape} expected, got {x.dtype} {tuple(x.shape)}")
-    if contiguous and not x.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+    if x.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device")
+    raise ValueError(f"{what} must be contiguous")
 
 
-def _cache_bytes(what: str, L: Layout, x) -> None:
-    _tensor(what, x, "uint8", None)
-    if not (x is None or isinstance(x, int)) and x.numel() < L.total_bytes:
+def _ptr(what: str, x, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of the given type and shape on device
+    dev; None and raw addresses pass.  The C call would read anything else as
+    something it is not."""
+    if x is None:
+        return 0
+    if x.__class__ is int:
+        return x
+    if x.dtype is dtype and x.shape == shape and x.is_contiguous() and x.get_device() == dev:
+        return x.data_ptr()
+    return _refuse(what, x, str(dtype)[6:], shape, dev)
+
+
+def _cache_ptr(what: str, L: Layout, x, dtype, dev: int) -> int:
+    if x.__class__ is int:
+        return x
+    if x.dtype is dtype and x.is_contiguous() and x.get_device() == dev:
+        if x.numel() >= L.total_bytes:
+            return x.data_ptr()
         raise ValueError(f"{what}: {L.total_bytes} bytes expected, got {x.numel()}")
+    return _refuse(what, x, "uint8", None, dev)
 
 
-def _drafts(L: Layout, k, v, n_q: int):
-    """Strides of the drafted rows ([B, H_kv, n_q, D], last dimension contiguous)."""
-    shape = (L.d.B, L.d.H_kv, n_q, L.d.D)
-    _tensor("k_draft", k, "bfloat16", shape, False)
-    _tensor("v_draft", v, "bfloat16", shape, False)
+def _drafts(k, v, shape, dtype, dev: int):
+    """Addresses and strides of the drafted rows ([B, H_kv, n_q, D], last
+    dimension contiguous)."""
+    for what, x in (("k_draft", k), ("v_draft", v)):
+        if not (x.dtype is dtype and x.shape == shape and x.get_device() == dev):
+            _refuse(what, x, "bfloat16", shape, dev)
     s = k.stride()
     if s != v.stride():
         raise ValueError("k_draft and v_draft must share strides")
     if s[3] != 1:
         raise ValueError("last dim must be contiguous")
-    return [0 if shape[i] == 1 else s[i] for i in range(3)]
+    # a dimension of one row has no stride to speak of
+    return (k.data_ptr(), v.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0,
+            s[2] if shape[2] > 1 else 0)
+
+
+_raw_stream = None
+
+
+def _current(stream):
+    """(torch, current device, raw stream): the given stream, or the current one."""
+    import torch
+    global _raw_stream
+    if _raw_stream is None:  # the public call builds a Stream object first
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    if stream is None:
+        dev = torch.cuda.current_device()
+        return torch, dev, _raw_stream(dev)
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    return torch, dev, stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
 def decode_tree_workspace_bytes(L: Layout, n_q: int) -> int:
@@ -398,26 +430,25 @@ def decode_attention_tree(L: Layout, cache, q, k_draft, v_draft, tree_mask, T_ct
     [1, n_q] for one tree of the whole batch (bit j of entry i: token i sees
     draft j).  Token i attends the cache positions [0, seq_len[b]) ([0, T_ctx)
     without seq_len) and its drafts; out [B, n_q, H_q, D], lse [B, n_q, H_q]."""
-    d = L.d
     if q.dim() != 4:
         raise ValueError("q must be [B, n_q, H_q, D]")
-    n_q = int(q.shape[1])
-    _cache_bytes("cache", L, cache)
-    _tensor("q", q, "bfloat16", (d.B, n_q, d.H_q, d.D))
-    sb, sh, st_ = _drafts(L, k_draft, v_draft, n_q)
-    shared = tree_mask.dim() == 1 or tree_mask.shape[0] != d.B
-    _tensor("tree_mask", tree_mask, "int64", ((n_q,) if tree_mask.dim() == 1 else (1, n_q)) if shared else (d.B, n_q))
-    _tensor("out", out, "bfloat16", (d.B, n_q, d.H_q, d.D))
-    _tensor("lse", lse, "float32", (d.B, n_q, d.H_q))
-    _tensor("seq_len", seq_len, "int32", (d.B,))
+    torch, dev, st = _current(stream)
+    d, bf16 = L.d, torch.bfloat16
+    B, n_q, Hq = d.B, q.shape[1], d.H_q
+    rows = (B, n_q, Hq, d.D)
+    cp, qp = _cache_ptr("cache", L, cache, torch.uint8, dev), _ptr("q", q, bf16, rows, dev)
+    kp, vp, sb, sh, sd = _drafts(k_draft, v_draft, (B, d.H_kv, n_q, d.D), bf16, dev)
+    shared = tree_mask.dim() == 1 or tree_mask.shape[0] != B
+    mask = _ptr("tree_mask", tree_mask, torch.int64,
+                ((n_q,) if tree_mask.dim() == 1 else (1, n_q)) if shared else (B, n_q), dev)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d.D)
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = load().kvq_decode_attention_tree(ctypes.byref(L), _addr(cache), _addr(q), _addr(k_draft), _addr(v_draft), sb, sh,
-                                          st_, n_q, _addr(tree_mask), 0 if shared else n_q, _addr(seq_len), int(T_ctx),
-                                          float(softmax_scale), _addr(out), _addr(lse), _addr(workspace), int(ws_bytes),
-                                          _stream(stream))
+    st = load().kvq_decode_attention_tree(
+        ctypes.byref(L), cp, qp, kp, vp, sb, sh, sd, n_q, mask, 0 if shared else n_q,
+        _ptr("seq_len", seq_len, torch.int32, (B,), dev), T_ctx, softmax_scale,
+        _ptr("out", out, bf16, rows, dev), _ptr("lse", lse, torch.float32, (B, n_q, Hq), dev), _addr(workspace), ws_bytes, st)
     if st != 0:
         raise KvqError(st, "kvq_decode_attention_tree")
 
@@ -428,18 +459,17 @@ def tree_commit(L: Layout, cache, k_draft, v_draft, path, path_len, T_ctx: int, 
     seq_len) takes drafted row path[b, k] (int32 [B, max_path]) for
     k < path_len[b] (int32 [B]); new_len (int32 [B], other memory than
     seq_len) gets the new lengths, -1 for an inactive sequence."""
-    d = L.d
     if k_draft.dim() != 4 or path.dim() != 2:
         raise ValueError("k_draft must be [B, H_kv, n_q, D] and path [B, max_path]")
-    n_q, max_path = int(k_draft.shape[2]), int(path.shape[1])
-    _cache_bytes("cache", L, cache)
-    sb, sh, st_ = _drafts(L, k_draft, v_draft, n_q)
-    _tensor("path", path, "int32", (d.B, max_path))
-    _tensor("path_len", path_len, "int32", (d.B,))
-    _tensor("seq_len", seq_len, "int32", (d.B,))
-    _tensor("new_len", new_len, "int32", (d.B,))
-    st = load().kvq_tree_commit(ctypes.byref(L), _addr(cache), _addr(k_draft), _addr(v_draft), sb, sh, st_, n_q, _addr(path),
-                                max_path, _addr(path_len), _addr(seq_len), int(T_ctx), _addr(new_len), _stream(stream))
+    torch, dev, st = _current(stream)
+    d, i32 = L.d, torch.int32
+    B, n_q, max_path = d.B, k_draft.shape[2], path.shape[1]
+    per_seq = (B,)
+    kp, vp, sb, sh, sd = _drafts(k_draft, v_draft, (B, d.H_kv, n_q, d.D), torch.bfloat16, dev)
+    st = load().kvq_tree_commit(
+        ctypes.byref(L), _cache_ptr("cache", L, cache, torch.uint8, dev), kp, vp, sb, sh, sd, n_q,
+        _ptr("path", path, i32, (B, max_path), dev), max_path, _ptr("path_len", path_len, i32, per_seq, dev),
+        _ptr("seq_len", seq_len, i32, per_seq, dev), T_ctx, _ptr("new_len", new_len, i32, per_seq, dev), st)
     if st != 0:
         raise KvqError(st, "kvq_tree_commit")
 
@@ -452,25 +482,22 @@ def attention_mass(L: Layout, cache, q, lse, T: int, mass, mass_in=None, softmax
     [B, H_q]) of one attention call; mass and mass_in float32
     [B, H_kv, T_cap] (mass_in: None for zeros, or mass itself); path int32
     [B, max_path] and path_len int32 [B] pick the tokens (all without)."""
-    d = L.d
-    n_q = int(q.shape[1]) if q.dim() == 4 else 1
-    rows = (d.B, n_q, d.H_q) if q.dim() == 4 else (d.B, d.H_q)
-    _cache_bytes("cache", L, cache)
-    _tensor("q", q, "bfloat16", rows + (d.D,))
-    _tensor("lse", lse, "float32", rows)
-    _tensor("mass", mass, "float32", (d.B, d.H_kv, d.T_cap))
-    _tensor("mass_in", mass_in, "float32", (d.B, d.H_kv, d.T_cap))
-    _tensor("seq_len", seq_len, "int32", (d.B,))
+    torch, dev, st = _current(stream)
+    d, f32, i32 = L.d, torch.float32, torch.int32
+    B = d.B
+    n_q = q.shape[1] if q.dim() == 4 else 1
+    rows = (B, n_q, d.H_q) if q.dim() == 4 else (B, d.H_q)
+    acc, per_seq = (B, d.H_kv, d.T_cap), (B,)
     max_path = 0
     if path is not None:
-        max_path = int(path.shape[1]) if path.dim() == 2 else 0
-        _tensor("path", path, "int32", (d.B, max_path))
-        _tensor("path_len", path_len, "int32", (d.B,))
+        max_path = path.shape[1] if path.dim() == 2 else 0
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d.D)
-    st = load().kvq_attention_mass(ctypes.byref(L), _addr(cache), _addr(q), _addr(lse), n_q, _addr(seq_len), int(T),
-                                   _addr(path), max_path, _addr(path_len), float(softmax_scale), _addr(mass_in),
-                                   float(decay), _addr(mass), _stream(stream))
+    st = load().kvq_attention_mass(
+        ctypes.byref(L), _cache_ptr("cache", L, cache, torch.uint8, dev), _ptr("q", q, torch.bfloat16, rows + (d.D,), dev),
+        _ptr("lse", lse, f32, rows, dev), n_q, _ptr("seq_len", seq_len, i32, per_seq, dev), T,
+        _ptr("path", path, i32, (B, max_path), dev), max_path, _ptr("path_len", path_len, i32, per_seq, dev), softmax_scale,
+        _ptr("mass_in", mass_in, f32, acc, dev), decay, _ptr("mass", mass, f32, acc, dev), st)
     if st != 0:
         raise KvqError(st, "kvq_attention_mass")
 
@@ -482,17 +509,14 @@ def cache_evict(L: Layout, cache, mass, T: int, L_dst: Layout, cache_dst, T_dst:
     cache_dst, whose layout L_dst has a smaller visual block; keep int32
     [B, H_kv, T_dst] gets their source positions, mass_dst float32
     [B, H_kv, T_cap_dst] their masses, new_len int32 [B] the new lengths."""
-    d = L.d
-    _cache_bytes("cache", L, cache)
-    _cache_bytes("cache_dst", L_dst, cache_dst)
-    _tensor("mass", mass, "float32", (d.B, d.H_kv, d.T_cap))
-    _tensor("keep", keep, "int32", (d.B, d.H_kv, int(T_dst)))
-    _tensor("mass_dst", mass_dst, "float32", (d.B, d.H_kv, L_dst.d.T_cap))
-    _tensor("seq_len", seq_len, "int32", (d.B,))
-    _tensor("new_len", new_len, "int32", (d.B,))
-    st = load().kvq_cache_evict(ctypes.byref(L), _addr(cache), _addr(mass), _addr(seq_len), int(T), ctypes.byref(L_dst),
-                                _addr(cache_dst), int(T_dst), int(n_recent), _addr(keep), _addr(mass_dst), _addr(new_len),
-                                _stream(stream))
+    torch, dev, st = _current(stream)
+    d, f32, i32, u8 = L.d, torch.float32, torch.int32, torch.uint8
+    B, H = d.B, d.H_kv
+    st = load().kvq_cache_evict(
+        ctypes.byref(L), _cache_ptr("cache", L, cache, u8, dev), _ptr("mass", mass, f32, (B, H, d.T_cap), dev),
+        _ptr("seq_len", seq_len, i32, (B,), dev), T, ctypes.byref(L_dst), _cache_ptr("cache_dst", L_dst, cache_dst, u8, dev),
+        T_dst, n_recent, _ptr("keep", keep, i32, (B, H, T_dst), dev),
+        _ptr("mass_dst", mass_dst, f32, (B, H, L_dst.d.T_cap), dev), _ptr("new_len", new_len, i32, (B,), dev), st)
     if st != 0:
         raise KvqError(st, "kvq_cache_evict")
 

@@ -45,8 +45,7 @@ __device__ __forceinline__ int evict_len(const EvictArgs& a, int b) {
 // found in three passes of 11, 11 and 10 bits: a histogram in shared memory of
 // the keys that share the digits found so far, and the bin in which the count
 // from above reaches `want`.  11 bits spread the exponents of real masses over
-// enough bins that the shared-memory atomics do not queue; a warp whose keys
-// all fall into one bin (ties, zeros) adds once.
+// enough bins that the shared-memory atomics do not queue.
 constexpr int kBins = 2048;
 
 template <int NT>
@@ -57,18 +56,6 @@ struct SelectSmem {
   uint2 start[1024];
   uint32_t digit, want;
 };
-
-__device__ __forceinline__ void hist_add(uint32_t* hist, uint32_t bin, bool in) {
-  const uint32_t who = __ballot_sync(0xffffffffu, in);
-  if (who == 0) return;
-  const int leader = __ffs(who) - 1;
-  const uint32_t b0 = __shfl_sync(0xffffffffu, bin, leader);
-  if (__all_sync(0xffffffffu, !in || bin == b0)) {
-    if ((threadIdx.x & 31) == leader) atomicAdd(&hist[b0], __popc(who));
-  } else if (in) {
-    atomicAdd(&hist[bin], 1u);
-  }
-}
 
 // The bin in which the count from the highest one down reaches sm.want;
 // sm.want becomes what is wanted of that bin.  Thread k has the kBins / NT
@@ -100,8 +87,7 @@ __device__ __forceinline__ void find_bin(SelectSmem<NT>& sm) {
   __syncthreads();
 }
 
-// load(f) calls f(key, there is one) for every key of the thread, all threads
-// the same number of times.
+// load(f) calls f(key, there is one) for every key of the thread.
 template <int NT, typename F>
 __device__ __forceinline__ uint32_t find_threshold(SelectSmem<NT>& sm, int want, F&& load) {
   const int tid = threadIdx.x;
@@ -114,7 +100,9 @@ __device__ __forceinline__ uint32_t find_threshold(SelectSmem<NT>& sm, int want,
     const uint32_t high = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
     for (int k = tid; k < kBins; k += NT) sm.hist[k] = 0;
     __syncthreads();
-    load([&](uint32_t key, bool in) { hist_add(sm.hist, (key >> shift) & mask, in && (key & high) == prefix); });
+    load([&](uint32_t key, bool in) {
+      if (in && (key & high) == prefix) atomicAdd(&sm.hist[(key >> shift) & mask], 1u);
+    });
     __syncthreads();
     find_bin(sm);
     prefix |= sm.digit << shift;
@@ -132,10 +120,10 @@ __device__ void select_in_registers(SelectSmem<NT>& sm, const float* x, int n, i
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t key[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = tid + NT * r;
-    key[r] = i < n ? order_key(__ldcg(x + i)) : 0u;
-  }
+  for (int r = 0; r < R; ++r)  // every load before any use
+    key[r] = tid + NT * r < n ? __float_as_uint(__ldcg(x + tid + NT * r)) : 0u;
+#pragma unroll
+  for (int r = 0; r < R; ++r) key[r] = order_key(__uint_as_float(key[r]));
   const uint32_t T = find_threshold<NT>(sm, want, [&](auto&& f) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -185,18 +173,29 @@ __device__ void select_in_registers(SelectSmem<NT>& sm, const float* x, int n, i
     }
   __syncthreads();
   const uint32_t below = (1u << lane) - 1u;
+  constexpr int kBatch = R < 8 ? R : 8;  // values in flight
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = tid + NT * r;
-    const bool in = i < n;
-    const uint32_t gt = __ballot_sync(0xffffffffu, in && key[r] > T), eq = __ballot_sync(0xffffffffu, in && key[r] == T);
-    const uint2 at = sm.start[r * NW + warp];
-    const uint32_t q = at.y + __popc(eq & below);
-    if (in && (key[r] > T || (key[r] == T && q < ties))) {
-      const uint32_t o = at.x + __popc(gt & below) + min(q, ties);
-      out[o] = pos0 + i;
-      if (xout) xout[o] = __ldcg(x + i);
+  for (int r0 = 0; r0 < R; r0 += kBatch) {
+    if (NT * r0 >= n) break;
+    int at[kBatch];
+    float v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k, i = tid + NT * r;
+      const bool in = i < n;
+      const uint32_t gt = __ballot_sync(0xffffffffu, in && key[r] > T), eq = __ballot_sync(0xffffffffu, in && key[r] == T);
+      const uint2 s = sm.start[r * NW + warp];
+      const uint32_t q = s.y + __popc(eq & below);
+      const bool stays = in && (key[r] > T || (key[r] == T && q < ties));
+      at[k] = stays ? static_cast<int>(s.x + __popc(gt & below) + min(q, ties)) : -1;
+      v[k] = stays && xout ? __ldcg(x + i) : 0.f;
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (at[k] >= 0) {
+        out[at[k]] = pos0 + tid + NT * (r0 + k);
+        if (xout) xout[at[k]] = v[k];
+      }
   }
 }
 

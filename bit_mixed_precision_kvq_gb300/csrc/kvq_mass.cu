@@ -348,34 +348,41 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
         store(t0, m, m_in);
       }
     };
+    // Packed rows: a warp has a contiguous run of blocks, so that its pointers
+    // step and one prefetch serves four of them.  A block past the last row
+    // reads on into the segment's padding (whole blocks of 16 rows).
     auto run_packed = [&](int lo, int hi) {
       if constexpr (KB < 16) {
-        auto prefetch = [&](int i) {
-          if (i >= hi) return;
-          const int m = min(kRows, n_vis - i * kRows);
+        const int w_lo = lo + (hi - lo) * warp / kWarps, w_hi = lo + (hi - lo) * (warp + 1) / kWarps;
+        if (w_lo >= w_hi) return;
+        const int64_t row0 = static_cast<int64_t>(w_lo) * kRows;
+        const uint8_t* kp = hr.vis_k + (row0 + gid) * p.krow;
+        const uint8_t* sp = hr.vis_ksz + (row0 + gid) * p.kszrow;
+        const int kstep = kRows * p.krow, sstep = kRows * p.kszrow;
+        auto prefetch = [&](int i) {  // blocks [i, i + 4)
+          const int m = min(4, w_hi - i);
+          if (m <= 0) return;
           const int64_t r = static_cast<int64_t>(i) * kRows;
-          prefetch_bytes(hr.vis_k + r * p.krow, m * p.krow);
-          prefetch_bytes(hr.vis_ksz + r * p.kszrow, m * p.kszrow);
-          if (a.mass_in) prefetch_bytes(a.mass_in + base + p.vs + r, 4 * m);
+          prefetch_bytes(hr.vis_k + r * p.krow, m * kstep);
+          prefetch_bytes(hr.vis_ksz + r * p.kszrow, m * sstep);
+          if (a.mass_in) prefetch_bytes(a.mass_in + base + p.vs + r, 4 * min(m * kRows, n_vis - i * kRows));
         };
         RawRow<KB> r0, r1;
         float next_mass = 0.f;
         auto fetch = [&](int i) {
-          const int m = min(kRows, n_vis - i * kRows);
-          const int64_t r = static_cast<int64_t>(i) * kRows;
-          const uint8_t *row = hr.vis_k + r * p.krow, *sz = hr.vis_ksz + r * p.kszrow;
-          const int i0 = min(gid, m - 1), i1 = min(gid + 8, m - 1);
-          load_packed<KB, G>(row + i0 * p.krow, sz + i0 * p.kszrow, tig, r0);
-          load_packed<KB, G>(row + i1 * p.krow, sz + i1 * p.kszrow, tig, r1);
-          next_mass = fetch_mass(p.vs + i * kRows, m);
+          load_packed<KB, G>(kp, sp, tig, r0);
+          load_packed<KB, G>(kp + (kstep >> 1), sp + (sstep >> 1), tig, r1);
+          kp += kstep;
+          sp += sstep;
+          next_mass = fetch_mass(p.vs + i * kRows, n_vis - i * kRows);
         };
-        if (lane == 0 && col0 == 0)
-          for (int k = 1; k < kAhead; ++k) prefetch(lo + warp + k * kWarps);
-        if (lo + warp < hi) fetch(lo + warp);
+        if (lane == 0 && col0 == 0) prefetch(w_lo);
+        fetch(w_lo);
 #pragma unroll 1
-        for (int i = lo + warp; i < hi; i += kWarps) {
-          const int m = min(kRows, n_vis - i * kRows), t0 = p.vs + i * kRows;
+        for (int i = w_lo; i < w_hi; ++i) {
+          const int m = n_vis - i * kRows, t0 = p.vs + i * kRows;
           const float m_in = next_mass;
+          if (lane == 0 && col0 == 0 && ((i - w_lo) & 3) == 0) prefetch(i + 4);
           uint32_t f0[4][4], f1[4][4];
           slice_regs<KB>(r0, f0);
           slice_regs<KB>(r1, f1);
@@ -405,9 +412,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
             s0[g] *= kf;
             s1[g] *= kf;
           }
-          if (i + kWarps < hi) fetch(i + kWarps);
-          if (lane == 0 && col0 == 0) prefetch(i + kAhead * kWarps);
-          const bool late = t0 + m > reach;
+          if (i + 1 < w_hi) fetch(i + 1);
+          const bool late = t0 + kRows > reach;
           w0 = w1 = 0.f;
 #pragma unroll 2
           for (int t = 0; t < tiles; ++t) {
@@ -502,9 +508,10 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
   a.decay = decay;
   a.mass_in = mass_in;
   a.mass = mass;
-  // CTAs per (sequence, KV head): one wave of resident CTAs, the pairs with
-  // bf16 K rows split finer (a bf16 block takes about twice as long), but no
-  // CTA below a block for each of its warps.
+  // CTAs per (sequence, KV head): one wave of resident CTAs (several when
+  // there are many pairs), the pairs with bf16 K rows split finer (a bf16
+  // block takes about twice as long), but no CTA below a block for each of
+  // its warps.
   int h = 0;
   for (int k = 0; k < L->n_prot; ++k) a.head[h++] = L->prot_head[k];
   for (int k = 0; k < L->n_konly; ++k) a.head[h++] = L->konly_head[k];
@@ -513,15 +520,16 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
   a.U[0] = L->d.B * a.n_bf16;
   a.U[1] = L->d.B * L->n_packed;
   const double cost[2] = {2.0, 1.0};
-  const int64_t cap = static_cast<int64_t>(kvq::kCtasPerSm) * n_sm;
-  const int most = std::max(1, T / (kvq::kRows * kvq::kWarps));
+  const int64_t wave = static_cast<int64_t>(kvq::kCtasPerSm) * n_sm;
+  const int64_t cap = units <= wave / 2 ? wave : 6 * wave;  // many pairs: several waves, for an even end
+  const int most = std::max(1, T / ((units <= wave / 2 ? 1 : 4) * kvq::kRows * kvq::kWarps));
   a.S[0] = a.S[1] = 1;
   for (;;) {
     int worst = -1;
     for (int k = 0; k < 2; ++k)
-      if (a.U[k] && (worst < 0 || cost[k] / a.S[k] > cost[worst] / a.S[worst])) worst = k;
+      if (a.U[k] && a.S[k] < most && (worst < 0 || cost[k] / a.S[k] > cost[worst] / a.S[worst])) worst = k;
     const int64_t used = static_cast<int64_t>(a.U[0]) * a.S[0] + static_cast<int64_t>(a.U[1]) * a.S[1];
-    if (a.S[worst] >= most || used + a.U[worst] > cap) break;
+    if (worst < 0 || used + a.U[worst] > cap) break;
     ++a.S[worst];
   }
   return kvq::launch_dependent(fn, dim3(a.U[0] * a.S[0] + a.U[1] * a.S[1]), kvq::kWarps * 32, 0, stream, &a);
