@@ -254,6 +254,7 @@ template <int NT>
 __device__ __forceinline__ void select_range(SelectSmem<NT>& sm, const float* x, int n, int want, int pos0, int32_t* out,
                                              float* xout) {
   if (n <= 4 * NT) select_in_registers<NT, 4>(sm, x, n, want, pos0, out, xout);
+  else if (n <= 8 * NT) select_in_registers<NT, 8>(sm, x, n, want, pos0, out, xout);
   else if (n <= 32 * NT) select_in_registers<NT, 32>(sm, x, n, want, pos0, out, xout);
   else select_from_memory(sm, x, n, want, pos0, out, xout);
 }

@@ -89,12 +89,12 @@ int64_t ws_bytes_of(const kvq_layout* L, int32_t n_q) {
   return kWsHead + static_cast<int64_t>(kMaxSplitCtas) * columns_of(L, n_q).N * (kD + 2) * 4;
 }
 
-const void* kernel_for(int kb, int vb) {
+const void* kernel_for(int kb, int vb, int G) {
   switch (kb) {
-    case 2: return tree_kernel_k2(vb);
-    case 4: return tree_kernel_k4(vb);
-    case 8: return tree_kernel_k8(vb);
-    case 16: return tree_kernel_k16(vb);
+    case 2: return tree_kernel_k2(vb, G);
+    case 4: return tree_kernel_k4(vb, G);
+    case 8: return tree_kernel_k8(vb, G);
+    case 16: return tree_kernel_k16(vb, G);
   }
   return nullptr;
 }
@@ -102,7 +102,7 @@ const void* kernel_for(int kb, int vb) {
 // Once per kernel and device: more than 48 KB of shared memory.
 kvq_status prepare(const void* fn) {
   static std::mutex mu;
-  static const void* done[64][16];
+  static const void* done[64][64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return kvq_cuda_fail(e);
@@ -199,7 +199,7 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
   const kvq::tree::Columns cols = kvq::tree::columns_of(L, n_q);
   const int64_t units = static_cast<int64_t>(L->d.B) * L->d.H_kv * cols.nblk;
   if (rows > 0x7fffffffLL || units > 0x7fffffffLL || static_cast<int64_t>(L->g) * n_q > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  const void* fn = kvq::tree::kernel_for(L->d.k_bits, L->d.v_bits);
+  const void* fn = kvq::tree::kernel_for(L->d.k_bits, L->d.v_bits, L->d.group_size);
   if (!fn) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;

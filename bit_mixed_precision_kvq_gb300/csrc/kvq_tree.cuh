@@ -228,26 +228,35 @@ __device__ __forceinline__ void k_codes(const uint4 (&r)[8], uint32_t (&c)[32]) 
   }
 }
 
-// Scale (fp16 bits) and zero of group g of a scale/zero row [z.., s..] of n groups.
-__device__ __forceinline__ uint32_t half_of(const uint4& r, int k) {
-  const uint32_t w = k < 4 ? (k < 2 ? r.x : r.y) : (k < 6 ? r.z : r.w);
-  return (k & 1) ? w >> 16 : w & 0xffffu;
+// Both halves of a half2 register as floats.
+__device__ __forceinline__ void h2_to_f2(uint32_t w, float& lo, float& hi) {
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ float f16_bits(uint32_t h) { return __half2float(__ushort_as_half(static_cast<uint16_t>(h))); }
 
 // A packed half V row, dequantised in order.
-template <int VB>
-__device__ __forceinline__ void v_values(const uint4 (&r)[8], const uint4& sz, int hf, int G, uint32_t (&o)[32]) {
-  const int ng = kD / G;
-  uint32_t s2[8], z2[8];  // of chunk kk
-#pragma unroll
-  for (int kk = 0; kk < 8; kk += 4) {  // a group is at least 4 chunks
-    const int g = (64 * hf + 8 * kk) / G;
-    const uint32_t s = half_of(sz, ng + g) * 0x10001u, z = half_of(sz, g) * 0x10001u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s2[kk + j] = s, z2[kk + j] = z;
+template <int VB, int G>
+__device__ __forceinline__ void v_values(const uint4 (&r)[8], const uint4& sz, int hf, uint32_t (&o)[32]) {
+  // scale and zero (twice in a word) of chunks 0 .. 3 and 4 .. 7: a group is
+  // at least 4 chunks
+  uint32_t s2[2], z2[2];
+  if constexpr (G == 32) {
+    const uint32_t z = hf ? sz.y : sz.x, s = hf ? sz.w : sz.z;
+    z2[0] = prmt(z, z, 0x1010u);
+    z2[1] = prmt(z, z, 0x3232u);
+    s2[0] = prmt(s, s, 0x1010u);
+    s2[1] = prmt(s, s, 0x3232u);
+  } else if constexpr (G == 64) {
+    const uint32_t sel = hf ? 0x3232u : 0x1010u;
+    z2[0] = z2[1] = prmt(sz.x, sz.x, sel);
+    s2[0] = s2[1] = prmt(sz.y, sz.y, sel);
+  } else {
+    z2[0] = z2[1] = prmt(sz.x, sz.x, 0x1010u);
+    s2[0] = s2[1] = prmt(sz.x, sz.x, 0x3232u);
   }
-  auto put = [&](int kk, int j, uint32_t c) { o[4 * kk + j] = hfma2_u(c, s2[kk], z2[kk]); };
+  auto put = [&](int kk, int j, uint32_t c) { o[4 * kk + j] = hfma2_u(c, s2[kk >> 2], z2[kk >> 2]); };
   if constexpr (VB == 2) {
     const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
 #pragma unroll
@@ -334,10 +343,11 @@ __device__ __forceinline__ Row row_of(const Args& a, const Source& s, int t) {
 }
 
 // The raw bytes of half hf of a packed row and its scale/zero row.
-__device__ __forceinline__ void load_sz(const uint8_t* p, int G, uint4& sz) {
-  if (G == 32) {
+template <int G>
+__device__ __forceinline__ void load_sz(const uint8_t* p, uint4& sz) {
+  if constexpr (G == 32) {
     sz = *reinterpret_cast<const uint4*>(p);
-  } else if (G == 64) {
+  } else if constexpr (G == 64) {
     const uint2 x = *reinterpret_cast<const uint2*>(p);
     sz.x = x.x;
     sz.y = x.y;
@@ -400,29 +410,46 @@ __device__ __forceinline__ void k_parts(const uint32_t (&c)[32], int t, const ui
     }
 }
 
-// The zero points' A row: z' / 2 as (high, low, high) of each group.
-template <int KB>
-__device__ __forceinline__ void z_parts(const uint4& sz, int G, uint32_t (&zz)[8]) {
-  const int ng = kD / G;
+// The zero points' A row: z' / 2 as (high, low, high) of each group, groups
+// in pairs (words 0-1, 2-3, 4-5); and s / 2 of the four 32-element blocks.
+template <int KB, int G>
+__device__ __forceinline__ void z_parts(const uint4& sz, uint32_t (&zz)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) zz[j] = 0u;
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    if (g < ng) {
-      const float z = 0.5f * fmaf(k_center<KB>(), f16_bits(half_of(sz, ng + g)), f16_bits(half_of(sz, g)));
-      const __half zh = __float2half_rn(z);
-      const uint32_t h = __half_as_ushort(zh), l = __half_as_ushort(__float2half_rn(z - __half2float(zh)));
-      zz[g >> 1] |= h << (16 * (g & 1));
-      zz[2 + (g >> 1)] |= l << (16 * (g & 1));
-      zz[4 + (g >> 1)] |= h << (16 * (g & 1));
-    }
+  for (int w = 0; w < (G == 32 ? 2 : 1); ++w) {
+    uint32_t z, t;
+    if constexpr (G == 32) z = w ? sz.y : sz.x, t = w ? sz.w : sz.z;
+    else if constexpr (G == 64) z = sz.x, t = sz.y;
+    else z = sz.x & 0xffffu, t = sz.x >> 16;
+    float z0, z1, s0, s1, h0, h1;
+    h2_to_f2(z, z0, z1);
+    h2_to_f2(t, s0, s1);
+    z0 = fmaf(0.5f * k_center<KB>(), s0, 0.5f * z0);
+    z1 = fmaf(0.5f * k_center<KB>(), s1, 0.5f * z1);
+    const uint32_t h = pack_f16x2(z0, z1);
+    h2_to_f2(h, h0, h1);
+    zz[w] = zz[4 + w] = h;
+    zz[2 + w] = pack_f16x2(z0 - h0, z1 - h1);
+  }
 }
-
-// s / 2 of the four 32-element blocks.
-__device__ __forceinline__ void k_scales(const uint4& sz, int G, uint32_t (&s2)[4]) {
-  const int ng = kD / G;
-#pragma unroll
-  for (int P = 0; P < 4; ++P) s2[P] = hmul2_u(half_of(sz, ng + 32 * P / G) * 0x10001u, 0x38003800u);
+template <int G>
+__device__ __forceinline__ void k_scales(const uint4& sz, uint32_t (&s2)[4]) {
+  constexpr uint32_t half = 0x38003800u;
+  if constexpr (G == 32) {
+    const uint32_t a = hmul2_u(sz.z, half), b = hmul2_u(sz.w, half);
+    s2[0] = prmt(a, a, 0x1010u);
+    s2[1] = prmt(a, a, 0x3232u);
+    s2[2] = prmt(b, b, 0x1010u);
+    s2[3] = prmt(b, b, 0x3232u);
+  } else if constexpr (G == 64) {
+    const uint32_t a = hmul2_u(sz.y, half);
+    s2[0] = s2[1] = prmt(a, a, 0x1010u);
+    s2[2] = s2[3] = prmt(a, a, 0x3232u);
+  } else {
+    const uint32_t a = hmul2_u(sz.x, half);
+    s2[0] = s2[1] = s2[2] = s2[3] = prmt(a, a, 0x3232u);
+  }
 }
 
 // The visual rows of tile i, K (key) or V: the bulk of a unit's bytes.
@@ -441,7 +468,7 @@ __device__ __forceinline__ void prefetch_tile(const Geom& c, const HeadRows& r, 
   }
 }
 
-template <int KB, int VB>
+template <int KB, int VB, int G>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -558,14 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if constexpr (KB < 16) {
         const int64_t x = i * kTile + pos - c.vs;
         load_k_packed<KB>(src.r.vis_k + x * c.krow, hf, kr);
-        load_sz(src.r.vis_ksz + x * c.kszrow, c.G, ksz);
+        load_sz<G>(src.r.vis_ksz + x * c.kszrow, ksz);
       }
     };
     auto load_v = [&](int i) {
       if constexpr (VB < 16) {
         const int64_t x = i * kTile + pos - c.vs;
         load_v_packed<VB>(src.r.vis_v + x * c.vrow, hf, vr);
-        load_sz(src.r.vis_vsz + x * c.vszrow, c.G, vsz);
+        load_sz<G>(src.r.vis_vsz + x * c.vszrow, vsz);
       }
     };
     if (i0 < i1 && all_visual(i0)) {
@@ -590,9 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if constexpr (KB < 16) {
           uint32_t cc[32], s2[4];
           k_codes<KB>(kr, cc);
-          k_scales(ksz, c.G, s2);
+          k_scales<G>(ksz, s2);
           uint32_t zz[8];
-          if (hf == 0) z_parts<KB>(ksz, c.G, zz);
+          if (hf == 0) z_parts<KB, G>(ksz, zz);
           if (next) load_k(i + 1);
           k_buffer();
 #pragma unroll
@@ -625,10 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (row.kind == kRowPacked) {
             uint4 sz = make_uint4(0u, 0u, 0u, 0u);
             load_k_packed<KB>(row.p, hf, raw);
-            load_sz(row.sz, c.G, sz);
+            load_sz<G>(row.sz, sz);
             k_codes<KB>(raw, cc);
-            k_scales(sz, c.G, s2);
-            if (hf == 0) z_parts<KB>(sz, c.G, zz);
+            k_scales<G>(sz, s2);
+            if (hf == 0) z_parts<KB, G>(sz, zz);
           }
         }
         if (kp && next) load_k(i + 1);
@@ -663,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       uint32_t o[32];
       if (vp && vis) {
         if constexpr (VB < 16) {
-          v_values<VB>(vr, vsz, hf, c.G, o);
+          v_values<VB, G>(vr, vsz, hf, o);
           if (next) load_v(i + 1);
         }
       } else {
@@ -681,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (row.kind == kRowPacked) {
             uint4 sz = make_uint4(0u, 0u, 0u, 0u);
             load_v_packed<VB>(row.p, hf, raw);
-            load_sz(row.sz, c.G, sz);
-            v_values<VB>(raw, sz, hf, c.G, o);
+            load_sz<G>(row.sz, sz);
+            v_values<VB, G>(raw, sz, hf, o);
             done = true;
           }
         }
@@ -736,7 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     named_bar(1, 128);
     if (tid < N) {
-      const int c = tid, ng = kD / a.c.G, per = 4 / ng;
+      constexpr int ng = kD / G, per = 4 / ng;
+      const int c = tid;
       uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
       for (int g = 0; g < 4; ++g)
@@ -794,106 +822,113 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int k = 0; k < 16; ++k)
           if (!((b >> k) & 1)) x[k] = -INFINITY;
       };
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int c0 = 0; c0 < N; c0 += 16) {
-        uint32_t s[16];
-        float x[16];
-        tmem_ld16(sb + c0, s);
-        tmem_ld_wait();
-        rel16(s, c0, x);
-        if (!whole) hide16(c0, x);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) top = fmaxf(top, x[k]);
-      }
-      if (bar_or(1, 128, top > kMaxGrowth)) {
-        // Some column's reference is too low (or unset): the columns that
-        // need it take their maximum over this tile.
-#pragma unroll 1
-        for (int c0 = 0; c0 < N; c0 += 16) {
-          uint32_t s[16];
-          float x[16];
-          tmem_ld16(sb + c0, s);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]) * sl2;
-          if (!whole) hide16(c0, x);
-          // maxima over the lanes of 16 columns: halve the columns a lane
-          // holds four times; lane bits 4 .. 1 end up naming the column
-#pragma unroll
-          for (int h = 8; h > 0; h >>= 1) {
-            const bool up = lane & (2 * h);
-#pragma unroll
-            for (int k = 0; k < h; ++k) {
-              const float give = up ? x[k] : x[k + h];
-              const float got = __shfl_xor_sync(0xffffffffu, give, 2 * h);
-              x[k] = fmaxf(up ? x[k + h] : x[k], got);
-            }
-          }
-          x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-          if (!(lane & 1)) sm.lsum[warp][c0 + (lane >> 1)] = x[0];
-        }
-        named_bar(1, 128);
-        if (tid < N) {
-          const float v = fmaxf(fmaxf(sm.lsum[0][tid], sm.lsum[1][tid]), fmaxf(sm.lsum[2][tid], sm.lsum[3][tid]));
-          const float old = sm.m[tid];
-          const bool move = v > old + kMaxGrowth;
-          sm.fac[tid] = move ? ex2(old - v) : 1.f;
-          if (move) sm.m[tid] = v;
-        }
-        named_bar(1, 128);
-        if (n > 0) {  // every earlier PV has landed before O is rescaled
-          wait_for(a, sm, &sm.pv_done[buf ^ 1], ((n - 1) >> 1) & 1);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < N; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(tm + lanes + kTmO + c0, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.fac[c0 + k]);
-            tmem_st16(tm + lanes + kTmO + c0, o);
-          }
-          tmem_st_wait();
-#pragma unroll
-          for (int c = 0; c < kMaxCols; ++c)
-            if (c < N) l[c] *= sm.fac[c];
-        }
-      }
       if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);  // P's buffer is free
       uint8_t* pt = sm.pt[buf] + (tid >> 3) * (16 * N) + (tid & 7) * 16;
-      uint32_t s[2][16];
-      tmem_ld16(sb, s[0]);
+      // Weights by the references as they are; if a score of some column is
+      // past its reference by more than kMaxGrowth, the references move and the
+      // tile is done again (always for the first tile, which sets them).
+      for (bool move = n == 0;; move = true) {
+        if (move) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < N; c0 += 16) {
+            uint32_t s[16];
+            float x[16];
+            tmem_ld16(sb + c0, s);
+            tmem_ld_wait();
 #pragma unroll
-      for (int c0 = 0; c0 < kMaxCols; c0 += 16)
-        if (c0 < N) {
-          const int cur = (c0 >> 4) & 1;
-          float x[16];
-          tmem_ld_wait();
-          if (c0 + 16 < N) {
-            tmem_ld16(sb + c0 + 16, s[cur ^ 1]);
-          } else {  // S is read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-          }
-          rel16(s[cur], c0, x);
-          if (!whole) hide16(c0, x);
-          uint32_t y[8];
+            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]) * sl2;
+            if (!whole) hide16(c0, x);
+            // maxima over the lanes of 16 columns: halve the columns a lane
+            // holds four times; lane bits 4 .. 1 end up naming the column
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float p0 = ex2(x[k]), p1 = ex2(x[k + 1]);
-            l[c0 + k] += p0;
-            l[c0 + k + 1] += p1;
-            y[k >> 1] = pack_f16x2(p0, p1);
+            for (int h = 8; h > 0; h >>= 1) {
+              const bool up = lane & (2 * h);
+#pragma unroll
+              for (int k = 0; k < h; ++k) {
+                const float give = up ? x[k] : x[k + h];
+                const float got = __shfl_xor_sync(0xffffffffu, give, 2 * h);
+                x[k] = fmaxf(up ? x[k + h] : x[k], got);
+              }
+            }
+            x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
+            if (!(lane & 1)) sm.lsum[warp][c0 + (lane >> 1)] = x[0];
           }
-          *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128 + 128) = make_uint4(y[4], y[5], y[6], y[7]);
+          named_bar(1, 128);
+          float v = -INFINITY, old = 0.f;
+          if (tid < N) {
+            v = fmaxf(fmaxf(sm.lsum[0][tid], sm.lsum[1][tid]), fmaxf(sm.lsum[2][tid], sm.lsum[3][tid]));
+            old = sm.m[tid];
+            // 2^-100 of a sum is nothing next to the new one, which is at least 1
+            sm.fac[tid] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - v) : 1.f);
+          }
+          named_bar(1, 128);
+          if (n > 0) {
+            // Undo what the tile added to the sums and rescale them; O, too,
+            // once every earlier PV has landed.
+            uint32_t s[16];
+#pragma unroll
+            for (int c0 = 0; c0 < kMaxCols; c0 += 16)
+              if (c0 < N) {
+                float x[16];
+                tmem_ld16(sb + c0, s);
+                tmem_ld_wait();
+                rel16(s, c0, x);
+                if (!whole) hide16(c0, x);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float f = sm.fac[c0 + k];
+                  l[c0 + k] = f == 0.f ? 0.f : (l[c0 + k] - ex2(x[k])) * f;
+                }
+              }
+            wait_for(a, sm, &sm.pv_done[buf ^ 1], ((n - 1) >> 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < N; c0 += 16) {
+              tmem_ld16(tm + lanes + kTmO + c0, s);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * sm.fac[c0 + k]);
+              tmem_st16(tm + lanes + kTmO + c0, s);
+            }
+            tmem_st_wait();
+            named_bar(1, 128);  // every thread is done with the old references
+          }
+          if (v > old + kMaxGrowth) sm.m[tid] = v;
+          named_bar(1, 128);
         }
+        float top = -INFINITY;
+        uint32_t s[2][16];
+        tmem_ld16(sb, s[0]);
+#pragma unroll
+        for (int c0 = 0; c0 < kMaxCols; c0 += 16)
+          if (c0 < N) {
+            const int cur = (c0 >> 4) & 1;
+            float x[16];
+            tmem_ld_wait();
+            if (c0 + 16 < N) tmem_ld16(sb + c0 + 16, s[cur ^ 1]);
+            rel16(s[cur], c0, x);
+            if (!whole) hide16(c0, x);
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              top = fmaxf(top, fmaxf(x[k], x[k + 1]));
+              const float p0 = ex2(x[k]), p1 = ex2(x[k + 1]);
+              l[c0 + k] += p0;
+              l[c0 + k + 1] += p1;
+              y[k >> 1] = pack_f16x2(p0, p1);
+            }
+            *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128 + 128) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+        if (!bar_or(1, 128, top > kMaxGrowth)) break;
+      }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+      if (lane == 0) {
+        mbar_arrive(&sm.s_free[buf]);
+        mbar_arrive(&sm.p_full[buf]);
+      }
     }
     // ---- the column sums over the lanes, then the outputs (thread = d) ----
     const int nd = i1 - i0;
@@ -968,10 +1003,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
 }
 
-const void* tree_kernel_k2(int vb);
-const void* tree_kernel_k4(int vb);
-const void* tree_kernel_k8(int vb);
-const void* tree_kernel_k16(int vb);
+const void* tree_kernel_k2(int vb, int G);
+const void* tree_kernel_k4(int vb, int G);
+const void* tree_kernel_k8(int vb, int G);
+const void* tree_kernel_k16(int vb, int G);
 
 }  // namespace tree
 }  // namespace kvq

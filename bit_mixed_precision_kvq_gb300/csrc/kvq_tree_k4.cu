@@ -1,15 +1,28 @@
 // Instantiations of the tree-attention kernel for K bit-width 4 (all V
-// widths); one translation unit per K width so that they compile in parallel.
+// widths and group sizes); one translation unit per K width so that they
+// compile in parallel.
 #include "kvq_tree.cuh"
 
 namespace kvq {
 namespace tree {
-const void* tree_kernel_k4(int vb) {
+namespace {
+template <int VB>
+const void* by_group(int G) {
+  switch (G) {
+    case 32: return reinterpret_cast<const void*>(&tree_kernel<4, VB, 32>);
+    case 64: return reinterpret_cast<const void*>(&tree_kernel<4, VB, 64>);
+    case 128: return reinterpret_cast<const void*>(&tree_kernel<4, VB, 128>);
+  }
+  return nullptr;
+}
+}  // namespace
+
+const void* tree_kernel_k4(int vb, int G) {
   switch (vb) {
-    case 2: return reinterpret_cast<const void*>(&tree_kernel<4, 2>);
-    case 4: return reinterpret_cast<const void*>(&tree_kernel<4, 4>);
-    case 8: return reinterpret_cast<const void*>(&tree_kernel<4, 8>);
-    case 16: return reinterpret_cast<const void*>(&tree_kernel<4, 16>);
+    case 2: return by_group<2>(G);
+    case 4: return by_group<4>(G);
+    case 8: return by_group<8>(G);
+    case 16: return by_group<16>(G);
   }
   return nullptr;
 }
