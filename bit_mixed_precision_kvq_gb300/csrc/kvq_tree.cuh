@@ -31,10 +31,10 @@
 // all lanes at once, when a score of a tile exceeds it by more than 2^12
 // (P <= 4096 in fp16); the column sums stay in the threads until the end.
 //
-// CTA = 13 warps: 0-3 softmax (TMEM lanes 32 w ..), 4-11 unpack (warp w: lanes
-// 32 (w mod 4) .., half (w - 4) / 4 of the row), 12 issues the MMAs.  TMEM: two
-// K buffers (64 columns high, 64 low, 8 zero points), two S buffers of 64, O
-// of 64.
+// CTA = 17 warps: 0-7 softmax (warp w: TMEM lanes 32 (w mod 4) .., half w / 4 of
+// the columns), 8-15 unpack (lanes 32 (w mod 4) .., half (w - 8) / 4 of the row),
+// 16 issues the MMAs.  TMEM: two K buffers (64 columns high, 64 low, 8 zero
+// points), two S buffers of 64, O of 64.
 #pragma once
 
 #include "kvq_geom.cuh"
@@ -43,11 +43,14 @@
 namespace kvq {
 namespace tree {
 
-constexpr int kThreads = 416;
-constexpr int kMmaWarp = 12;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kMmaWarp = 16;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kAhead = 4;               // tiles that the L2 prefetch runs ahead
 constexpr int kTile = 128;              // positions per tile (TMEM lanes)
 constexpr int kMaxCols = 64;            // columns per unit (at most)
+constexpr int kHalfCols = kMaxCols / 2;  // columns of a softmax thread
 constexpr int kMaxSplitCtas = 160;      // CTAs of a call whose units are split (workspace slots)
 constexpr float kMaxGrowth = 12.f;      // log2 of the largest P
 constexpr float kUnset = -1e30f;        // reference of a column that has attended nothing
@@ -177,54 +180,41 @@ __device__ __forceinline__ constexpr float k_center() {
   return KB == 2 ? 1.f : (KB == 4 ? 8.f : 128.f);
 }
 
-// c' of the 32 pairs of a half K row.
+// c' of the 16 pairs (4 P + i) of slice t of a K row, from its words.
 template <int KB>
-__device__ __forceinline__ void k_codes(const uint4 (&r)[8], uint32_t (&c)[32]) {
+__device__ __forceinline__ void k_codes(const uint32_t* x, uint32_t (&c)[16]) {
   constexpr float off = k_center<KB>();
   if constexpr (KB == 2) {
-    const uint32_t x[4] = {r[0].x, r[0].y, r[0].z, r[0].w};  // word 2 (t & 1) + i / 2
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w = x[2 * t + h], y = w >> 6;
-        uint32_t* o = c + 16 * t + 2 * h;  // i = 2 h, 2 h + 1
-        o[0] = code_at<8>(w, 0x00030003u, off);
-        o[1] = code_at<8>(y, 0x00030003u, off);
-        o[4] = code_at<6>(w, 0x00030003u, off);
-        o[5] = code_at<6>(y, 0x00030003u, off);
-        o[8] = code_at<4>(w, 0x00030003u, off);
-        o[9] = code_at<4>(y, 0x00030003u, off);
-        o[12] = code_at<0>(w, 0x00030003u, off);
-        o[13] = code_at<2>(w, 0x00030003u, off);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = x[h], y = w >> 6;
+      uint32_t* o = c + 2 * h;  // i = 2 h, 2 h + 1
+      o[0] = code_at<8>(w, 0x00030003u, off);
+      o[1] = code_at<8>(y, 0x00030003u, off);
+      o[4] = code_at<6>(w, 0x00030003u, off);
+      o[5] = code_at<6>(y, 0x00030003u, off);
+      o[8] = code_at<4>(w, 0x00030003u, off);
+      o[9] = code_at<4>(y, 0x00030003u, off);
+      o[12] = code_at<0>(w, 0x00030003u, off);
+      o[13] = code_at<2>(w, 0x00030003u, off);
+    }
   } else if constexpr (KB == 4) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t x[4] = {r[t].x, r[t].y, r[t].z, r[t].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = x[i], y = w >> 8;
-        uint32_t* o = c + 16 * t + i;
-        o[0] = code_at<0>(w, 0x000F000Fu, off);
-        o[4] = code_at<4>(w, 0x000F000Fu, off);
-        o[8] = code_at<0>(y, 0x000F000Fu, off);
-        o[12] = code_at<4>(y, 0x000F000Fu, off);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = x[i], y = w >> 8;
+      c[i] = code_at<0>(w, 0x000F000Fu, off);
+      c[4 + i] = code_at<4>(w, 0x000F000Fu, off);
+      c[8 + i] = code_at<0>(y, 0x000F000Fu, off);
+      c[12 + i] = code_at<4>(y, 0x000F000Fu, off);
     }
   } else if constexpr (KB == 8) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t x[8] = {r[2 * t].x,     r[2 * t].y,     r[2 * t].z,     r[2 * t].w,
-                             r[2 * t + 1].x, r[2 * t + 1].y, r[2 * t + 1].z, r[2 * t + 1].w};
+    for (int P = 0; P < 4; ++P)
 #pragma unroll
-      for (int P = 0; P < 4; ++P)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = x[2 * P + (i >> 1)];
-          c[16 * t + 4 * P + i] = code_at<0>((i & 1) ? w >> 8 : w, 0x00FF00FFu, off);
-        }
-    }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = x[2 * P + (i >> 1)];
+        c[4 * P + i] = code_at<0>((i & 1) ? w >> 8 : w, 0x00FF00FFu, off);
+      }
   }
 }
 
@@ -236,65 +226,56 @@ __device__ __forceinline__ void h2_to_f2(uint32_t w, float& lo, float& hi) {
 }
 __device__ __forceinline__ float f16_bits(uint32_t h) { return __half2float(__ushort_as_half(static_cast<uint16_t>(h))); }
 
-// A packed half V row, dequantised in order.
-template <int VB, int G>
-__device__ __forceinline__ void v_values(const uint4 (&r)[8], const uint4& sz, int hf, uint32_t (&o)[32]) {
-  // scale and zero (twice in a word) of chunks 0 .. 3 and 4 .. 7: a group is
-  // at least 4 chunks
-  uint32_t s2[2], z2[2];
+// Scale and zero (twice in a word) of chunks 4 e .. 4 e + 3 of half hf of a V
+// row: a group is at least 4 chunks.
+template <int G>
+__device__ __forceinline__ void v_scales(const uint4& sz, int hf, int e, uint32_t& s2, uint32_t& z2) {
   if constexpr (G == 32) {
-    const uint32_t z = hf ? sz.y : sz.x, s = hf ? sz.w : sz.z;
-    z2[0] = prmt(z, z, 0x1010u);
-    z2[1] = prmt(z, z, 0x3232u);
-    s2[0] = prmt(s, s, 0x1010u);
-    s2[1] = prmt(s, s, 0x3232u);
+    const uint32_t z = hf ? sz.y : sz.x, s = hf ? sz.w : sz.z, sel = e ? 0x3232u : 0x1010u;
+    z2 = prmt(z, z, sel);
+    s2 = prmt(s, s, sel);
   } else if constexpr (G == 64) {
     const uint32_t sel = hf ? 0x3232u : 0x1010u;
-    z2[0] = z2[1] = prmt(sz.x, sz.x, sel);
-    s2[0] = s2[1] = prmt(sz.y, sz.y, sel);
+    z2 = prmt(sz.x, sz.x, sel);
+    s2 = prmt(sz.y, sz.y, sel);
   } else {
-    z2[0] = z2[1] = prmt(sz.x, sz.x, 0x1010u);
-    s2[0] = s2[1] = prmt(sz.x, sz.x, 0x3232u);
+    z2 = prmt(sz.x, sz.x, 0x1010u);
+    s2 = prmt(sz.x, sz.x, 0x3232u);
   }
-  auto put = [&](int kk, int j, uint32_t c) { o[4 * kk + j] = hfma2_u(c, s2[kk >> 2], z2[kk >> 2]); };
-  if constexpr (VB == 2) {
-    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+}
+// Chunks 4 e .. 4 e + 3 of half hf of a packed V row, dequantised in order;
+// w: the words loaded by load_v_packed.
+template <int VB>
+__device__ __forceinline__ void v_values(const uint32_t* w, int hf, int e, uint32_t s2, uint32_t z2, uint32_t (&o)[16]) {
+  auto put = [&](int kk, int j, uint32_t c) { o[4 * kk + j] = hfma2_u(c, s2, z2); };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; ++j) {  // elements 2 j, 2 j + 1 of every chunk
+    if constexpr (VB == 2) {
       const uint32_t x = prmt(w[2 * j], w[2 * j + 1], hf ? 0x7632u : 0x5410u), y = x >> 6;
-      put(0, j, code_at<0>(x, 0x00030003u, 0.f));
-      put(1, j, code_at<2>(x, 0x00030003u, 0.f));
-      put(2, j, code_at<4>(x, 0x00030003u, 0.f));
-      put(3, j, code_at<6>(x, 0x00030003u, 0.f));
-      put(4, j, code_at<8>(x, 0x00030003u, 0.f));
-      put(5, j, code_at<4>(y, 0x00030003u, 0.f));
-      put(6, j, code_at<6>(y, 0x00030003u, 0.f));
-      put(7, j, code_at<8>(y, 0x00030003u, 0.f));
-    }
-  } else if constexpr (VB == 4) {
-    // word 2 n + hf
-    const uint32_t w[8] = {hf ? r[0].y : r[0].x, hf ? r[0].w : r[0].z, hf ? r[1].y : r[1].x, hf ? r[1].w : r[1].z,
-                           hf ? r[2].y : r[2].x, hf ? r[2].w : r[2].z, hf ? r[3].y : r[3].x, hf ? r[3].w : r[3].z};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t x = prmt(w[2 * j], w[2 * j + 1], e ? 0x7632u : 0x5410u), y = x >> 8;
-        put(4 * e, j, code_at<0>(x, 0x000F000Fu, 0.f));
-        put(4 * e + 1, j, code_at<4>(x, 0x000F000Fu, 0.f));
-        put(4 * e + 2, j, code_at<0>(y, 0x000F000Fu, 0.f));
-        put(4 * e + 3, j, code_at<4>(y, 0x000F000Fu, 0.f));
+      if (e == 0) {
+        put(0, j, code_at<0>(x, 0x00030003u, 0.f));
+        put(1, j, code_at<2>(x, 0x00030003u, 0.f));
+        put(2, j, code_at<4>(x, 0x00030003u, 0.f));
+        put(3, j, code_at<6>(x, 0x00030003u, 0.f));
+      } else {
+        put(0, j, code_at<8>(x, 0x00030003u, 0.f));
+        put(1, j, code_at<4>(y, 0x00030003u, 0.f));
+        put(2, j, code_at<6>(y, 0x00030003u, 0.f));
+        put(3, j, code_at<8>(y, 0x00030003u, 0.f));
       }
-  } else if constexpr (VB == 8) {
-    // words 4 n + 2 hf, + 1: r[n / 2] holds the pairs of n even and odd
+    } else if constexpr (VB == 4) {  // words 2 n + hf
+      const uint32_t a = hf ? w[4 * j + 1] : w[4 * j], b = hf ? w[4 * j + 3] : w[4 * j + 2];
+      const uint32_t x = prmt(a, b, e ? 0x7632u : 0x5410u), y = x >> 8;
+      put(0, j, code_at<0>(x, 0x000F000Fu, 0.f));
+      put(1, j, code_at<4>(x, 0x000F000Fu, 0.f));
+      put(2, j, code_at<0>(y, 0x000F000Fu, 0.f));
+      put(3, j, code_at<4>(y, 0x000F000Fu, 0.f));
+    } else if constexpr (VB == 8) {  // words 4 n + 2 hf, + 1, as pairs of n
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t wa[2] = {r[j].x, r[j].y}, wb[2] = {r[j].z, r[j].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {  // half-words: chunks 2 e, 2 e + 1
-        const uint32_t x = prmt(wa[e >> 1], wb[e >> 1], (e & 1) ? 0x7632u : 0x5410u);
-        put(2 * e, j, code_at<0>(x, 0x00FF00FFu, 0.f));
-        put(2 * e + 1, j, code_at<0>(x >> 8, 0x00FF00FFu, 0.f));
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t x = prmt(w[4 * j + e], w[4 * j + 2 + e], k ? 0x7632u : 0x5410u);
+        put(2 * k, j, code_at<0>(x, 0x00FF00FFu, 0.f));
+        put(2 * k + 1, j, code_at<0>(x >> 8, 0x00FF00FFu, 0.f));
       }
     }
   }
@@ -355,25 +336,34 @@ __device__ __forceinline__ void load_sz(const uint8_t* p, uint4& sz) {
     sz.x = *reinterpret_cast<const uint32_t*>(p);
   }
 }
-template <int KB>
-__device__ __forceinline__ void load_k_packed(const uint8_t* row, int hf, uint4 (&r)[8]) {
-  const uint4* p = reinterpret_cast<const uint4*>(row + hf * 8 * KB);
+template <int N4>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {  // N4 x 16 bytes
 #pragma unroll
-  for (int i = 0; i < KB / 2; ++i) r[i] = p[i];
+  for (int i = 0; i < N4; ++i) {
+    const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+    w[4 * i] = x.x;
+    w[4 * i + 1] = x.y;
+    w[4 * i + 2] = x.z;
+    w[4 * i + 3] = x.w;
+  }
 }
+// Half hf of a packed K row: KB words for slice 2 hf, KB for slice 2 hf + 1.
+template <int KB>
+__device__ __forceinline__ void load_k_packed(const uint8_t* row, int hf, uint32_t* w) {
+  load_words<KB / 2>(row + hf * 8 * KB, w);
+}
+// What half hf of a packed V row needs: 4 VB words (16 for VB = 8).
 template <int VB>
-__device__ __forceinline__ void load_v_packed(const uint8_t* row, int hf, uint4 (&r)[8]) {
+__device__ __forceinline__ void load_v_packed(const uint8_t* row, int hf, uint32_t* w) {
   if constexpr (VB == 8) {
 #pragma unroll
-    for (int n = 0; n < 8; n += 2) {
+    for (int n = 0; n < 8; ++n) {
       const uint2 x = *reinterpret_cast<const uint2*>(row + 16 * n + 8 * hf);
-      const uint2 y = *reinterpret_cast<const uint2*>(row + 16 * n + 16 + 8 * hf);
-      r[n / 2] = make_uint4(x.x, x.y, y.x, y.y);
+      w[2 * n] = x.x;
+      w[2 * n + 1] = x.y;
     }
   } else {
-    const uint4* p = reinterpret_cast<const uint4*>(row);
-#pragma unroll
-    for (int i = 0; i < VB; ++i) r[i] = p[i];
+    load_words<VB>(row, w);
   }
 }
 
@@ -395,17 +385,15 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// c' -> the high (and low) fp16 parts of c' s / 2 for 16 pairs of slice t of a
-// half K row (c holds both slices' c').
+// c' -> the high (and low) fp16 parts of c' s / 2, in place and in lo.
 template <int KB>
-__device__ __forceinline__ void k_parts(const uint32_t (&c)[32], int t, const uint32_t (&s2)[4], uint32_t (&hi)[16],
-                                        uint32_t (&lo)[16]) {
+__device__ __forceinline__ void k_parts(uint32_t (&c)[16], const uint32_t (&s2)[4], uint32_t (&lo)[16]) {
 #pragma unroll
   for (int P = 0; P < 4; ++P)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t x = c[16 * t + 4 * P + j], h = hmul2_u(x, s2[P]);
-      hi[4 * P + j] = h;
+      const uint32_t x = c[4 * P + j], h = hmul2_u(x, s2[P]);
+      c[4 * P + j] = h;
       if constexpr (KB > 2) lo[4 * P + j] = hfma2_u(x, s2[P], h ^ 0x80008000u);
     }
 }
@@ -479,11 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init(&sm.k_free[i], 1);
       mbar_init(&sm.v_full[i], 8);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_free[i], 4);
-      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.s_free[i], kSoftmaxWarps);
+      mbar_init(&sm.p_full[i], kSoftmaxWarps);
       mbar_init(&sm.pv_done[i], 1);
     }
-    mbar_init(&sm.q_ready, 4);
+    mbar_init(&sm.q_ready, kSoftmaxWarps);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -554,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (n > 0) issue_pv(n - 1);
     }
     if (i0 < i1) issue_pv(i1 - i0 - 1);
-  } else if (warp >= 4) {
+  } else if (warp >= kSoftmaxWarps) {
     // ---------------- unpack ----------------
-    const int hf = (warp - 4) >> 2, pos = 32 * (warp & 3) + lane;
+    const int hf = (warp - kSoftmaxWarps) >> 2, pos = 32 * (warp & 3) + lane;
     const Geom& c = a.c;
     Source src;
     src.r = head_rows(c, w.b, w.h);
@@ -575,12 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       src.any = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x))) |
                 (static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x >> 32))) << 32);
     }
-    // All 32 rows of this warp in tile i are packed ones (the same for K and
-    // V of the head: a K-only head has packed V rows alone).
+    // All 32 rows of this warp in tile i are visual ones.
     const int first = 32 * (warp & 3), vend = min(c.ve, src.len);
     auto all_visual = [&](int i) { return i * kTile + first >= c.vs && i * kTile + first + 32 <= vend; };
     const bool kp = KB < 16 && src.r.k_packed, vp = VB < 16 && src.r.v_packed;
-    uint4 kr[8], vr[8], ksz = make_uint4(0, 0, 0, 0), vsz = ksz;
+    // the next tile's packed half rows, loaded while this one is unpacked
+    constexpr int KW = KB < 16 ? 2 * KB : 2, VW = VB == 8 ? 16 : (VB < 16 ? 4 * VB : 2);
+    uint32_t kr[KW], vr[VW];
+    uint4 ksz = make_uint4(0, 0, 0, 0), vsz = ksz;
     auto load_k = [&](int i) {
       if constexpr (KB < 16) {
         const int64_t x = i * kTile + pos - c.vs;
@@ -606,139 +596,136 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (fetch && i + kAhead < i1) prefetch_tile(c, src.r, i + kAhead, src.len, hf == 0);
       // ---- K: registers -> TMEM ----
       const uint32_t kt = tm + lanes + kTmK + buf * kTmKStride + 32 * hf;
-      auto k_buffer = [&]() {
-        if (n >= 2) {
-          wait_for(a, sm, &sm.k_free[buf], ((n - 2) >> 1) & 1);
-          tc_fence_after();
-        }
-      };
-      uint32_t hi[16], lo[16];
+      if (n >= 2) {
+        wait_for(a, sm, &sm.k_free[buf], ((n - 2) >> 1) & 1);
+        tc_fence_after();
+      }
       if (kp && vis) {
         if constexpr (KB < 16) {
-          uint32_t cc[32], s2[4];
-          k_codes<KB>(kr, cc);
+          uint32_t s2[4];
           k_scales<G>(ksz, s2);
-          uint32_t zz[8];
-          if (hf == 0) z_parts<KB, G>(ksz, zz);
-          if (next) load_k(i + 1);
-          k_buffer();
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            k_parts<KB>(cc, t, s2, hi, lo);
+            uint32_t hi[16], lo[16];
+            k_codes<KB>(kr + t * KB, hi);
+            k_parts<KB>(hi, s2, lo);
             tmem_st16(kt + 16 * t, hi);
             if constexpr (KB > 2) tmem_st16(kt + kTmLo + 16 * t, lo);
           }
-          if (hf == 0) tmem_st8(kt + kTmZ, zz);
+          if (hf == 0) {
+            uint32_t zz[8];
+            z_parts<KB, G>(ksz, zz);
+            tmem_st8(kt + kTmZ, zz);
+          }
         }
       } else {
         const Row row = row_of<true>(a, src, i * kTile + pos);
         const bool packed = has_packed(i);
-        uint32_t zz[8], s2[4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) zz[j] = 0u;
-        uint32_t cc[32];
-        uint4 raw[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (row.kind == kRowBf16) {  // d = 32 P + 16 hf .. + 15
-#pragma unroll
-          for (int P = 0; P < 4; ++P) {
-            const uint4* p = reinterpret_cast<const uint4*>(row.p + 64 * P + 32 * hf);
-            raw[2 * P] = p[0];
-            raw[2 * P + 1] = p[1];
-          }
-        }
-        if constexpr (KB < 16) {
-          if (row.kind == kRowPacked) {
-            uint4 sz = make_uint4(0u, 0u, 0u, 0u);
-            load_k_packed<KB>(row.p, hf, raw);
-            load_sz<G>(row.sz, sz);
-            k_codes<KB>(raw, cc);
-            k_scales<G>(sz, s2);
-            if (hf == 0) z_parts<KB, G>(sz, zz);
-          }
-        }
-        if (kp && next) load_k(i + 1);
-        k_buffer();
+        uint4 sz = make_uint4(0u, 0u, 0u, 0u);
+        if (KB < 16 && row.kind == kRowPacked) load_sz<G>(row.sz, sz);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
+          uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) lo[j] = 0u;
-          if (KB < 16 && row.kind == kRowPacked) {
-            if constexpr (KB < 16) k_parts<KB>(cc, t, s2, hi, lo);
-          } else {
+          for (int j = 0; j < 16; ++j) hi[j] = lo[j] = 0u;
+          if (row.kind == kRowBf16) {  // d = 32 P + 16 hf + 8 t .. + 7
+            uint4 raw[4];
+#pragma unroll
+            for (int P = 0; P < 4; ++P) raw[P] = *reinterpret_cast<const uint4*>(row.p + 64 * P + 32 * hf + 16 * t);
 #pragma unroll
             for (int P = 0; P < 4; ++P) {
-              const uint4 x = raw[2 * P + t];
-              hi[4 * P] = pack_f16x2(0.5f * bf16_lo(x.x), 0.5f * bf16_lo(x.z));
-              hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(x.x), 0.5f * bf16_hi(x.z));
-              hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(x.y), 0.5f * bf16_lo(x.w));
-              hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(x.y), 0.5f * bf16_hi(x.w));
+              hi[4 * P] = pack_f16x2(0.5f * bf16_lo(raw[P].x), 0.5f * bf16_lo(raw[P].z));
+              hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(raw[P].x), 0.5f * bf16_hi(raw[P].z));
+              hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(raw[P].y), 0.5f * bf16_lo(raw[P].w));
+              hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(raw[P].y), 0.5f * bf16_hi(raw[P].w));
+            }
+          }
+          if constexpr (KB < 16) {
+            if (row.kind == kRowPacked) {
+              uint32_t s2[4], raw[2 * KB];
+              load_k_packed<KB>(row.p, hf, raw);
+              k_scales<G>(sz, s2);
+              k_codes<KB>(raw + t * KB, hi);
+              k_parts<KB>(hi, s2, lo);
             }
           }
           __syncwarp();
           tmem_st16(kt + 16 * t, hi);
           if (KB > 2 && packed) tmem_st16(kt + kTmLo + 16 * t, lo);
         }
-        if (packed && hf == 0) tmem_st8(kt + kTmZ, zz);
+        if (packed && hf == 0) {
+          uint32_t zz[8];
+          if constexpr (KB < 16) z_parts<KB, G>(sz, zz);  // zeros for a bf16 row
+          tmem_st8(kt + kTmZ, zz);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[buf]);
+      if (kp && next) load_k(i + 1);
       // ---- V: registers -> shared memory ----
-      uint32_t o[32];
+      if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);
+      uint8_t* vt = sm.vt[buf] + (pos >> 3) * 2048 + (pos & 7) * 16 + 1024 * hf;
+      auto put_v = [&](int e, const uint32_t (&o)[16]) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          *reinterpret_cast<uint4*>(vt + 512 * e + 128 * kk) =
+              make_uint4(o[4 * kk], o[4 * kk + 1], o[4 * kk + 2], o[4 * kk + 3]);
+      };
       if (vp && vis) {
         if constexpr (VB < 16) {
-          v_values<VB, G>(vr, vsz, hf, o);
-          if (next) load_v(i + 1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t s2, z2, o[16];
+            v_scales<G>(vsz, hf, e, s2, z2);
+            v_values<VB>(vr, hf, e, s2, z2, o);
+            put_v(e, o);
+          }
         }
       } else {
         const Row row = row_of<false>(a, src, i * kTile + pos);
-        uint4 raw[8];
+        uint4 sz = make_uint4(0u, 0u, 0u, 0u);
+        if (VB < 16 && row.kind == kRowPacked) load_sz<G>(row.sz, sz);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (row.kind == kRowBf16) {
-          const uint4* p = reinterpret_cast<const uint4*>(row.p + 128 * hf);
+        for (int e = 0; e < 2; ++e) {
+          uint32_t o[16];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) raw[j] = p[j];
-        }
-        bool done = false;
-        if constexpr (VB < 16) {
-          if (row.kind == kRowPacked) {
-            uint4 sz = make_uint4(0u, 0u, 0u, 0u);
-            load_v_packed<VB>(row.p, hf, raw);
-            load_sz<G>(row.sz, sz);
-            v_values<VB, G>(raw, sz, hf, o);
-            done = true;
+          for (int j = 0; j < 16; ++j) o[j] = 0u;
+          if (row.kind == kRowBf16) {
+            uint4 raw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw[j] = *reinterpret_cast<const uint4*>(row.p + 128 * hf + 64 * e + 16 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[4 * j] = bf16x2_to_f16x2(raw[j].x);
+              o[4 * j + 1] = bf16x2_to_f16x2(raw[j].y);
+              o[4 * j + 2] = bf16x2_to_f16x2(raw[j].z);
+              o[4 * j + 3] = bf16x2_to_f16x2(raw[j].w);
+            }
           }
-        }
-        if (!done) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o[4 * j] = bf16x2_to_f16x2(raw[j].x);
-            o[4 * j + 1] = bf16x2_to_f16x2(raw[j].y);
-            o[4 * j + 2] = bf16x2_to_f16x2(raw[j].z);
-            o[4 * j + 3] = bf16x2_to_f16x2(raw[j].w);
+          if constexpr (VB < 16) {
+            if (row.kind == kRowPacked) {
+              uint32_t s2, z2, raw[VW];
+              load_v_packed<VB>(row.p, hf, raw);
+              v_scales<G>(sz, hf, e, s2, z2);
+              v_values<VB>(raw, hf, e, s2, z2, o);
+            }
           }
+          put_v(e, o);
         }
-        if (vp && next) load_v(i + 1);
       }
-      if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);
-      uint8_t* vt = sm.vt[buf] + (pos >> 3) * 2048 + (pos & 7) * 16 + 1024 * hf;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        *reinterpret_cast<uint4*>(vt + 128 * kk) = make_uint4(o[4 * kk], o[4 * kk + 1], o[4 * kk + 2], o[4 * kk + 3]);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[buf]);
+      if (vp && next) load_v(i + 1);
     }
   } else {
     // ---------------- softmax ----------------
     const int tid = threadIdx.x;
     // q into shared memory: 16-byte chunk ch (8 d) of a column's row goes to
     // chunk 4 t + P of the permuted order; the sums of the 32-element blocks
-    for (int x = tid; x < N * 4; x += 128) {
+    for (int x = tid; x < N * 4; x += kSoftmaxThreads) {
       const int c = x >> 2, P = x & 3;
       const bool ok = c < ncols;
       const int cg = col0 + c, tok = cg / a.c.g;
@@ -761,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       sm.qs[c][P] = sum;
     }
-    named_bar(1, 128);
+    named_bar(1, kSoftmaxThreads);
     if (tid < N) {
       constexpr int ng = kD / G, per = 4 / ng;
       const int c = tid;
@@ -784,23 +771,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       sm.m[c] = kUnset;
     }
     fence_async_smem();  // the tensor cores read q
-    named_bar(1, 128);
+    named_bar(1, kSoftmaxThreads);
     if (lane == 0) mbar_arrive(&sm.q_ready);
 
     const float sl2 = a.scale_log2 * kOperandScale;
-    float l[kMaxCols];
+    // this thread's position of a tile (a TMEM lane) and its columns [ch, ce)
+    const int lp = 32 * (warp & 3) + lane;
+    const int ch = (N / 2 + 15) / 16 * 16 * (warp >> 2), ce = warp < 4 ? min(N, (N / 2 + 15) / 16 * 16) : N;
+    float l[kHalfCols];
 #pragma unroll
-    for (int c = 0; c < kMaxCols; ++c) l[c] = 0.f;
+    for (int c = 0; c < kHalfCols; ++c) l[c] = 0.f;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
-      const int t = i * kTile + tid;  // this thread's position
+      const int t = i * kTile + lp;
       // bit c: column c attends it
       uint64_t sees = t < len ? ~0ull : 0ull;
       const bool whole = (i + 1) * kTile <= len;
       if (t >= len && t < len + a.n_q) {
 #pragma unroll 1
-        for (int c = 0; c < N; ++c) sees |= ((sm.colmask[c] >> (t - len)) & 1) << c;
+        for (int c = ch; c < ce; ++c) sees |= ((sm.colmask[c] >> (t - len)) & 1) << c;
       }
       const uint32_t sb = tm + lanes + kTmS + buf * kTmSStride;
       wait_for(a, sm, &sm.s_full[buf], (n >> 1) & 1);
@@ -823,14 +813,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (!((b >> k) & 1)) x[k] = -INFINITY;
       };
       if (n >= 2) wait_for(a, sm, &sm.pv_done[buf], ((n - 2) >> 1) & 1);  // P's buffer is free
-      uint8_t* pt = sm.pt[buf] + (tid >> 3) * (16 * N) + (tid & 7) * 16;
+      uint8_t* pt = sm.pt[buf] + (lp >> 3) * (16 * N) + (lp & 7) * 16 + 16 * ch;
       // Weights by the references as they are; if a score of some column is
       // past its reference by more than kMaxGrowth, the references move and the
       // tile is done again (always for the first tile, which sets them).
       for (bool move = n == 0;; move = true) {
         if (move) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < N; c0 += 16) {
+          for (int c0 = ch; c0 < ce; c0 += 16) {
             uint32_t s[16];
             float x[16];
             tmem_ld16(sb + c0, s);
@@ -851,9 +841,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               }
             }
             x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-            if (!(lane & 1)) sm.lsum[warp][c0 + (lane >> 1)] = x[0];
+            if (!(lane & 1)) sm.lsum[warp & 3][c0 + (lane >> 1)] = x[0];
           }
-          named_bar(1, 128);
+          named_bar(1, kSoftmaxThreads);
           float v = -INFINITY, old = 0.f;
           if (tid < N) {
             v = fmaxf(fmaxf(sm.lsum[0][tid], sm.lsum[1][tid]), fmaxf(sm.lsum[2][tid], sm.lsum[3][tid]));
@@ -861,29 +851,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             // 2^-100 of a sum is nothing next to the new one, which is at least 1
             sm.fac[tid] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - v) : 1.f);
           }
-          named_bar(1, 128);
+          named_bar(1, kSoftmaxThreads);
           if (n > 0) {
             // Undo what the tile added to the sums and rescale them; O, too,
             // once every earlier PV has landed.
             uint32_t s[16];
 #pragma unroll
-            for (int c0 = 0; c0 < kMaxCols; c0 += 16)
-              if (c0 < N) {
+            for (int c0 = 0; c0 < kHalfCols; c0 += 16)
+              if (ch + c0 < ce) {
                 float x[16];
-                tmem_ld16(sb + c0, s);
+                tmem_ld16(sb + ch + c0, s);
                 tmem_ld_wait();
-                rel16(s, c0, x);
-                if (!whole) hide16(c0, x);
+                rel16(s, ch + c0, x);
+                if (!whole) hide16(ch + c0, x);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                  const float f = sm.fac[c0 + k];
+                  const float f = sm.fac[ch + c0 + k];
                   l[c0 + k] = f == 0.f ? 0.f : (l[c0 + k] - ex2(x[k])) * f;
                 }
               }
             wait_for(a, sm, &sm.pv_done[buf ^ 1], ((n - 1) >> 1) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < N; c0 += 16) {
+            for (int c0 = ch; c0 < ce; c0 += 16) {
               tmem_ld16(tm + lanes + kTmO + c0, s);
               tmem_ld_wait();
 #pragma unroll
@@ -891,23 +881,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               tmem_st16(tm + lanes + kTmO + c0, s);
             }
             tmem_st_wait();
-            named_bar(1, 128);  // every thread is done with the old references
+            named_bar(1, kSoftmaxThreads);  // every thread is done with the old references
           }
           if (v > old + kMaxGrowth) sm.m[tid] = v;
-          named_bar(1, 128);
+          named_bar(1, kSoftmaxThreads);
         }
         float top = -INFINITY;
         uint32_t s[2][16];
-        tmem_ld16(sb, s[0]);
+        if (ch < ce) tmem_ld16(sb + ch, s[0]);
+        if (ch + 16 < ce) tmem_ld16(sb + ch + 16, s[1]);
+        tmem_ld_wait();
 #pragma unroll
-        for (int c0 = 0; c0 < kMaxCols; c0 += 16)
-          if (c0 < N) {
-            const int cur = (c0 >> 4) & 1;
+        for (int c0 = 0; c0 < kHalfCols; c0 += 16)
+          if (ch + c0 < ce) {
             float x[16];
-            tmem_ld_wait();
-            if (c0 + 16 < N) tmem_ld16(sb + c0 + 16, s[cur ^ 1]);
-            rel16(s[cur], c0, x);
-            if (!whole) hide16(c0, x);
+            rel16(s[c0 >> 4], ch + c0, x);
+            if (!whole) hide16(ch + c0, x);
             uint32_t y[8];
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
@@ -920,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128 + 128) = make_uint4(y[4], y[5], y[6], y[7]);
           }
-        if (!bar_or(1, 128, top > kMaxGrowth)) break;
+        if (!bar_or(1, kSoftmaxThreads, top > kMaxGrowth)) break;
       }
       fence_async_smem();
       tc_fence_before();
@@ -936,10 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       wait_for(a, sm, &sm.pv_done[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
       tc_fence_after();
     }
-    named_bar(1, 128);  // lsum's last readers are done
+    named_bar(1, kSoftmaxThreads);  // lsum's last readers are done
 #pragma unroll
-    for (int c0 = 0; c0 < kMaxCols; c0 += 16)
-      if (c0 < N) {
+    for (int c0 = 0; c0 < kHalfCols; c0 += 16)
+      if (ch + c0 < ce) {
 #pragma unroll
         for (int h = 8; h > 0; h >>= 1) {
           const bool up = lane & (2 * h);
@@ -951,14 +940,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
         }
         const float s = l[c0] + __shfl_xor_sync(0xffffffffu, l[c0], 1);
-        if (!(lane & 1)) sm.lsum[warp][c0 + (lane >> 1)] = s;
+        if (!(lane & 1)) sm.lsum[warp & 3][ch + c0 + (lane >> 1)] = s;
       }
-    named_bar(1, 128);
+    named_bar(1, kSoftmaxThreads);
     const bool bad = sm.abort != 0;
     const float nan = __int_as_float(0x7fffffff);
     float* slot = a.ws + static_cast<int64_t>(blockIdx.x) * N * (kD + 2);
 #pragma unroll 1
-    for (int c0 = 0; c0 < N; c0 += 16) {
+    for (int c0 = ch; c0 < ce; c0 += 16) {
       uint32_t o[16];
       if (nd > 0) {
         tmem_ld16(tm + lanes + kTmO + c0, o);
@@ -972,13 +961,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const int c = c0 + k;
         if (c >= ncols) break;
         if (w.S > 1) {
-          slot[c * kD + tid] = __uint_as_float(o[k]);
+          slot[c * kD + lp] = __uint_as_float(o[k]);
         } else {
           const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
           const int cg = col0 + c, tok = cg / a.c.g;
           const int64_t row = (static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g);
           const float inv = bad ? nan : (L > 0.f ? 1.f / L : 0.f);
-          a.out[row * kD + tid] = f32_to_bf16_bits(__uint_as_float(o[k]) * inv);
+          a.out[row * kD + lp] = f32_to_bf16_bits(__uint_as_float(o[k]) * inv);
         }
       }
     }
