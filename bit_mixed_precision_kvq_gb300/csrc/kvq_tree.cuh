@@ -515,9 +515,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       __syncwarp();
     };
+    // the rows of the tiles to come into L2: K by lane 0, V by lane 1
+    const HeadRows rows = head_rows(a.c, w.b, w.h);
+    if (lane < 2)
+      for (int i = i0; i < min(i0 + kAhead, i1); ++i) prefetch_tile(a.c, rows, i, len, lane == 0);
     if (i0 < i1) wait_for(a, sm, &sm.q_ready, 0);
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
+      if (lane < 2 && i + kAhead < i1) prefetch_tile(a.c, rows, i + kAhead, len, lane == 0);
+      __syncwarp();
       wait_for(a, sm, &sm.k_full[buf], (n >> 1) & 1);
       if (n >= 2) wait_for(a, sm, &sm.s_free[buf], ((n - 2) >> 1) & 1);
       tc_fence_after();
@@ -549,9 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     Source src;
     src.r = head_rows(c, w.b, w.h);
     src.len = max(len, 0);
-    const bool fetch = (warp & 3) == 0 && lane == 0;  // of K (hf = 0) or V (hf = 1)
-    if (fetch)
-      for (int k = 0; k < kAhead && i0 + k < i1; ++k) prefetch_tile(c, src.r, i0 + k, src.len, hf == 0);
     const int64_t d0 = w.b * a.sb + w.h * a.sh;
     src.kd = reinterpret_cast<const uint8_t*>(a.kd + d0);
     src.vd = reinterpret_cast<const uint8_t*>(a.vd + d0);
@@ -593,7 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
       const bool vis = all_visual(i), next = i + 1 < i1 && all_visual(i + 1);
-      if (fetch && i + kAhead < i1) prefetch_tile(c, src.r, i + kAhead, src.len, hf == 0);
       // ---- K: registers -> TMEM ----
       const uint32_t kt = tm + lanes + kTmK + buf * kTmKStride + 32 * hf;
       if (n >= 2) {
@@ -784,13 +786,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
-      const int t = i * kTile + lp;
-      // bit c: column c attends it
-      uint64_t sees = t < len ? ~0ull : 0ull;
-      const bool whole = (i + 1) * kTile <= len;
-      if (t >= len && t < len + a.n_q) {
+      const bool whole = (i + 1) * kTile <= len;  // every position is context
+      uint32_t sees = 0xffffffffu;                // bit c - ch: column c attends this thread's position
+      if (!whole) {
+        const int t = i * kTile + lp;
+        if (t >= len) {
+          sees = 0u;
+          if (t < len + a.n_q) {
 #pragma unroll 1
-        for (int c = ch; c < ce; ++c) sees |= ((sm.colmask[c] >> (t - len)) & 1) << c;
+            for (int c = ch; c < ce; ++c)
+              sees |= static_cast<uint32_t>((sm.colmask[c] >> (t - len)) & 1) << (c - ch);
+          }
+        }
       }
       const uint32_t sb = tm + lanes + kTmS + buf * kTmSStride;
       wait_for(a, sm, &sm.s_full[buf], (n >> 1) & 1);
@@ -807,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
       };
       auto hide16 = [&](int c0, float (&x)[16]) {
-        const uint32_t b = static_cast<uint32_t>(sees >> c0);
+        const uint32_t b = sees >> (c0 - ch);
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if (!((b >> k) & 1)) x[k] = -INFINITY;
