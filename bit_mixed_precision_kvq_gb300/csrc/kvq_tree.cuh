@@ -88,7 +88,7 @@ struct Smem {
   alignas(1024) uint8_t qt[kMaxCols * 256];   // q: column, d contiguous (permuted)
   alignas(128) uint8_t qz[kMaxCols * 32];     // group sums of q: column, 16 K indexes
   uint64_t colmask[kMaxCols];
-  alignas(16) float m[kMaxCols];
+  alignas(16) float neg_m[kMaxCols];  // minus the references
   alignas(16) float fac[kMaxCols];
   float lsum[4][kMaxCols];  // per softmax warp: column maxima of a tile; at the end column sums
   float qs[kMaxCols][4];
@@ -376,6 +376,26 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
 // Both operands' majors as bits 15 (A) and 16 (B): 0 K-major, 1 MN-major.
 __host__ __device__ constexpr uint32_t idesc(int n, bool a_mn, bool b_mn) {
   return umma_idesc_f16(kTile, n, b_mn) | (static_cast<uint32_t>(a_mn) << 15);
+}
+
+// Pairs of fp32 in one 64-bit register: two operations an instruction.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // One lane of a converged warp; what it issues stays in uniform registers.
@@ -770,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       *reinterpret_cast<uint4*>(d) = make_uint4(z[0], z[1], z[2], z[3]);
       *reinterpret_cast<uint4*>(d + 16 * N) = make_uint4(z[4], z[5], z[6], z[7]);
       sm.colmask[c] = c < ncols ? a.mask[w.b * a.mask_sb + (col0 + c) / a.c.g] : 0;
-      sm.m[c] = kUnset;
+      sm.neg_m[c] = -kUnset;
     }
     fence_async_smem();  // the tensor cores read q
     named_bar(1, kSoftmaxThreads);
@@ -780,9 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     // this thread's position of a tile (a TMEM lane) and its columns [ch, ce)
     const int lp = 32 * (warp & 3) + lane;
     const int ch = (N / 2 + 15) / 16 * 16 * (warp >> 2), ce = warp < 4 ? min(N, (N / 2 + 15) / 16 * 16) : N;
-    float l[kHalfCols];
+    uint64_t l2[kHalfCols / 2];  // sums of its columns, in pairs
 #pragma unroll
-    for (int c = 0; c < kHalfCols; ++c) l[c] = 0.f;
+    for (int c = 0; c < kHalfCols / 2; ++c) l2[c] = 0ull;
+    const uint64_t scale2 = pair_of(sl2, sl2);
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
@@ -806,11 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       auto rel16 = [&](const uint32_t (&s)[16], int c0, float (&x)[16]) {
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
-          const float4 mm = *reinterpret_cast<const float4*>(&sm.m[c0 + k]);
-          x[k] = fmaf(__uint_as_float(s[k]), sl2, -mm.x);
-          x[k + 1] = fmaf(__uint_as_float(s[k + 1]), sl2, -mm.y);
-          x[k + 2] = fmaf(__uint_as_float(s[k + 2]), sl2, -mm.z);
-          x[k + 3] = fmaf(__uint_as_float(s[k + 3]), sl2, -mm.w);
+          const ulonglong2 mm = *reinterpret_cast<const ulonglong2*>(&sm.neg_m[c0 + k]);
+          unpair(fma_pair(pair_of(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, mm.x), x[k], x[k + 1]);
+          unpair(fma_pair(pair_of(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), scale2, mm.y), x[k + 2], x[k + 3]);
         }
       };
       auto hide16 = [&](int c0, float (&x)[16]) {
@@ -854,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           float v = -INFINITY, old = 0.f;
           if (tid < N) {
             v = fmaxf(fmaxf(sm.lsum[0][tid], sm.lsum[1][tid]), fmaxf(sm.lsum[2][tid], sm.lsum[3][tid]));
-            old = sm.m[tid];
+            old = -sm.neg_m[tid];
             // 2^-100 of a sum is nothing next to the new one, which is at least 1
             sm.fac[tid] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - v) : 1.f);
           }
@@ -872,9 +891,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 rel16(s, ch + c0, x);
                 if (!whole) hide16(ch + c0, x);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float f = sm.fac[ch + c0 + k];
-                  l[c0 + k] = f == 0.f ? 0.f : (l[c0 + k] - ex2(x[k])) * f;
+                for (int k = 0; k < 16; k += 2) {
+                  const float f0 = sm.fac[ch + c0 + k], f1 = sm.fac[ch + c0 + k + 1];
+                  float u, v;
+                  unpair(l2[(c0 + k) / 2], u, v);
+                  l2[(c0 + k) / 2] = pair_of(f0 == 0.f ? 0.f : (u - ex2(x[k])) * f0, f1 == 0.f ? 0.f : (v - ex2(x[k + 1])) * f1);
                 }
               }
             wait_for(a, sm, &sm.pv_done[buf ^ 1], ((n - 1) >> 1) & 1);
@@ -890,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             tmem_st_wait();
             named_bar(1, kSoftmaxThreads);  // every thread is done with the old references
           }
-          if (v > old + kMaxGrowth) sm.m[tid] = v;
+          if (v > old + kMaxGrowth) sm.neg_m[tid] = -v;
           named_bar(1, kSoftmaxThreads);
         }
         float top = -INFINITY;
@@ -909,8 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int k = 0; k < 16; k += 2) {
               top = fmaxf(top, fmaxf(x[k], x[k + 1]));
               const float p0 = ex2(x[k]), p1 = ex2(x[k + 1]);
-              l[c0 + k] += p0;
-              l[c0 + k + 1] += p1;
+              l2[(c0 + k) / 2] = add_pair(l2[(c0 + k) / 2], pair_of(p0, p1));
               y[k >> 1] = pack_f16x2(p0, p1);
             }
             *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -933,6 +953,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       tc_fence_after();
     }
     named_bar(1, kSoftmaxThreads);  // lsum's last readers are done
+    float l[kHalfCols];
+#pragma unroll
+    for (int c = 0; c < kHalfCols; c += 2) unpair(l2[c / 2], l[c], l[c + 1]);
 #pragma unroll
     for (int c0 = 0; c0 < kHalfCols; c0 += 16)
       if (ch + c0 < ce) {
@@ -981,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (tid < ncols) {
       const int c = tid, cg = col0 + c, tok = cg / a.c.g;
       const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
-      const float M = bad ? nan : (L > 0.f ? sm.m[c] : -INFINITY);
+      const float M = bad ? nan : (L > 0.f ? -sm.neg_m[c] : -INFINITY);
       if (w.S > 1) {
         *reinterpret_cast<float2*>(slot + N * kD + 2 * c) = make_float2(M, L);
       } else if (a.lse) {
