@@ -398,6 +398,12 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // One lane of a converged warp; what it issues stays in uniform registers.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -460,20 +466,21 @@ __device__ __forceinline__ void k_scales(const uint4& sz, uint32_t (&s2)[4]) {
   }
 }
 
-// The visual rows of tile i, K (key) or V: the bulk of a unit's bytes.
+// The context rows of tile i, K (key) or V, into L2.
 __device__ __forceinline__ void prefetch_tile(const Geom& c, const HeadRows& r, int i, int len, bool key) {
-  const int t0 = max(i * kTile, c.vs), t1 = min(min((i + 1) * kTile, c.ve), len);
-  if (t0 >= t1) return;
-  const int64_t i0 = t0 - c.vs;
-  if (key) {
-    const int w = r.k_packed ? c.krow : kRowBytes;
-    prefetch_bytes(r.vis_k + i0 * w, (t1 - t0) * w);
-    if (r.k_packed) prefetch_bytes(r.vis_ksz + i0 * c.kszrow, (t1 - t0) * c.kszrow);
-  } else {
-    const int w = r.v_packed ? c.vrow : kRowBytes;
-    prefetch_bytes(r.vis_v + i0 * w, (t1 - t0) * w);
-    if (r.v_packed) prefetch_bytes(r.vis_vsz + i0 * c.vszrow, (t1 - t0) * c.vszrow);
+  const int t0 = i * kTile, t1 = min(t0 + kTile, len);
+  const int v0 = max(t0, c.vs), v1 = min(t1, c.ve);  // visual ones
+  if (v0 < v1) {
+    const int64_t x = v0 - c.vs;
+    const bool packed = key ? r.k_packed : r.v_packed;
+    const int w = packed ? (key ? c.krow : c.vrow) : kRowBytes, zw = key ? c.kszrow : c.vszrow;
+    prefetch_bytes((key ? r.vis_k : r.vis_v) + x * w, (v1 - v0) * w);
+    if (packed) prefetch_bytes((key ? r.vis_ksz : r.vis_vsz) + x * zw, (v1 - v0) * zw);
   }
+  const uint8_t* text = key ? r.text_k : r.text_v;
+  if (t0 < min(t1, c.vs)) prefetch_bytes(text + static_cast<int64_t>(t0) * kRowBytes, (min(t1, c.vs) - t0) * kRowBytes);
+  const int s0 = max(t0, c.ve);
+  if (s0 < t1) prefetch_bytes(text + static_cast<int64_t>(s0 - c.Tv) * kRowBytes, (t1 - s0) * kRowBytes);
 }
 
 template <int KB, int VB, int G>
@@ -644,31 +651,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const Row row = row_of<true>(a, src, i * kTile + pos);
         const bool packed = has_packed(i);
         uint4 sz = make_uint4(0u, 0u, 0u, 0u);
-        if (KB < 16 && row.kind == kRowPacked) load_sz<G>(row.sz, sz);
+        uint32_t raw[32], s2[4];  // every load before the first use
+#pragma unroll
+        for (int j = 0; j < 32; ++j) raw[j] = 0u;
+        if (row.kind == kRowBf16) {  // words 16 t + 4 P ..: d = 32 P + 16 hf + 8 t .. + 7
+#pragma unroll
+          for (int P = 0; P < 4; ++P) {
+            load_words<1>(row.p + 64 * P + 32 * hf, raw + 4 * P);
+            load_words<1>(row.p + 64 * P + 32 * hf + 16, raw + 16 + 4 * P);
+          }
+        }
+        if constexpr (KB < 16) {
+          if (row.kind == kRowPacked) {
+            load_k_packed<KB>(row.p, hf, raw);
+            load_sz<G>(row.sz, sz);
+          }
+          k_scales<G>(sz, s2);
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) hi[j] = lo[j] = 0u;
-          if (row.kind == kRowBf16) {  // d = 32 P + 16 hf + 8 t .. + 7
-            uint4 raw[4];
-#pragma unroll
-            for (int P = 0; P < 4; ++P) raw[P] = *reinterpret_cast<const uint4*>(row.p + 64 * P + 32 * hf + 16 * t);
-#pragma unroll
-            for (int P = 0; P < 4; ++P) {
-              hi[4 * P] = pack_f16x2(0.5f * bf16_lo(raw[P].x), 0.5f * bf16_lo(raw[P].z));
-              hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(raw[P].x), 0.5f * bf16_hi(raw[P].z));
-              hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(raw[P].y), 0.5f * bf16_lo(raw[P].w));
-              hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(raw[P].y), 0.5f * bf16_hi(raw[P].w));
-            }
-          }
+          bool done = false;
           if constexpr (KB < 16) {
             if (row.kind == kRowPacked) {
-              uint32_t s2[4], raw[2 * KB];
-              load_k_packed<KB>(row.p, hf, raw);
-              k_scales<G>(sz, s2);
               k_codes<KB>(raw + t * KB, hi);
               k_parts<KB>(hi, s2, lo);
+              done = true;
+            }
+          }
+          if (!done) {
+#pragma unroll
+            for (int P = 0; P < 4; ++P) {
+              const uint32_t* x = raw + 16 * t + 4 * P;
+              hi[4 * P] = pack_f16x2(0.5f * bf16_lo(x[0]), 0.5f * bf16_lo(x[2]));
+              hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(x[0]), 0.5f * bf16_hi(x[2]));
+              hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(x[1]), 0.5f * bf16_lo(x[3]));
+              hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(x[1]), 0.5f * bf16_hi(x[3]));
+            }
+            if constexpr (KB > 2) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) lo[j] = 0u;
             }
           }
           __syncwarp();
@@ -708,31 +730,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       } else {
         const Row row = row_of<false>(a, src, i * kTile + pos);
         uint4 sz = make_uint4(0u, 0u, 0u, 0u);
-        if (VB < 16 && row.kind == kRowPacked) load_sz<G>(row.sz, sz);
+        uint32_t raw[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) raw[j] = 0u;
+        if (row.kind == kRowBf16) load_words<8>(row.p + 128 * hf, raw);
+        if constexpr (VB < 16) {
+          if (row.kind == kRowPacked) {
+            load_v_packed<VB>(row.p, hf, raw);
+            load_sz<G>(row.sz, sz);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0u;
-          if (row.kind == kRowBf16) {
-            uint4 raw[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[j] = *reinterpret_cast<const uint4*>(row.p + 128 * hf + 64 * e + 16 * j);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              o[4 * j] = bf16x2_to_f16x2(raw[j].x);
-              o[4 * j + 1] = bf16x2_to_f16x2(raw[j].y);
-              o[4 * j + 2] = bf16x2_to_f16x2(raw[j].z);
-              o[4 * j + 3] = bf16x2_to_f16x2(raw[j].w);
-            }
-          }
+          bool done = false;
           if constexpr (VB < 16) {
             if (row.kind == kRowPacked) {
-              uint32_t s2, z2, raw[VW];
-              load_v_packed<VB>(row.p, hf, raw);
+              uint32_t s2, z2;
               v_scales<G>(sz, hf, e, s2, z2);
               v_values<VB>(raw, hf, e, s2, z2, o);
+              done = true;
             }
+          }
+          if (!done) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = bf16x2_to_f16x2(raw[16 * e + j]);
           }
           put_v(e, o);
         }
@@ -800,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     // this thread's position of a tile (a TMEM lane) and its columns [ch, ce)
     const int lp = 32 * (warp & 3) + lane;
     const int ch = (N / 2 + 15) / 16 * 16 * (warp >> 2), ce = warp < 4 ? min(N, (N / 2 + 15) / 16 * 16) : N;
+    const uint32_t half_bar = 2 + (warp >> 2);  // barrier of the four warps that share the columns
     uint64_t l2[kHalfCols / 2];  // sums of its columns, in pairs
 #pragma unroll
     for (int c = 0; c < kHalfCols / 2; ++c) l2[c] = 0ull;
@@ -854,30 +877,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
             for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]) * sl2;
             if (!whole) hide16(c0, x);
-            // maxima over the lanes of 16 columns: halve the columns a lane
-            // holds four times; lane bits 4 .. 1 end up naming the column
+            float mine = -INFINITY;  // lane k: the maximum of column c0 + k over the warp's positions
 #pragma unroll
-            for (int h = 8; h > 0; h >>= 1) {
-              const bool up = lane & (2 * h);
-#pragma unroll
-              for (int k = 0; k < h; ++k) {
-                const float give = up ? x[k] : x[k + h];
-                const float got = __shfl_xor_sync(0xffffffffu, give, 2 * h);
-                x[k] = fmaxf(up ? x[k + h] : x[k], got);
-              }
+            for (int k = 0; k < 16; ++k) {
+              const float r = warp_max(x[k]);
+              if (lane == k) mine = r;
             }
-            x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-            if (!(lane & 1)) sm.lsum[warp & 3][c0 + (lane >> 1)] = x[0];
+            if (lane < 16) sm.lsum[warp & 3][c0 + lane] = mine;
           }
-          named_bar(1, kSoftmaxThreads);
+          named_bar(half_bar, 128);
           float v = -INFINITY, old = 0.f;
-          if (tid < N) {
-            v = fmaxf(fmaxf(sm.lsum[0][tid], sm.lsum[1][tid]), fmaxf(sm.lsum[2][tid], sm.lsum[3][tid]));
-            old = -sm.neg_m[tid];
+          const int mine = ch + (tid & 127);  // the column whose reference this thread keeps
+          if (mine < ce) {
+            v = fmaxf(fmaxf(sm.lsum[0][mine], sm.lsum[1][mine]), fmaxf(sm.lsum[2][mine], sm.lsum[3][mine]));
+            old = -sm.neg_m[mine];
             // 2^-100 of a sum is nothing next to the new one, which is at least 1
-            sm.fac[tid] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - v) : 1.f);
+            sm.fac[mine] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - v) : 1.f);
           }
-          named_bar(1, kSoftmaxThreads);
+          named_bar(half_bar, 128);
           if (n > 0) {
             // Undo what the tile added to the sums and rescale them; O, too,
             // once every earlier PV has landed.
@@ -909,10 +926,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               tmem_st16(tm + lanes + kTmO + c0, s);
             }
             tmem_st_wait();
-            named_bar(1, kSoftmaxThreads);  // every thread is done with the old references
+            named_bar(half_bar, 128);  // every thread is done with the old references
           }
-          if (v > old + kMaxGrowth) sm.neg_m[tid] = -v;
-          named_bar(1, kSoftmaxThreads);
+          if (v > old + kMaxGrowth) sm.neg_m[mine] = -v;
+          named_bar(half_bar, 128);
         }
         float top = -INFINITY;
         uint32_t s[2][16];
@@ -936,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<uint4*>(pt + (c0 >> 3) * 128 + 128) = make_uint4(y[4], y[5], y[6], y[7]);
           }
-        if (!bar_or(1, kSoftmaxThreads, top > kMaxGrowth)) break;
+        if (!bar_or(half_bar, 128, top > kMaxGrowth)) break;
       }
       fence_async_smem();
       tc_fence_before();
