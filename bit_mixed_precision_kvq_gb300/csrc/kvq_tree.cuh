@@ -546,6 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const HeadRows rows = head_rows(a.c, w.b, w.h);
     if (lane < 2)
       for (int i = i0; i < min(i0 + kAhead, i1); ++i) prefetch_tile(a.c, rows, i, len, lane == 0);
+    if (i1 * kTile > len)  // ... and the drafts
+      for (int j = lane; j < a.n_q; j += 32) {
+        const int64_t d = w.b * a.sb + w.h * a.sh + j * a.st;
+        prefetch_l2(a.kd + d, kRowBytes);
+        prefetch_l2(a.vd + d, kRowBytes);
+      }
     if (i0 < i1) wait_for(a, sm, &sm.q_ready, 0);
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
@@ -651,46 +657,48 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const Row row = row_of<true>(a, src, i * kTile + pos);
         const bool packed = has_packed(i);
         uint4 sz = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t raw[32], s2[4];  // every load before the first use
-#pragma unroll
-        for (int j = 0; j < 32; ++j) raw[j] = 0u;
-        if (row.kind == kRowBf16) {  // words 16 t + 4 P ..: d = 32 P + 16 hf + 8 t .. + 7
-#pragma unroll
-          for (int P = 0; P < 4; ++P) {
-            load_words<1>(row.p + 64 * P + 32 * hf, raw + 4 * P);
-            load_words<1>(row.p + 64 * P + 32 * hf + 16, raw + 16 + 4 * P);
-          }
-        }
+        uint32_t s2[4];
         if constexpr (KB < 16) {
-          if (row.kind == kRowPacked) {
-            load_k_packed<KB>(row.p, hf, raw);
-            load_sz<G>(row.sz, sz);
-          }
+          if (row.kind == kRowPacked) load_sz<G>(row.sz, sz);
           k_scales<G>(sz, s2);
         }
-#pragma unroll
+        // Not unrolled: this path runs once or twice a CTA of a packed head,
+        // mostly from a cold instruction cache.
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
-          uint32_t hi[16], lo[16];
-          bool done = false;
+          // both kinds of rows with the same loads: four 16-byte pieces of a
+          // bf16 row (d = 32 P + 16 hf + 8 t .. + 7), the slice of a packed one
+          uint32_t hi[16], lo[16], raw[16];
+          const bool bf = row.kind == kRowBf16;
+          const int pieces = bf ? 4 : (KB < 16 && row.kind == kRowPacked ? (KB + 3) / 4 : 0), step = bf ? 64 : 16;
+          const uint8_t* p = row.p + (bf ? 32 * hf + 16 * t : hf * 8 * KB + (KB > 2 ? t * 4 * KB : 0));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (j < pieces) x = *reinterpret_cast<const uint4*>(p + j * step);
+            raw[4 * j] = x.x;
+            raw[4 * j + 1] = x.y;
+            raw[4 * j + 2] = x.z;
+            raw[4 * j + 3] = x.w;
+          }
+#pragma unroll
+          for (int P = 0; P < 4; ++P) {
+            const uint32_t* x = raw + 4 * P;
+            hi[4 * P] = pack_f16x2(0.5f * bf16_lo(x[0]), 0.5f * bf16_lo(x[2]));
+            hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(x[0]), 0.5f * bf16_hi(x[2]));
+            hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(x[1]), 0.5f * bf16_lo(x[3]));
+            hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(x[1]), 0.5f * bf16_hi(x[3]));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) lo[j] = 0u;
           if constexpr (KB < 16) {
             if (row.kind == kRowPacked) {
-              k_codes<KB>(raw + t * KB, hi);
+              if (KB == 2 && t) {  // the piece holds both slices
+                raw[0] = raw[2];
+                raw[1] = raw[3];
+              }
+              k_codes<KB>(raw, hi);
               k_parts<KB>(hi, s2, lo);
-              done = true;
-            }
-          }
-          if (!done) {
-#pragma unroll
-            for (int P = 0; P < 4; ++P) {
-              const uint32_t* x = raw + 16 * t + 4 * P;
-              hi[4 * P] = pack_f16x2(0.5f * bf16_lo(x[0]), 0.5f * bf16_lo(x[2]));
-              hi[4 * P + 1] = pack_f16x2(0.5f * bf16_hi(x[0]), 0.5f * bf16_hi(x[2]));
-              hi[4 * P + 2] = pack_f16x2(0.5f * bf16_lo(x[1]), 0.5f * bf16_lo(x[3]));
-              hi[4 * P + 3] = pack_f16x2(0.5f * bf16_hi(x[1]), 0.5f * bf16_hi(x[3]));
-            }
-            if constexpr (KB > 2) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) lo[j] = 0u;
             }
           }
           __syncwarp();
@@ -730,31 +738,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       } else {
         const Row row = row_of<false>(a, src, i * kTile + pos);
         uint4 sz = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t raw[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) raw[j] = 0u;
-        if (row.kind == kRowBf16) load_words<8>(row.p + 128 * hf, raw);
         if constexpr (VB < 16) {
-          if (row.kind == kRowPacked) {
-            load_v_packed<VB>(row.p, hf, raw);
-            load_sz<G>(row.sz, sz);
-          }
+          if (row.kind == kRowPacked) load_sz<G>(row.sz, sz);
         }
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-          uint32_t o[16];
-          bool done = false;
+          uint32_t o[16], raw[16];
+          const bool bf = row.kind == kRowBf16;
+          const int pieces = bf ? 4 : (VB < 8 && row.kind == kRowPacked ? VB : 0);
+          const uint8_t* p = row.p + (bf ? 128 * hf + 64 * e : 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (j < pieces) x = *reinterpret_cast<const uint4*>(p + 16 * j);
+            raw[4 * j] = x.x;
+            raw[4 * j + 1] = x.y;
+            raw[4 * j + 2] = x.z;
+            raw[4 * j + 3] = x.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = bf16x2_to_f16x2(raw[j]);
           if constexpr (VB < 16) {
             if (row.kind == kRowPacked) {
+              if constexpr (VB == 8) load_v_packed<VB>(row.p, hf, raw);
               uint32_t s2, z2;
               v_scales<G>(sz, hf, e, s2, z2);
               v_values<VB>(raw, hf, e, s2, z2, o);
-              done = true;
             }
-          }
-          if (!done) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = bf16x2_to_f16x2(raw[16 * e + j]);
           }
           put_v(e, o);
         }
