@@ -92,7 +92,7 @@ struct Smem {
   alignas(16) float fac[kMaxCols];
   float lsum[4][kMaxCols];  // per softmax warp: column maxima of a tile; at the end column sums
   float qs[kMaxCols][4];
-  uint64_t k_full[2], k_free[2], v_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready;
+  uint64_t k_full[2], k_free[2], v_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drained;
   uint32_t tmem_base;
   int abort;
 };
@@ -139,8 +139,9 @@ __device__ __forceinline__ int context_len(const Args& a, int b) {
 // A wait that gives up marks the CTA (its outputs become NaN) and the status
 // word; every later wait of the CTA then polls once.
 __device__ __forceinline__ void wait_for(const Args& a, Smem& sm, uint64_t* bar, uint32_t parity) {
-  if (mbar_wait(bar, parity, a.polls)) return;
+  if (mbar_try_wait(bar, parity)) return;
   if (*static_cast<volatile int*>(&sm.abort)) return;
+  if (mbar_wait(bar, parity, a.polls)) return;
   sm.abort = 1;
   atomicOr(a.status, KVQ_STATUS_TILE_WAIT);
 }
@@ -499,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init(&sm.pv_done[i], 1);
     }
     mbar_init(&sm.q_ready, kSoftmaxWarps);
+    mbar_init(&sm.drained, 1);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -580,7 +582,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       __syncwarp();
       if (n > 0) issue_pv(n - 1);
     }
-    if (i0 < i1) issue_pv(i1 - i0 - 1);
+    if (i0 < i1) {
+      issue_pv(i1 - i0 - 1);
+      // No MMA is in flight when the CTA gives its tensor memory back, also
+      // where a wait above gave up (so not by the caller's limit).
+      if (elect_one()) umma_commit(&sm.drained);
+      __syncwarp();
+      mbar_wait(&sm.drained, 0, kDefaultTilePolls);
+    }
   } else if (warp >= kSoftmaxWarps) {
     // ---------------- unpack ----------------
     const int hf = (warp - kSoftmaxWarps) >> 2, pos = 32 * (warp & 3) + lane;
@@ -876,8 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // Weights by the references as they are; if a score of some column is
       // past its reference by more than kMaxGrowth, the references move and the
       // tile is done again (always for the first tile, which sets them).
-      for (bool move = n == 0;; move = true) {
-        if (move) {
+      // (Twice settles it: no score is past the new references.  The bound is
+      // for scores that a failed wait left unfinished.)
+      for (int round = n == 0 ? 1 : 0; round < 4; ++round) {
+        if (round > 0) {
 #pragma unroll 1
           for (int c0 = ch; c0 < ce; c0 += 16) {
             uint32_t s[16];
