@@ -92,7 +92,7 @@ struct Smem {
   alignas(16) float fac[kMaxCols];
   float lsum[4][kMaxCols];  // per softmax warp: column maxima of a tile; at the end column sums
   float qs[kMaxCols][4];
-  uint64_t k_full[2], k_free[2], v_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drained;
+  uint64_t k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2], q_ready, drained;
   uint32_t tmem_base;
   int abort;
 };
@@ -492,10 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.k_full[i], 8);
-      mbar_init(&sm.k_free[i], 1);
       mbar_init(&sm.v_full[i], 8);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_free[i], kSoftmaxWarps);
       mbar_init(&sm.p_full[i], kSoftmaxWarps);
       mbar_init(&sm.pv_done[i], 1);
     }
@@ -527,19 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (warp == kMmaWarp) {
     // ---------------- MMAs ----------------
     const uint32_t id_qk = idesc(N, false, false), id_pv = idesc(N, true, true);
-    const uint32_t lbo = 16 * N;
-    const uint32_t qa = smem_u32(sm.qt), qz = smem_u32(sm.qz);
+    // descriptors of the first K step; a step further is so many 16-byte units
+    const uint32_t lbo = 16 * N, step = 2 * lbo >> 4;
+    const uint64_t dq = umma_sdesc(smem_u32(sm.qt), lbo, 128), dz = umma_sdesc(smem_u32(sm.qz), lbo, 128);
+    const uint64_t dv = umma_sdesc(smem_u32(sm.vt[0]), 2048, 128), dp = umma_sdesc(smem_u32(sm.pt[0]), lbo, 128);
     auto issue_pv = [&](int n) {
       const int buf = n & 1;
       wait_for(a, sm, &sm.v_full[buf], (n >> 1) & 1);
       wait_for(a, sm, &sm.p_full[buf], (n >> 1) & 1);
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t va = smem_u32(sm.vt[buf]), pa = smem_u32(sm.pt[buf]);
+        const uint64_t v = dv + buf * (sizeof(sm.vt[0]) >> 4), p = dp + buf * (sizeof(sm.pt[0]) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_ss(tm + kTmO, umma_sdesc(va + ks * 4096, 2048, 128), umma_sdesc(pa + ks * 2 * lbo, lbo, 128), id_pv,
-                  n > 0 || ks > 0);
+        for (int ks = 0; ks < 8; ++ks) umma_ss(tm + kTmO, v + ks * 256, p + ks * step, id_pv, n > 0 || ks > 0);
         umma_commit(&sm.pv_done[buf]);
       }
       __syncwarp();
@@ -557,28 +555,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (i0 < i1) wait_for(a, sm, &sm.q_ready, 0);
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
-      if (lane < 2 && i + kAhead < i1) prefetch_tile(a.c, rows, i + kAhead, len, lane == 0);
-      __syncwarp();
       wait_for(a, sm, &sm.k_full[buf], (n >> 1) & 1);
-      if (n >= 2) wait_for(a, sm, &sm.s_free[buf], ((n - 2) >> 1) & 1);
       tc_fence_after();
+      // S's buffer is free: the P of tile n - 2 was waited for before its PV
       const bool packed = has_packed(i);
       if (elect_one()) {
         const uint32_t kb = tm + kTmK + buf * kTmKStride, sb = tm + kTmS + buf * kTmSStride;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_ts(sb, kb + 8 * ks, umma_sdesc(qa + ks * 2 * lbo, lbo, 128), id_qk, ks > 0);
+        for (int ks = 0; ks < 8; ++ks) umma_ts(sb, kb + 8 * ks, dq + ks * step, id_qk, ks > 0);
         if (packed) {
           if constexpr (KB > 2) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_ts(sb, kb + kTmLo + 8 * ks, umma_sdesc(qa + ks * 2 * lbo, lbo, 128), id_qk, true);
+            for (int ks = 0; ks < 8; ++ks) umma_ts(sb, kb + kTmLo + 8 * ks, dq + ks * step, id_qk, true);
           }
-          umma_ts(sb, kb + kTmZ, umma_sdesc(qz, lbo, 128), id_qk, true);
+          umma_ts(sb, kb + kTmZ, dz, id_qk, true);
         }
-        umma_commit(&sm.s_full[buf]);
-        umma_commit(&sm.k_free[buf]);
+        umma_commit(&sm.s_full[buf]);  // S is there, and K's buffer free
       }
+      __syncwarp();
+      if (lane < 2 && i + kAhead < i1) prefetch_tile(a.c, rows, i + kAhead, len, lane == 0);
       __syncwarp();
       if (n > 0) issue_pv(n - 1);
     }
@@ -641,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // ---- K: registers -> TMEM ----
       const uint32_t kt = tm + lanes + kTmK + buf * kTmKStride + 32 * hf;
       if (n >= 2) {
-        wait_for(a, sm, &sm.k_free[buf], ((n - 2) >> 1) & 1);
+        wait_for(a, sm, &sm.s_full[buf], ((n - 2) >> 1) & 1);  // its QK has read K's buffer
         tc_fence_after();
       }
       if (kp && vis) {
@@ -979,10 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.s_free[buf]);
-        mbar_arrive(&sm.p_full[buf]);
-      }
+      if (lane == 0) mbar_arrive(&sm.p_full[buf]);  // S is free, too
     }
     // ---- the column sums over the lanes, then the outputs (thread = d) ----
     const int nd = i1 - i0;
