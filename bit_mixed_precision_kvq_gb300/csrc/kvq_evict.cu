@@ -305,41 +305,66 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Evic
 }
 
 // The kept rows: a CTA per (sequence, KV head, 64 rows of the new cache).
-// Consecutive threads copy consecutive granules of the destination, so the
-// stores are whole lines and the loads are whole rows; a thread has up to
-// eight granules in flight.
+// Consecutive threads copy consecutive 16-byte granules of the destination, so
+// the stores are whole lines and the loads are whole rows; a thread loads its
+// scale/zero row and up to four granules of K and V before it stores any
+// (the row sizes leave no more than that in flight: it is what bounds a copy
+// of short rows).
 constexpr int kMoveRows = 64;
-constexpr int kMoveThreads = 128;
-constexpr int kMoveBatch = 8;
+constexpr int kMoveThreads = 2 * kMoveRows;
+constexpr int kMoveBatch = 4;
 
-// Rows [0, n) of w bytes at dst from the rows at[i] >= 0 of src, in granules
-// of T (w a multiple of its size).
-template <typename T>
-__device__ __forceinline__ void move_rows(uint8_t* dst, const uint8_t* src, int w, int n, const int32_t* at) {
-  const int per = w / static_cast<int>(sizeof(T));  // a power of two
-  const int sh = 31 - __clz(per), total = n << sh;
+// A scale/zero row of w = 4, 8 or 16 bytes.
+__device__ __forceinline__ uint4 load_row(const uint8_t* p, int w) {
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if (w == 16) {
+    r = __ldcg(reinterpret_cast<const uint4*>(p));
+  } else if (w == 8) {
+    const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
+    r.x = x.x;
+    r.y = x.y;
+  } else {
+    r.x = __ldcg(reinterpret_cast<const uint32_t*>(p));
+  }
+  return r;
+}
+__device__ __forceinline__ void store_row(uint8_t* p, int w, const uint4& r) {
+  if (w == 16) *reinterpret_cast<uint4*>(p) = r;
+  else if (w == 8) *reinterpret_cast<uint2*>(p) = make_uint2(r.x, r.y);
+  else *reinterpret_cast<uint32_t*>(p) = r.x;
+}
+
+// K rows of kw bytes and V rows of vw bytes (powers of two from 32 on): rows
+// [0, n) at kd, vd from the rows at[i] >= 0 of ks, vs.
+__device__ __forceinline__ void move_rows(uint8_t* kd, const uint8_t* ks, int kw, uint8_t* vd, const uint8_t* vs, int vw,
+                                          int n, const int32_t* at) {
+  const int ksh = 27 - __clz(kw), vsh = 27 - __clz(vw);  // log2 of the granules in a row
+  const int nk = n << ksh, total = nk + (n << vsh);
   for (int x0 = threadIdx.x; x0 < total; x0 += kMoveThreads * kMoveBatch) {
-    T v[kMoveBatch];
+    uint4 r[kMoveBatch];
     bool ok[kMoveBatch];
 #pragma unroll
     for (int k = 0; k < kMoveBatch; ++k) {
       const int x = x0 + kMoveThreads * k;
-      const int row = x < total ? at[x >> sh] : -1;
+      const bool key = x < nk;
+      const int y = key ? x : x - nk, sh = key ? ksh : vsh;
+      const int row = x < total ? at[y >> sh] : -1;
       ok[k] = row >= 0;
-      if (ok[k]) v[k] = __ldcg(reinterpret_cast<const T*>(src + static_cast<int64_t>(row) * w) + (x & (per - 1)));
+      if (ok[k])
+        r[k] = __ldcg(reinterpret_cast<const uint4*>((key ? ks : vs) + (static_cast<int64_t>(row) << (sh + 4))) +
+                      (y & ((1 << sh) - 1)));
     }
 #pragma unroll
     for (int k = 0; k < kMoveBatch; ++k)
-      if (ok[k]) reinterpret_cast<T*>(dst)[x0 + kMoveThreads * k] = v[k];
+      if (ok[k]) {
+        const int x = x0 + kMoveThreads * k;
+        if (x < nk) reinterpret_cast<uint4*>(kd)[x] = r[k];
+        else reinterpret_cast<uint4*>(vd)[x - nk] = r[k];
+      }
   }
 }
-__device__ __forceinline__ void move_sz(uint8_t* dst, const uint8_t* src, int w, int n, const int32_t* at) {
-  if (w == 16) move_rows<uint4>(dst, src, w, n, at);
-  else if (w == 8) move_rows<uint2>(dst, src, w, n, at);
-  else move_rows<uint32_t>(dst, src, w, n, at);
-}
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 10) move_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int32_t at[2][kMoveRows];  // source rows: visual, text (-1: none)
   const Geom &c = a.c, &d = a.d;
   const int chunks = (a.T_dst + kMoveRows - 1) / kMoveRows;
@@ -361,15 +386,18 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   if (v1 > v0) {
     const int kw = s.k_packed ? c.krow : kRowBytes, vw = s.v_packed ? c.vrow : kRowBytes, m = v1 - v0;
     const int64_t o = v0;
-    move_rows<uint4>(r.vis_k + o * kw, s.vis_k, kw, m, at[0]);
-    move_rows<uint4>(r.vis_v + o * vw, s.vis_v, vw, m, at[0]);
-    if (s.k_packed) move_sz(r.vis_ksz + o * c.kszrow, s.vis_ksz, c.kszrow, m, at[0]);
-    if (s.v_packed) move_sz(r.vis_vsz + o * c.vszrow, s.vis_vsz, c.vszrow, m, at[0]);
+    // the scale/zero rows: K's by the first 64 threads, V's by the others
+    const bool key = threadIdx.x < kMoveRows;
+    const int i = key ? threadIdx.x : threadIdx.x - kMoveRows, zw = key ? c.kszrow : c.vszrow;
+    const int from = i < m && (key ? s.k_packed : s.v_packed) ? at[0][i] : -1;
+    uint4 z;
+    if (from >= 0) z = load_row((key ? s.vis_ksz : s.vis_vsz) + static_cast<int64_t>(from) * zw, zw);
+    move_rows(r.vis_k + o * kw, s.vis_k, kw, r.vis_v + o * vw, s.vis_v, vw, m, at[0]);
+    if (from >= 0) store_row((key ? r.vis_ksz : r.vis_vsz) + (o + i) * zw, zw, z);
   }
   if (t1 > t0) {
     const int64_t o = static_cast<int64_t>(t0) * kRowBytes;
-    move_rows<uint4>(r.text_k + o, s.text_k, kRowBytes, t1 - t0, at[1]);
-    move_rows<uint4>(r.text_v + o, s.text_v, kRowBytes, t1 - t0, at[1]);
+    move_rows(r.text_k + o, s.text_k, kRowBytes, r.text_v + o, s.text_v, kRowBytes, t1 - t0, at[1]);
   }
 }
 

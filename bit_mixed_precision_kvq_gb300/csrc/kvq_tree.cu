@@ -76,10 +76,10 @@ struct Columns {
   int nblk, nb, N;
 };
 Columns columns_of(const kvq_layout* L, int32_t n_q) {
-  const int cols = L->g * n_q;
+  const int64_t cols = static_cast<int64_t>(L->g) * n_q;
   Columns c;
-  c.nblk = (cols + kMaxCols - 1) / kMaxCols;
-  c.nb = (cols + c.nblk - 1) / c.nblk;
+  c.nblk = static_cast<int>((cols + kMaxCols - 1) / kMaxCols);  // below 2^31: n_q and kMaxCols are at most 64
+  c.nb = static_cast<int>((cols + c.nblk - 1) / c.nblk);
   c.N = (c.nb + 15) / 16 * 16;
   return c;
 }
@@ -222,7 +222,7 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
   const int64_t rows = static_cast<int64_t>(L->d.B) * n_q * L->d.H_q;
   const kvq::tree::Columns cols = kvq::tree::columns_of(L, n_q);
   const int64_t units = static_cast<int64_t>(L->d.B) * L->d.H_kv * cols.nblk;
-  if (rows > 0x7fffffffLL || units > 0x7fffffffLL || static_cast<int64_t>(L->g) * n_q > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffffLL || units > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   const void* fn = kvq::tree::kernel_for(L->d.k_bits, L->d.v_bits, L->d.group_size);
   if (!fn) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
