@@ -9,6 +9,10 @@
 // Order of values: NaN below every number, -0 equal to +0; of equal ones the
 // lowest position stays.  Kept positions keep their order, and their rows are
 // copied as they are stored (codes, scales and zeros bit for bit).
+//
+// Two launches, selection and copy.  Measured (GB300): 32K x 8 sequences to 8K
+// 62 us (172 MB read and written; selection 24, copy 38), a LLaVA-OneVision
+// layer to half 11.8 us, a ragged batch of 16 LLaVA-1.5 chats 36.5 us.
 #include "kvq_geom.cuh"
 
 #include <algorithm>
@@ -45,7 +49,12 @@ __device__ __forceinline__ int evict_len(const EvictArgs& a, int b) {
 // found in three passes of 11, 11 and 10 bits: a histogram in shared memory of
 // the keys that share the digits found so far, and the bin in which the count
 // from above reaches `want`.  11 bits spread the exponents of real masses over
-// enough bins that the shared-memory atomics do not queue.
+// enough bins that the shared-memory atomics do not queue.  A range of up to
+// 32 keys a thread is read once and stays in registers; what bounds it then is
+// the instructions of one SM (32,736 keys: 4 us of loads, 6 of histograms, 2 of
+// bin searches, 10 of ballots and writes), as there are no more CTAs than
+// ranges.  (A bisection by counting, without atomics, took 47 us there against
+// 40 for this before either had its loads in flight together.)
 constexpr int kBins = 2048;
 
 template <int NT>
@@ -308,8 +317,8 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Evic
 // Consecutive threads copy consecutive 16-byte granules of the destination, so
 // the stores are whole lines and the loads are whole rows; a thread loads its
 // scale/zero row and up to four granules of K and V before it stores any
-// (the row sizes leave no more than that in flight: it is what bounds a copy
-// of short rows).
+// (short rows leave no more than that in flight, which is what bounds the
+// copy: 4.0 TB/s read and written together).
 constexpr int kMoveRows = 64;
 constexpr int kMoveThreads = 2 * kMoveRows;
 constexpr int kMoveBatch = 4;

@@ -15,11 +15,20 @@
 // high and low fp16 parts of the query's group sums), as in the split kernel;
 // bf16 rows and queries go to the bf16 MMA as they are stored.
 //
-// With few columns the pass is bound by the K bytes, with many by the MMA rate
-// (9 MMAs of 8 cycles per 16 positions and 8 columns), so the operands of a
-// 16-row block stay in registers over all columns.  mma.sync and not tcgen05:
-// the contraction is at most 64 columns thin between unpacking and exponential,
-// and the weights are wanted per position, where their fragments already are.
+// With few columns the pass would be bound by the K bytes, with many by the MMA
+// rate (9 MMAs of 8 cycles per 16 positions and 8 columns), so the operands of
+// a 16-row block stay in registers over all columns.  mma.sync and not tcgen05:
+// a decode step has at most 8 columns a KV head in most models, the weights are
+// wanted per position, where their fragments already are, and at 32 columns
+// 128 positions take 1.0 us of an SM (the tree kernel's tile, V included, 1.6).
+//
+// Measured (GB300): 32K positions x 8 after a decode step (172 MB) 70 us, 2.5
+// TB/s; 32 tokens over 2,972 positions x 32 x 40 heads (421 MB, 31 GFLOP) 200
+// us; a LLaVA-OneVision layer 4.9 us.  Bound by instruction issue and latency
+// (about 250 instructions a block and tile of columns, 0.45 a clock and
+// scheduler; DRAM 30%, tensor pipe 12-22%).  Rows are prefetched into L2 four
+// blocks ahead and into registers one ahead; 2 CTAs of 128 registers an SM and
+// 3 of 80 take the same.
 #include "kvq_split.cuh"
 
 #include "kvq_geom.cuh"

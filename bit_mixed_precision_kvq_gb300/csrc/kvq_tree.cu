@@ -17,7 +17,9 @@ namespace tree {
 namespace {
 
 // The outputs of units that are split over several CTAs: a CTA per output
-// row, thread = d.  Partials are o (relative to the reference m), m and l.
+// row, thread = d.  Partials are o (relative to the reference m), m and l;
+// each is read once, coalesced (latency-bound: 448 rows of 17 to 25 partials
+// in about 3 us, most of it hidden behind the last tree CTAs).
 __global__ void __launch_bounds__(kD) combine_kernel(const __grid_constant__ Args a) {
   __shared__ float wgt[kMaxSplitCtas];
   __shared__ float red[4][2];

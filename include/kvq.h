@@ -536,8 +536,9 @@ void kvq_set_wait_limits(uint32_t tile_polls, uint32_t peer_polls);
  * a memory copy separates it) before the call.  The library's own writers
  * (kvq_quantize_append, kvq_decode_step, kvq_decode_step_ragged) fence
  * their cache writes and let the next kernel launch only after them and
- * after their own dependency wait, which makes the early copies see every
- * row written before.  Off (0) by default.
+ * after their own dependency wait; kvq_tree_commit and kvq_cache_evict let
+ * it launch when they have finished.  So the early copies see every row
+ * written before.  Off (0) by default.
  */
 void kvq_set_cache_preload(int32_t enable);
 
