@@ -12,7 +12,7 @@
 //
 // Two launches, selection and copy.  Measured (GB300): 32K x 8 sequences to 8K
 // 62 us (172 MB read and written; selection 24, copy 38), a LLaVA-OneVision
-// layer to half 11.8 us, a ragged batch of 16 LLaVA-1.5 chats 36.5 us.
+// layer to half 12 us, a ragged batch of 16 LLaVA-1.5 chats 27 us.
 #include "kvq_geom.cuh"
 
 #include <algorithm>
@@ -54,44 +54,71 @@ __device__ __forceinline__ int evict_len(const EvictArgs& a, int b) {
 // the instructions of one SM (32,736 keys: 4 us of loads, 6 of histograms, 2 of
 // bin searches, 10 of ballots and writes), as there are no more CTAs than
 // ranges.  (A bisection by counting, without atomics, took 47 us there against
-// 40 for this before either had its loads in flight together.)
+// 40 for this before either had its loads in flight together; a cluster of 8
+// CTAs a range, histograms added up through distributed shared memory, took
+// twice as long, its CTAs waiting for one another.)
+//
+// A CTA has as few threads as hold its keys, so that many ranges share an SM
+// (1,280 pairs of sequence and head with 2,880 masses: 164 us with 512 threads and 8 keys
+// each, copy included, 218 with 1,024 threads; 512 ragged ones of 576: 27 us with
+// 256 threads bound to 32 registers, 36.5 without the bound), and no more than
+// 8 keys a thread below 1,024 threads (32,736 keys at 512 threads: 66 us for one
+// range against 25.5).
 constexpr int kBins = 2048;
+template <int NT>
+constexpr int kMostKeys = NT == 256 ? 4 : (NT == 512 ? 8 : 32);  // keys a thread of a CTA of NT holds
 
 template <int NT>
 struct SelectSmem {
-  uint32_t hist[kBins];
+  alignas(16) uint32_t hist[kBins];
+  alignas(8) uint32_t coarse[kBins / 32];  // sums of 32 bins
   uint32_t scan[NT / 32][2];
-  uint32_t count[1024];  // (round, warp): kept above the threshold | equal to it << 16
-  uint2 start[1024];
+  static constexpr int kPairs = NT / 32 * kMostKeys<NT>;
+  uint32_t count[kPairs];  // (round, warp): kept above the threshold | equal to it << 16
+  uint2 start[kPairs];
   uint32_t digit, want;
 };
 
-// The bin in which the count from the highest one down reaches sm.want;
-// sm.want becomes what is wanted of that bin.  Thread k has the kBins / NT
-// bins below kBins - k (kBins / NT).
+// The bin in which the count from the highest one down reaches sm.want; sm.want
+// becomes what is wanted of that bin.  Every thread adds up its kBins / NT
+// bins, the sums of 32 bins are left to one warp, which finds the one and then
+// the bin.
 template <int NT>
 __device__ __forceinline__ void find_bin(SelectSmem<NT>& sm) {
-  constexpr int PER = kBins / NT;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t own = 0;
+  constexpr int PER = kBins / NT, SHARE = PER < 32 ? 32 / PER : 1;  // threads to 32 bins
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t sum = 0;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) own += sm.hist[kBins - 1 - tid * PER - k];
-  uint32_t incl = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+  for (int k = 0; k < PER; k += 2) {
+    const uint2 v = reinterpret_cast<const uint2*>(sm.hist)[(PER * tid + k) / 2];
+    sum += v.x + v.y;
   }
-  if (lane == 31) sm.scan[warp][0] = incl;
-  const uint32_t want = sm.want;
+#pragma unroll
+  for (int o = 1; o < SHARE; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tid % SHARE == 0) sm.coarse[tid / SHARE] = sum;
   __syncthreads();
-  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp && lane < NT / 32 ? sm.scan[lane][0] : 0u);
-  uint32_t above = before + incl - own;
-  if (above < want && want <= above + own) {
-    int bin = kBins - 1 - tid * PER;
-    while (above + sm.hist[bin] < want) above += sm.hist[bin--];
-    sm.digit = bin;
-    sm.want = want - above;
+  if (tid < 32) {
+    const uint32_t want = sm.want;
+    auto scan = [&](uint32_t x) {  // inclusive, over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      return x;
+    };
+    // lane l: the sums 63 - 2 l and 62 - 2 l, then bin 31 - l of the one found
+    const uint2 c = *reinterpret_cast<const uint2*>(&sm.coarse[62 - 2 * lane]);
+    const uint32_t incl = scan(c.x + c.y), above = incl - c.x - c.y;
+    const bool in_hi = want <= above + c.y;
+    const uint32_t from = __ffs(__ballot_sync(0xffffffffu, want <= incl)) - 1;  // there is one: want <= all keys left
+    const uint32_t at = __shfl_sync(0xffffffffu, in_hi ? 63 - 2 * lane : 62 - 2 * lane, from);
+    const uint32_t base = __shfl_sync(0xffffffffu, in_hi ? above : above + c.y, from);
+    const uint32_t bin = 32 * at + 31 - lane, own = sm.hist[bin], over = base + scan(own) - own;
+    if (over < want && want <= over + own) {
+      sm.digit = bin;
+      sm.want = want - over;
+    }
   }
   __syncthreads();
 }
@@ -107,7 +134,7 @@ __device__ __forceinline__ uint32_t find_threshold(SelectSmem<NT>& sm, int want,
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
     const uint32_t high = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
-    for (int k = tid; k < kBins; k += NT) sm.hist[k] = 0;
+    for (int k = tid; k < kBins / 4; k += NT) reinterpret_cast<uint4*>(sm.hist)[k] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     load([&](uint32_t key, bool in) {
       if (in && (key & high) == prefix) atomicAdd(&sm.hist[(key >> shift) & mask], 1u);
@@ -124,7 +151,7 @@ __device__ __forceinline__ uint32_t find_threshold(SelectSmem<NT>& sm, int want,
 template <int NT, int R>
 __device__ void select_in_registers(SelectSmem<NT>& sm, const float* x, int n, int want, int pos0, int32_t* out,
                                     float* xout) {
-  static_assert(NT / 32 * R <= 1024, "one count per (round, warp)");
+  static_assert(R <= kMostKeys<NT>, "one count per (round, warp)");
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t key[R];
@@ -262,7 +289,7 @@ __device__ void select_from_memory(SelectSmem<NT>& sm, const float* x, int n, in
 template <int NT>
 __device__ __forceinline__ void select_range(SelectSmem<NT>& sm, const float* x, int n, int want, int pos0, int32_t* out,
                                              float* xout) {
-  if (n <= 4 * NT) select_in_registers<NT, 4>(sm, x, n, want, pos0, out, xout);
+  if constexpr (NT < 1024) select_in_registers<NT, kMostKeys<NT>>(sm, x, n, want, pos0, out, xout);
   else if (n <= 8 * NT) select_in_registers<NT, 8>(sm, x, n, want, pos0, out, xout);
   else if (n <= 32 * NT) select_in_registers<NT, 32>(sm, x, n, want, pos0, out, xout);
   else select_from_memory(sm, x, n, want, pos0, out, xout);
@@ -271,7 +298,7 @@ __device__ __forceinline__ void select_range(SelectSmem<NT>& sm, const float* x,
 // CTA (b, h, part): part 0 the text prefix and the visual block, part 1 the
 // text behind it and the tails of keep and mass_dst.
 template <int NT>
-__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(NT, NT < 1024 ? 2048 / NT : 1) select_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ SelectSmem<NT> sm;
   const Geom &c = a.c, &d = a.d;
   const int part = blockIdx.x & 1;
@@ -454,13 +481,14 @@ extern "C" kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, co
   a.keep = keep;
   a.mass_dst = mass_dst;
   a.new_len = new_len;
-  // Long ranges, or few of them: 1024 threads each; else 256, so that several
-  // share an SM.
+  // The threads of a range: as few as hold its keys in registers, so that
+  // several ranges share an SM.
   const int longest = std::max(L->Tv, T - s.vis_end);
-  const bool wide = longest > 4 * 256;
-  st = kvq::launch_dependent(wide ? reinterpret_cast<const void*>(&kvq::select_kernel<1024>)
-                                  : reinterpret_cast<const void*>(&kvq::select_kernel<256>),
-                             dim3(static_cast<unsigned>(2 * bh)), wide ? 1024 : 256, 0, stream, &a);
+  const int nt = longest <= 4 * 256 ? 256 : (longest <= 8 * 512 ? 512 : 1024);
+  const void* fn = nt == 256   ? reinterpret_cast<const void*>(&kvq::select_kernel<256>)
+                   : nt == 512 ? reinterpret_cast<const void*>(&kvq::select_kernel<512>)
+                               : reinterpret_cast<const void*>(&kvq::select_kernel<1024>);
+  st = kvq::launch_dependent(fn, dim3(static_cast<unsigned>(2 * bh)), nt, 0, stream, &a);
   if (st != KVQ_OK) return st;
   return kvq::launch_dependent(reinterpret_cast<const void*>(&kvq::move_kernel), dim3(static_cast<unsigned>(blocks)),
                                kvq::kMoveThreads, 0, stream, &a);

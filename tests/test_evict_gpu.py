@@ -131,3 +131,26 @@ def test_evict_values_that_tie(cuda_dev, kvq):
 def test_evict_without_optional_outputs(cuda_dev, kvq):
     c = Case(2, 4, 2, 300, 14, 256, 4, 4, 32, [])
     _evict(_quick(c, cuda_dev), _mass(c, 6300, cuda_dev), 280, 100, 10, 3, spare=0, optional=False)
+
+
+# Ranges on both sides of what the registers of each size of CTA hold:
+# (B, KV heads, visual, text, lengths)
+LONG = [(1, 1, 1024, 40, None), (1, 1, 4096, 40, None), (1, 1, 8192, 4, None), (1, 1, 8193, 4, None), (1, 1, 1025, 40, None), (3, 2, 1060, 1500, [2600, 1065, 1064]), (1, 2, 4097, 5, None),
+        (1, 1, 32768, 3, None), (2, 1, 32769, 40, None), (1, 1, 70001, 33000, None), (2, 80, 1111, 60, None),
+        (2, 1, 0, 9001, [9005, 20])]
+
+
+@pytest.mark.parametrize("case", LONG)
+def test_evict_long_ranges(cuda_dev, kvq, case):
+    """Random masses, masses of three values (the last kept one's equals are
+    spread over the whole range) and equal ones."""
+    B, H, n_vis, n_text, lens = case
+    vs = 5
+    c = Case(B, H, H, vs + n_vis + n_text + 11, vs, vs + n_vis, 2, 2, 128, [])
+    F = _quick(c, cuda_dev)
+    T = vs + n_vis + n_text
+    m = _mass(c, 6400, cuda_dev)
+    three = m.clamp(max=1.0).mul(2).round()
+    for mass in (m, three, torch.ones_like(m)):
+        _evict(F, mass, T, n_vis // 3, max(n_text // 2, 1), min(3, n_text // 2), lens)
+    _evict(F, three, T, n_vis, n_text, 0, lens)
