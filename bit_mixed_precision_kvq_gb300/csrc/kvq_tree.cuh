@@ -43,8 +43,12 @@
 // Softmax: a thread owns a position (a TMEM lane) and all columns, so the
 // maximum of a column would be a reduction over 128 lanes.  Instead every
 // column has a reference m (log2 units, shared memory) that only moves, for
-// all lanes at once, when a score of a tile exceeds it by more than 2^12
-// (P <= 4096 in fp16); the column sums stay in the threads until the end.
+// all lanes at once, when a score's P would pass 2^15 (fp16); the score that
+// moves it gets P = 2^3.  So weights are off by 2^-28 of the largest one at most
+// (half a step of fp16's subnormals; with P = 1 for the largest, 2^-25, a long
+// context's faint weights would be lost), and a score may pass its reference's
+// by 2^12 before it moves (by 2^9, from P = 2^6: 5% more time at 16K x 8).  The
+// column sums stay in the threads until the end.
 //
 // 128 positions a tile and not 64: M = 64 takes the tensor cores as long.  64
 // columns a unit at most: their sums are registers of the softmax threads.
@@ -70,7 +74,8 @@ constexpr int kTile = 128;              // positions per tile (TMEM lanes)
 constexpr int kMaxCols = 64;            // columns per unit (at most)
 constexpr int kHalfCols = kMaxCols / 2;  // columns of a softmax thread
 constexpr int kMaxSplitCtas = 160;      // CTAs of a call whose units are split (workspace slots)
-constexpr float kMaxGrowth = 12.f;      // log2 of the largest P
+constexpr float kMaxGrowth = 15.f;      // log2 of the largest P (fp16)
+constexpr float kLift = 3.f;            // log2 of the P of a score that sets its reference
 constexpr float kUnset = -1e30f;        // reference of a column that has attended nothing
 constexpr float kOperandScale = 256.f;  // undoes K / 2 and q / 2^7
 
@@ -926,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             v = fmaxf(fmaxf(sm.lsum[0][mine], sm.lsum[1][mine]), fmaxf(sm.lsum[2][mine], sm.lsum[3][mine]));
             old = -sm.neg_m[mine];
             // 2^-100 of a sum is nothing next to the new one, which is at least 1
-            sm.fac[mine] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - v) : 1.f);
+            sm.fac[mine] = v > old + 100.f ? 0.f : (v > old + kMaxGrowth ? ex2(old - (v - kLift)) : 1.f);
           }
           named_bar(half_bar, 128);
           if (n > 0) {
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             tmem_st_wait();
             named_bar(half_bar, 128);  // every thread is done with the old references
           }
-          if (v > old + kMaxGrowth) sm.neg_m[mine] = -v;
+          if (v > old + kMaxGrowth) sm.neg_m[mine] = kLift - v;
           named_bar(half_bar, 128);
         }
         float top = -INFINITY;

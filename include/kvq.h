@@ -369,7 +369,8 @@ kvq_status kvq_sensitivity_probe(const kvq_layout* L, const void* cache, const v
  *             on entry are ignored; overlapping calls must not share it
  * A token that attends nothing (empty context, empty mask) gets output zero
  * and lse -inf.  Drafted rows that no token of their sequence attends may
- * hold anything; all other values are finite, |x| <= 65504.
+ * hold anything; all other values are finite, |x| <= 65504, and scores
+ * softmax_scale * q.k stay below 2^20 in size (they are fp32).
  * kvq_decode_tree_workspace_bytes returns 0 for an invalid layout or n_q.
  */
 size_t kvq_decode_tree_workspace_bytes(const kvq_layout* L, int32_t n_q);

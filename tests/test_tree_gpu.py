@@ -66,6 +66,27 @@ def test_tree_matches_reference(cuda_dev, kvq, ci):
     check_tree(c, out, lse, f64(q), F.khat, F.vhat, f64(kd), f64(vd), masks, _active(lens or [T] * c.B, T))
 
 
+def test_tree_faint_tail(cuda_dev, kvq):
+    """One draft outweighs 63 others by e^17 each and holds zeros where they
+    hold ones: the output is their share.  A weight is off by half a step of
+    fp16's subnormals (2^-25) from P = 2^3 e^-17, and the output rounded once."""
+    c = Case(1, 2, 1, 100, 4, 60, 4, 4, 64, [])
+    F = Filled(c, 3900, cuda_dev)
+    q = torch.zeros(1, 64, 2, 128, dtype=torch.bfloat16, device=cuda_dev)
+    q[..., 0] = 1.0 / SCALE
+    assert float(q[0, 0, 0, 0]) * SCALE == pytest.approx(1.0, abs=2.0 ** -8)
+    gap = float(q[0, 0, 0, 0]) * SCALE * 17.0
+    kd = torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=cuda_dev)
+    vd = torch.ones_like(kd)
+    kd[:, :, 40, 0], vd[:, :, 40] = 17.0, 0.0
+    out, lse = _call(F, q, kd, vd, np.full((1, 64), -1, np.int64).view(np.uint64), 0)
+    w = np.exp(-gap)
+    want = 63 * w / (1 + 63 * w)
+    tol = 2.0 ** -25 / (2.0 ** 3 * w) + 2.0 ** -8 + 2.0 ** -16
+    assert np.all(np.abs(f64(out) / want - 1.0) <= tol)
+    assert np.all(np.abs(f64(lse) - gap - np.log1p(63 * w)) <= 2.0 ** -19 * gap)
+
+
 BITS = [(kb, vb, G) for kb in (2, 4, 8, 16) for vb in (2, 4, 8, 16) for G in (32, 64, 128)]
 
 
