@@ -9,6 +9,9 @@
 #include "kvq_device.cuh"
 #include "kvq_ptx.cuh"
 
+// Lets a kernel have `bytes` of dynamic shared memory (kvq_tree.cu).
+kvq_status kvq_allow_smem(const void* fn, int bytes);
+
 namespace kvq {
 
 constexpr int kRowBytes = 2 * kD;  // a bf16 row

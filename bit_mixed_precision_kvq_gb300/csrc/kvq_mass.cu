@@ -22,13 +22,14 @@
 // wanted per position, where their fragments already are, and at 32 columns
 // 128 positions take 1.0 us of an SM (the tree kernel's tile, V included, 1.6).
 //
-// Measured (GB300): 32K positions x 8 after a decode step (172 MB) 70 us, 2.5
-// TB/s; 32 tokens over 2,972 positions x 32 x 40 heads (421 MB, 31 GFLOP) 200
-// us; a LLaVA-OneVision layer 4.9 us.  Bound by instruction issue and latency
-// (about 250 instructions a block and tile of columns, 0.45 a clock and
-// scheduler; DRAM 30%, tensor pipe 12-22%).  Rows are prefetched into L2 four
-// blocks ahead and into registers one ahead; 2 CTAs of 128 registers an SM and
-// 3 of 80 take the same.
+// Measured (GB300): 32K positions x 8 after a decode step (172 MB) 54 us, 3.2
+// TB/s; 32 tokens over 2,972 positions x 32 x 40 heads (421 MB, 31 GFLOP) 172
+// us; a LLaVA-OneVision layer 4.7 us.  Bound by instruction issue and latency
+// (about 250 instructions a block and tile of columns).  A warp's packed blocks
+// come through shared memory, two under way (three or five take the same): one
+// ahead in registers, behind prefetches into L2, took 70 and 199 us.  fp32
+// arithmetic in pairs is 3% of the first, 0 of the second; 3 CTAs of 80
+// registers an SM instead of 2 take 54 and 165.
 #include "kvq_split.cuh"
 
 #include "kvq_geom.cuh"
@@ -64,7 +65,7 @@ struct MassSmem {
   uint4 qh[kMaxTiles][4][32];   // fp16 operand: [tile][32-element block][lane], see q_factor
   uint4 qb[kMaxTiles][4][32];   // bf16 operand
   uint32_t zb[kMaxTiles][32];   // group sums, high then low
-  float2 lse2[kMaxTiles][4];    // lse in log2 units of columns 2 tig, 2 tig + 1
+  float2 lse2[kMaxTiles][4];    // minus lse in log2 units of columns 2 tig, 2 tig + 1
   int2 lim[kMaxTiles][4];       // those columns see the positions below
   float qs[kMaxTiles * 8][4];
 };
@@ -143,7 +144,7 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
       if (P == 0) {
         float* l2 = reinterpret_cast<float*>(&sm.lse2[t][0]);
         int* lm = reinterpret_cast<int*>(&sm.lim[t][0]);
-        l2[c & 7] = l * 1.4426950408889634f;
+        l2[c & 7] = -l * 1.4426950408889634f;
         lm[c & 7] = len - n + 1 + k;
       }
     }
@@ -243,8 +244,29 @@ __device__ __forceinline__ void slice_regs(const RawRow<KB>& r, uint32_t (&f)[4]
   }
 }
 
+// A warp's blocks of packed rows on their way through shared memory.
+template <int KB, int G>
+struct Ring {
+  static constexpr int kCodes = kRows * kD / 8 * KB, kSz = kRows * (kD / G) * 4;  // bytes of a block
+  static constexpr int kStage = kCodes + kSz + kRows * 4, kStages = 3;
+  static constexpr int kBytes = kStages * kStage;
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int KB, int G>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __grid_constant__ MassArgs a) {
+  extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ MassSmem sm;
   const Geom& p = a.c;
   constexpr int NG = kD / G;
@@ -286,9 +308,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
       if (col0 > 0) return a.mass[base + t0 + my];
       return a.mass_in ? a.decay * a.mass_in[base + t0 + my] : 0.f;
     };
-    float w0 = 0.f, w1 = 0.f;  // weights of rows gid, gid + 8 of the block
-    auto add = [&](int t, const float (&x)[4], int t0, bool late) {
-      float e0 = ex2(x[0]), e1 = ex2(x[1]), e2 = ex2(x[2]), e3 = ex2(x[3]);
+    const bool in_ring = a.mass_in && col0 == 0;
+    // weights of rows gid, gid + 8 of the block, those of even and odd columns
+    uint64_t w0 = 0ull, w1 = 0ull;
+    auto add = [&](int t, uint64_t x0, uint64_t x1, int t0, bool late) {
+      float e0, e1, e2, e3;
+      unpair(x0, e0, e1);
+      unpair(x1, e2, e3);
+      e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
       if (late) {
         const int2 lim = sm.lim[t][tig];
         const int ta = t0 + gid, tb = ta + 8;
@@ -297,15 +324,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
         if (tb >= lim.x) e2 = 0.f;
         if (tb >= lim.y) e3 = 0.f;
       }
-      w0 += e0 + e1;
-      w1 += e2 + e3;
+      w0 = add_pair(w0, pair_of(e0, e1));
+      w1 = add_pair(w1, pair_of(e2, e3));
     };
-    auto store = [&](int t0, int m, float m_in) {
-      w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-      w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-      if (tig < 2 && my < m) a.mass[base + t0 + my] = m_in + (tig == 0 ? w0 : w1);
+    auto store = [&](int t0, int m, float m_in) {  // lanes tig 0 and 2 end up with row gid, 1 and 3 with gid + 8
+      float a0, a1, b0, b1;
+      unpair(w0, a0, a1);
+      unpair(w1, b0, b1);
+      a0 += a1;
+      b0 += b1;
+      float w = (tig & 1 ? b0 : a0) + __shfl_xor_sync(0xffffffffu, tig & 1 ? a0 : b0, 1);
+      w += __shfl_xor_sync(0xffffffffu, w, 2);
+      if (tig < 2 && my < m) a.mass[base + t0 + my] = m_in + w;
     };
     // A warp's blocks of a run of `rows` rows from position t_base on: the
     // blocks lo + warp, lo + warp + 8, .. below hi.  Rows past the last are
@@ -332,10 +362,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
         const float m_in = fetch_mass(t0, m);
         if (lane == 0 && col0 == 0) prefetch(i + kAhead * kWarps);
         const bool late = t0 + m > reach;
-        w0 = w1 = 0.f;
+        w0 = w1 = 0ull;
 #pragma unroll 2
         for (int t = 0; t < tiles; ++t) {
-          float C[2][4], x[4];
+          float C[2][4];
 #pragma unroll
           for (int P = 0; P < 4; ++P) {
             const uint4 q = sm.qb[t][P][lane];
@@ -349,49 +379,57 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
               mma_bf16(C[1], A1, q.z, q.w);
             }
           }
-          const float2 l2 = sm.lse2[t][tig];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = fmaf(C[0][k] + C[1][k], a.scale_log2, (k & 1) ? -l2.y : -l2.x);
-          add(t, x, t0, late);
+          const uint64_t l2 = *reinterpret_cast<const uint64_t*>(&sm.lse2[t][tig]);
+          const uint64_t s2 = pair_of(a.scale_log2, a.scale_log2);
+          add(t, fma_pair(add_pair(pair_of(C[0][0], C[0][1]), pair_of(C[1][0], C[1][1])), s2, l2),
+              fma_pair(add_pair(pair_of(C[0][2], C[0][3]), pair_of(C[1][2], C[1][3])), s2, l2), t0, late);
         }
         store(t0, m, m_in);
       }
     };
-    // Packed rows: a warp has a contiguous run of blocks, so that its pointers
-    // step and one prefetch serves four of them.  A block past the last row
-    // reads on into the segment's padding (whole blocks of 16 rows).
+    // Packed rows: a warp has a contiguous run of blocks, kStages - 1 of them
+    // (rows, scale/zero rows, masses) under way into its part of shared memory.
+    // A block past the last row reads on into the segment's padding (whole
+    // blocks of 16 rows).
     auto run_packed = [&](int lo, int hi) {
       if constexpr (KB < 16) {
+        using R = Ring<KB, G>;
         const int w_lo = lo + (hi - lo) * warp / kWarps, w_hi = lo + (hi - lo) * (warp + 1) / kWarps;
         if (w_lo >= w_hi) return;
-        const int64_t row0 = static_cast<int64_t>(w_lo) * kRows;
-        const uint8_t* kp = hr.vis_k + (row0 + gid) * p.krow;
-        const uint8_t* sp = hr.vis_ksz + (row0 + gid) * p.kszrow;
-        const int kstep = kRows * p.krow, sstep = kRows * p.kszrow;
-        auto prefetch = [&](int i) {  // blocks [i, i + 4)
-          const int m = min(4, w_hi - i);
-          if (m <= 0) return;
-          const int64_t r = static_cast<int64_t>(i) * kRows;
-          prefetch_bytes(hr.vis_k + r * p.krow, m * kstep);
-          prefetch_bytes(hr.vis_ksz + r * p.kszrow, m * sstep);
-          if (a.mass_in) prefetch_bytes(a.mass_in + base + p.vs + r, 4 * min(m * kRows, n_vis - i * kRows));
+        uint8_t* const ring = ring_smem + warp * R::kBytes;
+        auto issue = [&](int i, uint8_t* to) {
+          if (i < w_hi) {
+            const uint8_t* k = hr.vis_k + static_cast<int64_t>(i) * R::kCodes;
+#pragma unroll
+            for (int c = 0; c < R::kCodes / 512; ++c) cp_async16(to + 512 * c + 16 * lane, k + 512 * c + 16 * lane);
+            if (lane < R::kSz / 16)
+              cp_async16(to + R::kCodes + 16 * lane, hr.vis_ksz + static_cast<int64_t>(i) * R::kSz + 16 * lane);
+            if (in_ring && lane >= kRows && lane - kRows < n_vis - i * kRows)
+              cp_async4(to + R::kCodes + R::kSz + 4 * (lane - kRows),
+                        a.mass_in + base + p.vs + static_cast<int64_t>(i) * kRows + lane - kRows);
+          }
+          cp_async_commit();
         };
-        RawRow<KB> r0, r1;
-        float next_mass = 0.f;
-        auto fetch = [&](int i) {
-          load_packed<KB, G>(kp, sp, tig, r0);
-          load_packed<KB, G>(kp + (kstep >> 1), sp + (sstep >> 1), tig, r1);
-          kp += kstep;
-          sp += sstep;
-          next_mass = fetch_mass(p.vs + i * kRows, n_vis - i * kRows);
-        };
-        if (lane == 0 && col0 == 0) prefetch(w_lo);
-        fetch(w_lo);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < R::kStages - 1; ++k) issue(w_lo + k, ring + k * R::kStage);
+        uint8_t* at = ring;                                       // block i
+        uint8_t* into = ring + (R::kStages - 1) * R::kStage;      // block i + kStages - 1, where i - 1 was
+        auto step = [&](uint8_t* x) { return x == ring + (R::kStages - 1) * R::kStage ? ring : x + R::kStage; };
 #pragma unroll 1
         for (int i = w_lo; i < w_hi; ++i) {
           const int m = n_vis - i * kRows, t0 = p.vs + i * kRows;
-          const float m_in = next_mass;
-          if (lane == 0 && col0 == 0 && ((i - w_lo) & 3) == 0) prefetch(i + 4);
+          cp_async_wait<R::kStages - 2>();
+          __syncwarp();
+          issue(i + R::kStages - 1, into);
+          into = step(into);
+          RawRow<KB> r0, r1;
+          load_packed<KB, G>(at + gid * (R::kCodes / kRows), at + R::kCodes + gid * (R::kSz / kRows), tig, r0);
+          load_packed<KB, G>(at + (gid + 8) * (R::kCodes / kRows), at + R::kCodes + (gid + 8) * (R::kSz / kRows), tig, r1);
+          float m_in = 0.f;
+          if (in_ring) m_in = a.decay * *reinterpret_cast<const float*>(at + R::kCodes + R::kSz + 4 * my);
+          else if (col0 > 0) m_in = fetch_mass(t0, m);
+          at = step(at);
           uint32_t f0[4][4], f1[4][4];
           slice_regs<KB>(r0, f0);
           slice_regs<KB>(r1, f1);
@@ -416,14 +454,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
             h2_to_f2(r1.sz.x, z, s1[0]);
           }
           const float kf = a.scale_log2 * (pow2i(24 - k_first_shift<KB>()) / kZbScale);
+          uint64_t s0p[NG], s1p[NG];
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            s0[g] *= kf;
-            s1[g] *= kf;
+            s0p[g] = pair_of(s0[g] * kf, s0[g] * kf);
+            s1p[g] = pair_of(s1[g] * kf, s1[g] * kf);
           }
-          if (i + 1 < w_hi) fetch(i + 1);
           const bool late = t0 + kRows > reach;
-          w0 = w1 = 0.f;
+          w0 = w1 = 0ull;
 #pragma unroll 2
           for (int t = 0; t < tiles; ++t) {
             float C[NG][4], x[4];
@@ -438,14 +476,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
             }
             const uint32_t Z[4] = {za, zc, 0u, 0u};
             mma_f16_new(x, Z, sm.zb[t][lane], 0u);
-            const float2 l2 = sm.lse2[t][tig];
+            uint64_t x0 = pair_of(x[0], x[1]), x1 = pair_of(x[2], x[3]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-              for (int g = 0; g < NG; ++g) x[k] = fmaf(k < 2 ? s0[g] : s1[g], C[g][k], x[k]);
-              x[k] = fmaf(x[k], kZbScale, (k & 1) ? -l2.y : -l2.x);
+            for (int g = 0; g < NG; ++g) {
+              x0 = fma_pair(s0p[g], pair_of(C[g][0], C[g][1]), x0);
+              x1 = fma_pair(s1p[g], pair_of(C[g][2], C[g][3]), x1);
             }
-            add(t, x, t0, late);
+            const uint64_t l2 = *reinterpret_cast<const uint64_t*>(&sm.lse2[t][tig]), z2 = pair_of(kZbScale, kZbScale);
+            add(t, fma_pair(x0, z2, l2), fma_pair(x1, z2, l2), t0, late);
           }
           store(t0, m, m_in);
         }
@@ -462,15 +500,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
   }
 }
 
+struct Kernel {
+  const void* fn;
+  int smem;
+};
+template <int KB, int G>
+Kernel kernel_of() {
+  return {reinterpret_cast<const void*>(&mass_kernel<KB, G>), KB < 16 ? kWarps * Ring<KB, G>::kBytes : 0};
+}
 template <int KB>
-const void* mass_kernel_for(int G) {
-  if constexpr (KB == 16) return reinterpret_cast<const void*>(&mass_kernel<16, 128>);
+Kernel kernel_for(int G) {
+  if constexpr (KB == 16) return kernel_of<16, 128>();
   switch (G) {
-    case 32: return reinterpret_cast<const void*>(&mass_kernel<KB, 32>);
-    case 64: return reinterpret_cast<const void*>(&mass_kernel<KB, 64>);
-    case 128: return reinterpret_cast<const void*>(&mass_kernel<KB, 128>);
+    case 32: return kernel_of<KB, 32>();
+    case 64: return kernel_of<KB, 64>();
+    case 128: return kernel_of<KB, 128>();
   }
-  return nullptr;
+  return {nullptr, 0};
 }
 
 }  // namespace
@@ -480,7 +526,7 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
                                          int32_t n_q, const int32_t* seq_len, int32_t T, const int32_t* path,
                                          int32_t max_path, const int32_t* path_len, float softmax_scale,
                                          const float* mass_in, float decay, float* mass, void* stream) {
-  const kvq_status st = kvq_check_layout(L);
+  kvq_status st = kvq_check_layout(L);
   if (st != KVQ_OK) return st;
   if (!cache || !q_bf16 || !lse || !mass) return KVQ_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(cache) % 256 || reinterpret_cast<uintptr_t>(q_bf16) % 16 ||
@@ -498,11 +544,13 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
   if (units > 0x3fffffffLL || static_cast<int64_t>(L->g) * KVQ_MAX_QUERY_TOKENS > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
-  const void* fn = L->d.k_bits == 2   ? kvq::mass_kernel_for<2>(L->d.group_size)
-                   : L->d.k_bits == 4 ? kvq::mass_kernel_for<4>(L->d.group_size)
-                   : L->d.k_bits == 8 ? kvq::mass_kernel_for<8>(L->d.group_size)
-                                      : kvq::mass_kernel_for<16>(L->d.group_size);
-  if (!fn) return KVQ_ERR_UNSUPPORTED;
+  const kvq::Kernel k = L->d.k_bits == 2   ? kvq::kernel_for<2>(L->d.group_size)
+                        : L->d.k_bits == 4 ? kvq::kernel_for<4>(L->d.group_size)
+                        : L->d.k_bits == 8 ? kvq::kernel_for<8>(L->d.group_size)
+                                           : kvq::kernel_for<16>(L->d.group_size);
+  if (!k.fn) return KVQ_ERR_UNSUPPORTED;
+  st = kvq_allow_smem(k.fn, k.smem);
+  if (st != KVQ_OK) return st;
   kvq::MassArgs a;
   kvq::fill_geom(L, cache, &a.c);
   a.q = static_cast<const uint16_t*>(q_bf16);
@@ -541,5 +589,5 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
     if (worst < 0 || used + a.U[worst] > cap) break;
     ++a.S[worst];
   }
-  return kvq::launch_dependent(fn, dim3(a.U[0] * a.S[0] + a.U[1] * a.S[1]), kvq::kWarps * 32, 0, stream, &a);
+  return kvq::launch_dependent(k.fn, dim3(a.U[0] * a.S[0] + a.U[1] * a.S[1]), kvq::kWarps * 32, k.smem, stream, &a);
 }

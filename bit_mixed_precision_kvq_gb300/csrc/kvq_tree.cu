@@ -101,28 +101,6 @@ const void* kernel_for(int kb, int vb, int G) {
   return nullptr;
 }
 
-// Once per kernel and device: more than 48 KB of shared memory.
-kvq_status prepare(const void* fn) {
-  static std::mutex mu;
-  static const void* done[64][64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return kvq_cuda_fail(e);
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev < 64)
-    for (const void* f : done[dev])
-      if (f == fn) return KVQ_OK;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
-  if (e != cudaSuccess) return kvq_cuda_fail(e);
-  if (dev < 64)
-    for (const void*& f : done[dev])
-      if (!f) {
-        f = fn;
-        break;
-      }
-  return KVQ_OK;
-}
-
 // How many CTAs share a unit of each class: one wave of CTAs on the GPU's SMs
 // (a CTA fills an SM), split so that the longest CTA is as short as it can be.
 // A tile of bf16 rows takes about twice as long as a packed one where rows
@@ -179,6 +157,29 @@ void plan_splits(const kvq_layout* L, int tiles, int n_sm, Args* a) {
 }  // namespace tree
 }  // namespace kvq
 
+// Once per kernel and device: `bytes` of dynamic shared memory, above the 48 KB
+// that every kernel has.
+kvq_status kvq_allow_smem(const void* fn, int bytes) {
+  static std::mutex mu;
+  static const void* done[64][64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return kvq_cuda_fail(e);
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64)
+    for (const void* f : done[dev])
+      if (f == fn) return KVQ_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return kvq_cuda_fail(e);
+  if (dev < 64)
+    for (const void*& f : done[dev])
+      if (!f) {
+        f = fn;
+        break;
+      }
+  return KVQ_OK;
+}
+
 // Checks of the drafted rows shared by the tree's entry points: pointers,
 // strides, and that they do not lie in the cache buffer.
 kvq_status kvq_check_drafts(const kvq_layout* L, const void* cache, const void* k, const void* v, int64_t sb, int64_t sh,
@@ -229,7 +230,7 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
   if (!fn) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
-  st = kvq::tree::prepare(fn);
+  st = kvq_allow_smem(fn, sizeof(kvq::tree::Smem));
   if (st != KVQ_OK) return st;
   kvq::tree::Args a;
   kvq::fill_geom(L, cache, &a.c);
