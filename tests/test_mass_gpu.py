@@ -135,3 +135,20 @@ def test_mass_of_a_decode_call(cuda_dev, kvq):
     torch.cuda.synchronize()
     assert float((mass.double().sum(-1) - 7).abs().max()) <= 7 * 1e-4
     assert not mass[:, :, 1450:].any()
+
+
+@pytest.mark.parametrize("kb,G", [(2, 32), (4, 64), (8, 128)])
+def test_mass_long_runs_and_many_columns(cuda_dev, kvq, kb, G):
+    """Several blocks a warp and two passes over them (96 columns), in place,
+    with lengths that end in the prefix, inside a block and behind the visual
+    rows."""
+    c = Case(80, 32, 2, 700, 9, 650, kb, 2, G, [])
+    F = Filled(c, 5700, cuda_dev)
+    n_q, T = 6, 690
+    q = bf16((80, n_q, 32, 128), 5701, cuda_dev)
+    lens = [T - (7 * b) % 400 for b in range(80)]
+    lens[3], lens[4] = 8, 650
+    lse = _lse(c, f64(q), F.khat, lens, [list(range(n_q))] * 80)
+    mass_in = torch.rand(80, 2, 700, device=cuda_dev)
+    got, before = _run(F, q, lse, T, 0.9, mass_in, lens, in_place=True)
+    check_mass(c, got, f64(q), lse, F.khat, lens, [list(range(n_q))] * 80, f64(mass_in), 0.9, before)
