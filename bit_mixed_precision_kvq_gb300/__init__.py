@@ -383,6 +383,23 @@ def _cache_ptr(what: str, L: Layout, x, dtype, dev: int) -> int:
     return _refuse(what, x, "uint8", None, dev)
 
 
+def _workspace(x, ws_bytes, dev: int):
+    """Address and size of a workspace: a contiguous tensor on device dev, of
+    which ws_bytes may name a part, or a raw address with its size."""
+    if x is None or x.__class__ is int:
+        return x or 0, int(ws_bytes or 0)
+    if x.get_device() != dev:
+        raise ValueError("workspace must be on the current CUDA device")
+    if not x.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    have = x.numel() * x.element_size()
+    if ws_bytes is None:
+        ws_bytes = have
+    elif not 0 <= ws_bytes <= have:
+        raise ValueError(f"workspace has {have} bytes, ws_bytes is {ws_bytes}")
+    return x.data_ptr(), int(ws_bytes)
+
+
 def _drafts(k, v, shape, dtype, dev: int):
     """Addresses and strides of the drafted rows ([B, H_kv, n_q, D], last
     dimension contiguous)."""
@@ -443,12 +460,11 @@ def decode_attention_tree(L: Layout, cache, q, k_draft, v_draft, tree_mask, T_ct
                 ((n_q,) if tree_mask.dim() == 1 else (1, n_q)) if shared else (B, n_q), dev)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d.D)
-    if ws_bytes is None:
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    wp, ws_bytes = _workspace(workspace, ws_bytes, dev)
     st = load().kvq_decode_attention_tree(
         ctypes.byref(L), cp, qp, kp, vp, sb, sh, sd, n_q, mask, 0 if shared else n_q,
         _ptr("seq_len", seq_len, torch.int32, (B,), dev), T_ctx, softmax_scale,
-        _ptr("out", out, bf16, rows, dev), _ptr("lse", lse, torch.float32, (B, n_q, Hq), dev), _addr(workspace), ws_bytes, st)
+        _ptr("out", out, bf16, rows, dev), _ptr("lse", lse, torch.float32, (B, n_q, Hq), dev), wp, ws_bytes, st)
     if st != 0:
         raise KvqError(st, "kvq_decode_attention_tree")
 
