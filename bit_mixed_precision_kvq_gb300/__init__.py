@@ -383,6 +383,14 @@ def _cache_ptr(what: str, L: Layout, x, dtype, dev: int) -> int:
     return _refuse(what, x, "uint8", None, dev)
 
 
+def _i32(what: str, x) -> int:
+    """x as the int32 that the C call takes (ctypes would drop higher bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{what} must be an int32, got {x}")
+    return x
+
+
 def _workspace(x, ws_bytes, dev: int):
     """Address and size of a workspace: a contiguous tensor on device dev, of
     which ws_bytes may name a part, or a raw address with its size."""
@@ -463,7 +471,7 @@ def decode_attention_tree(L: Layout, cache, q, k_draft, v_draft, tree_mask, T_ct
     wp, ws_bytes = _workspace(workspace, ws_bytes, dev)
     st = load().kvq_decode_attention_tree(
         ctypes.byref(L), cp, qp, kp, vp, sb, sh, sd, n_q, mask, 0 if shared else n_q,
-        _ptr("seq_len", seq_len, torch.int32, (B,), dev), T_ctx, softmax_scale,
+        _ptr("seq_len", seq_len, torch.int32, (B,), dev), _i32("T_ctx", T_ctx), softmax_scale,
         _ptr("out", out, bf16, rows, dev), _ptr("lse", lse, torch.float32, (B, n_q, Hq), dev), wp, ws_bytes, st)
     if st != 0:
         raise KvqError(st, "kvq_decode_attention_tree")
@@ -485,7 +493,7 @@ def tree_commit(L: Layout, cache, k_draft, v_draft, path, path_len, T_ctx: int, 
     st = load().kvq_tree_commit(
         ctypes.byref(L), _cache_ptr("cache", L, cache, torch.uint8, dev), kp, vp, sb, sh, sd, n_q,
         _ptr("path", path, i32, (B, max_path), dev), max_path, _ptr("path_len", path_len, i32, per_seq, dev),
-        _ptr("seq_len", seq_len, i32, per_seq, dev), T_ctx, _ptr("new_len", new_len, i32, per_seq, dev), st)
+        _ptr("seq_len", seq_len, i32, per_seq, dev), _i32("T_ctx", T_ctx), _ptr("new_len", new_len, i32, per_seq, dev), st)
     if st != 0:
         raise KvqError(st, "kvq_tree_commit")
 
@@ -504,7 +512,7 @@ def attention_mass(L: Layout, cache, q, lse, T: int, mass, mass_in=None, softmax
     n_q = q.shape[1] if q.dim() == 4 else 1
     rows = (B, n_q, d.H_q) if q.dim() == 4 else (B, d.H_q)
     acc, per_seq = (B, d.H_kv, d.T_cap), (B,)
-    max_path = 0
+    T, max_path = _i32("T", T), 0
     if path is not None:
         max_path = path.shape[1] if path.dim() == 2 else 0
     if softmax_scale is None:
@@ -528,6 +536,7 @@ def cache_evict(L: Layout, cache, mass, T: int, L_dst: Layout, cache_dst, T_dst:
     torch, dev, st = _current(stream)
     d, f32, i32, u8 = L.d, torch.float32, torch.int32, torch.uint8
     B, H = d.B, d.H_kv
+    T, T_dst, n_recent = _i32("T", T), _i32("T_dst", T_dst), _i32("n_recent", n_recent)
     st = load().kvq_cache_evict(
         ctypes.byref(L), _cache_ptr("cache", L, cache, u8, dev), _ptr("mass", mass, f32, (B, H, d.T_cap), dev),
         _ptr("seq_len", seq_len, i32, (B,), dev), T, ctypes.byref(L_dst), _cache_ptr("cache_dst", L_dst, cache_dst, u8, dev),

@@ -1,5 +1,5 @@
-"""What the Python binding of the serving calls checks of a workspace
-before the C call sees it (no GPU: the current device and the
+"""What the Python binding of the serving calls checks of a workspace and of
+its integers, before the C call sees them (no GPU: the current device and the
 library are stood in for)."""
 import types
 
@@ -77,3 +77,35 @@ def test_tree_workspace_is_checked(L):
     _tree(L, None)
     assert [c[-3:-1] for c in L.calls] == [(FAR, 100), (FAR, 64), (FAR, 77), (0, 0)]
 
+
+def test_integers_are_converted_or_refused(L):
+    """Whole numbers of other types are taken, and what an int32 does not
+    hold is refused and not cut to 32 bits."""
+    import numpy as np
+    import torch
+    mass = torch.zeros(2, 4, 256)
+    i32 = dict(dtype=torch.int32)
+    kd = torch.zeros(2, 4, 3, 128, dtype=torch.bfloat16)
+    lse, q = torch.zeros(2, 3, 8), torch.zeros(2, 3, 8, 128, dtype=torch.bfloat16)
+
+    def calls(T, T_dst=120, recent=4):
+        yield lambda: _tree(L, Elsewhere(-1), T)
+        yield lambda: kvq.tree_commit(L, FAKE, kd, kd, torch.zeros(2, 2, **i32), torch.zeros(2, **i32), T)
+        yield lambda: kvq.attention_mass(L, FAKE, q, lse, T, mass)
+        yield lambda: kvq.cache_evict(L, FAKE, mass, T, L.smaller, FAR, T_dst, torch.zeros(2, 4, int(T_dst), **i32), recent)
+
+    for T in (2 ** 32 + 220, -2 ** 31 - 1):
+        for f in calls(T):
+            with pytest.raises(ValueError, match="int32"):
+                f()
+    for kw in (dict(recent=2 ** 32 + 4),):
+        with pytest.raises(ValueError, match="int32"):
+            list(calls(220, **kw))[-1]()
+    assert not L.calls
+    for T in (220, np.int64(220), torch.tensor(220)):
+        for f in calls(T, np.int32(120), np.int64(4)):
+            f()
+    assert len(L.calls) == 12
+    for c in L.calls:
+        assert all(type(x) in (int, float) or "Layout" in str(type(x)) or "byref" in str(type(x)) or "CArg" in str(type(x))
+                   for x in c), [type(x) for x in c]
