@@ -462,6 +462,7 @@ extern "C" kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, co
   if (T < s.vis_end || T < 1 || T > s.T_cap) return KVQ_ERR_INVALID_ARG;
   if (L_dst->Tv > L->Tv || T_dst < d.vis_end || T_dst < 1) return KVQ_ERR_INVALID_ARG;
   if (T_dst > d.T_cap) return KVQ_ERR_CAPACITY;
+  if (T > kvq::kMaxLen || d.T_cap > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;  // the tail of mass_dst goes to T_cap
   if (n_recent < 0 || n_recent > T_dst - d.vis_end) return KVQ_ERR_INVALID_ARG;
   const int64_t bh = static_cast<int64_t>(s.B) * s.H_kv;
   if (kvq::ranges_meet(cache, L->total_bytes, cache_dst, L_dst->total_bytes) ||

@@ -15,6 +15,9 @@ kvq_status kvq_allow_smem(const void* fn, int bytes);
 namespace kvq {
 
 constexpr int kRowBytes = 2 * kD;  // a bf16 row
+// The longest sequence of the tree, mass and eviction calls: positions are
+// 32-bit, and tiles, strides of a CTA and prefetches run past the last one.
+constexpr int32_t kMaxLen = 0x7fffffff - 0xffff;
 
 struct Geom {
   int32_t B, Hq, Hkv, g;

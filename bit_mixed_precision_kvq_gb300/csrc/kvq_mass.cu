@@ -535,6 +535,7 @@ extern "C" kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache,
       reinterpret_cast<uintptr_t>(path) % 4 || reinterpret_cast<uintptr_t>(path_len) % 4)
     return KVQ_ERR_INVALID_ARG;
   if (n_q < 1 || n_q > KVQ_MAX_QUERY_TOKENS || T < 1 || T > L->d.T_cap) return KVQ_ERR_INVALID_ARG;
+  if (T > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;
   if (!path != !path_len) return KVQ_ERR_INVALID_ARG;
   if (path ? (max_path < 1 || max_path > KVQ_MAX_QUERY_TOKENS) : (!seq_len && n_q > T)) return KVQ_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale) || !std::isfinite(decay)) return KVQ_ERR_INVALID_ARG;

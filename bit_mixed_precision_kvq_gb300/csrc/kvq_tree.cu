@@ -221,6 +221,7 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
     return KVQ_ERR_INVALID_ARG;
   if (mask_stride_b != 0 && mask_stride_b < n_q) return KVQ_ERR_INVALID_ARG;
   if (T_ctx < 0 || T_ctx > L->d.T_cap || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  if (T_ctx > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;
   if (ws_bytes < static_cast<size_t>(kvq::tree::ws_bytes_of(L, n_q))) return KVQ_ERR_CAPACITY;
   const int64_t rows = static_cast<int64_t>(L->d.B) * n_q * L->d.H_q;
   const kvq::tree::Columns cols = kvq::tree::columns_of(L, n_q);

@@ -363,6 +363,7 @@ kvq_status kvq_sensitivity_probe(const kvq_layout* L, const void* cache, const v
  *             T_ctx.  An entry outside [0, T_ctx] marks an inactive sequence
  *             (outputs zero, lse -inf)
  *   T_ctx     0 <= T_ctx <= T_cap: the (largest) context length
+ *             (KVQ_ERR_UNSUPPORTED above 2^31 - 2^16)
  *   out_bf16  device bf16 [B][n_q][H_q][D];  lse  fp32 [B][n_q][H_q] or NULL
  *   workspace at least kvq_decode_tree_workspace_bytes(L, n_q) bytes,
  *             256-byte aligned, first 4 bytes the status word; other contents
@@ -419,7 +420,8 @@ kvq_status kvq_tree_commit(const kvq_layout* L, void* cache, const void* k_draft
  *             tokens returned it; -inf or +inf: that row adds nothing
  *   seq_len   device int32 [B] of lengths, the tokens' own positions
  *             included, or NULL: every len_b is T
- *   T         1 <= T <= T_cap: the (largest) length
+ *   T         1 <= T <= T_cap: the (largest) length (KVQ_ERR_UNSUPPORTED above
+ *             2^31 - 2^16)
  *   path, max_path, path_len   the tokens taken, as in kvq_tree_commit (an
  *             entry outside [0, n_q) adds nothing), or NULL, 0, NULL: all
  *             n_q tokens in order (then n_q <= T without seq_len)
@@ -448,6 +450,7 @@ kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache, const void
  * rows bit for bit, never requantised).
  *   mass      device fp32 [B][H_kv][T_cap]
  *   seq_len, T   lengths as in kvq_attention_mass; T >= vis_end
+ *             (KVQ_ERR_UNSUPPORTED if T or T_cap_dst is above 2^31 - 2^16)
  *   L_dst, cache_dst   a layout that differs from L only in vis_end (a visual
  *             block of at most L's size) and T_cap, and its buffer, which
  *             must not overlap cache
