@@ -23,7 +23,7 @@ SOURCES = ["kvq_layout.cpp", "kvq_append.cu", "kvq_decode.cu", "kvq_split_k2.cu"
            "kvq_mq_umma_k16.cu", "kvq_tree.cu", "kvq_tree_k2.cu", "kvq_tree_k4.cu", "kvq_tree_k8.cu",
            "kvq_tree_k16.cu", "kvq_tree_commit.cu", "kvq_mass.cu", "kvq_evict.cu"]
 HEADERS = ["kvq_internal.h", "kvq_device.cuh", "kvq_ptx.cuh", "kvq_split.cuh", "kvq_split_inst.cuh", "kvq_umma.cuh",
-           "kvq_mq_umma.cuh", "kvq_geom.cuh", "kvq_tree.cuh"]
+           "kvq_mq_umma.cuh", "kvq_geom.cuh", "kvq_tree.cuh", "kvq_tree_plan.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

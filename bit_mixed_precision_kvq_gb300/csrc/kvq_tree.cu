@@ -101,58 +101,6 @@ const void* kernel_for(int kb, int vb, int G) {
   return nullptr;
 }
 
-// How many CTAs share a unit of each class: one wave of CTAs on the GPU's SMs
-// (a CTA fills an SM), split so that the longest CTA is as short as it can be.
-// A tile of bf16 rows takes about twice as long as a packed one where rows
-// come from HBM (16K x 8: 3.6 against 1.7 us).  With more units than SMs every
-// unit has one CTA, the dearest first.
-constexpr int kTileCost[3] = {4, 3, 2};  // protected, K-only, packed
-void plan_splits(const kvq_layout* L, int tiles, int n_sm, Args* a) {
-  const int n[3] = {L->n_prot, L->n_konly, L->n_packed};
-  const int cap = std::min(n_sm, kMaxSplitCtas);
-  int64_t units = 0;
-  for (int k = 0, h = 0; k < 3; ++k) {
-    a->U[k] = L->d.B * n[k] * a->nblk;
-    a->S[k] = 1;
-    a->head0[k] = h;
-    h += n[k];
-    units += a->U[k];
-  }
-  if (units >= cap || tiles <= 1) return;
-  // CTAs when no CTA of class k has more than m[k] tiles
-  auto splits = [&](int m) { return (tiles + m - 1) / m; };
-  auto ctas = [&](const int (&m)[3]) {
-    int64_t c = 0;
-    for (int k = 0; k < 3; ++k) c += static_cast<int64_t>(a->U[k]) * splits(m[k]);
-    return c;
-  };
-  int lo = kTileCost[0], hi = kTileCost[0] * tiles;  // the longest CTA's time: hi always fits
-  int m[3];
-  auto within = [&](int x) {
-    for (int k = 0; k < 3; ++k) m[k] = std::min(tiles, x / kTileCost[k]);
-    return ctas(m) <= cap;
-  };
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (within(mid)) hi = mid;
-    else lo = mid + 1;
-  }
-  within(hi);
-  for (bool more = true; more;) {  // what is left over: fewer tiles for any class
-    more = false;
-    for (int k = 2; k >= 0; --k)
-      while (a->U[k] && m[k] > 1) {
-        --m[k];
-        if (ctas(m) > cap) {
-          ++m[k];
-          break;
-        }
-        more = true;
-      }
-  }
-  for (int k = 0; k < 3; ++k) a->S[k] = splits(m[k]);
-}
-
 }  // namespace
 }  // namespace tree
 }  // namespace kvq
@@ -259,7 +207,7 @@ extern "C" kvq_status kvq_decode_attention_tree(const kvq_layout* L, const void*
   for (int k = 0; k < L->n_prot; ++k) a.head[h++] = L->prot_head[k];
   for (int k = 0; k < L->n_konly; ++k) a.head[h++] = L->konly_head[k];
   for (int k = 0; k < L->n_packed; ++k) a.head[h++] = L->packed_head[k];
-  kvq::tree::plan_splits(L, (T_ctx + n_q + kvq::tree::kTile - 1) / kvq::tree::kTile, n_sm, &a);
+  kvq::tree::plan_splits(L, cols.nblk, (T_ctx + n_q + kvq::tree::kTile - 1) / kvq::tree::kTile, n_sm, a.U, a.S, a.head0);
   const int grid = a.U[0] * a.S[0] + a.U[1] * a.S[1] + a.U[2] * a.S[2];
   st = kvq::launch_dependent(fn, dim3(grid), kvq::tree::kThreads, sizeof(kvq::tree::Smem), stream, &a);
   if (st != KVQ_OK || (a.S[0] == 1 && a.S[1] == 1 && a.S[2] == 1)) return st;

@@ -60,6 +60,7 @@
 #pragma once
 
 #include "kvq_geom.cuh"
+#include "kvq_tree_plan.h"
 #include "kvq_umma.cuh"
 
 namespace kvq {
@@ -73,7 +74,6 @@ constexpr int kAhead = 4;               // tiles that the L2 prefetch runs ahead
 constexpr int kTile = 128;              // positions per tile (TMEM lanes)
 constexpr int kMaxCols = 64;            // columns per unit (at most)
 constexpr int kHalfCols = kMaxCols / 2;  // columns of a softmax thread
-constexpr int kMaxSplitCtas = 160;      // CTAs of a call whose units are split (workspace slots)
 constexpr float kMaxGrowth = 15.f;      // log2 of the largest P (fp16)
 constexpr float kLift = 3.f;            // log2 of the P of a score that sets its reference
 constexpr float kUnset = -1e30f;        // reference of a column that has attended nothing
