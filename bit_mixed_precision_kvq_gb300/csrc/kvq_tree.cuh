@@ -34,11 +34,19 @@
 // z' = z + (c - c') s.  c' s is exact in fp16 for 2 bits and an exact
 // (high, low) fp16 pair for 4 and 8 bits, two MMAs; z' goes in as one more
 // K step, an fp16 (high, low) pair against the (high, low) pair of the query's
-// group sums (22 bits).  bf16 rows are exact in fp16.  K operands carry a
-// factor 1/2 and queries 2^-7, so that values up to 65504 do not overflow;
-// both powers of two are undone by the softmax scale.  V is dequantised to
-// fp16 (one rounding, 2^-11 of the value, below the output's 2^-8), P is
-// fp16 (2^-11), O and the softmax sums are fp32.
+// group sums (22 bits).  K operands carry a factor 1/2, so that values up to
+// 65504 do not overflow.  fp16 holds bf16's 8 bits down to 2^-17, so K is exact
+// from 2^-16 up, and off by at most 2^-24 below (2^-23 with its zero point),
+// which is where the stored scales and zeros, fp16 too, have their last bits
+// (halved scales below 2^-13 lose theirs).
+// Every column of queries has a power of two of its own, by which its largest
+// element lands in [2^8, 2^9) (128 of them sum to 65280 at most): exact down to
+// 2^-25 of that element, off by 2^-33 of it below.  It is undone by the column's
+// softmax scale.  (With one factor 2^-7 for all, queries of 5e-4 against keys of
+// 2e4 gave scores off by 0.15; the scale per column takes 0.5% at 16K x 8.)
+// V is dequantised to fp16 (one rounding, 2^-11 of the value, below the
+// output's 2^-8; steps of 2^-24 below 2^-14), P is fp16 (2^-11), O and the
+// softmax sums are fp32.
 //
 // Softmax: a thread owns a position (a TMEM lane) and all columns, so the
 // maximum of a column would be a reduction over 128 lanes.  Instead every
@@ -77,7 +85,7 @@ constexpr int kHalfCols = kMaxCols / 2;  // columns of a softmax thread
 constexpr float kMaxGrowth = 15.f;      // log2 of the largest P (fp16)
 constexpr float kLift = 3.f;            // log2 of the P of a score that sets its reference
 constexpr float kUnset = -1e30f;        // reference of a column that has attended nothing
-constexpr float kOperandScale = 256.f;  // undoes K / 2 and q / 2^7
+constexpr int kQueryExponent = 8;       // a column's largest |q| lands in [2^8, 2^9)
 
 constexpr uint32_t kTmK = 0, kTmKStride = 136, kTmLo = 64, kTmZ = 128;
 constexpr uint32_t kTmS = 272, kTmSStride = 64;
@@ -112,6 +120,7 @@ struct Smem {
   alignas(128) uint8_t qz[kMaxCols * 32];     // group sums of q: column, 16 K indexes
   uint64_t colmask[kMaxCols];
   alignas(16) float neg_m[kMaxCols];  // minus the references
+  alignas(16) float scale[kMaxCols];  // what takes a column's S to its score in log2 units
   alignas(16) float fac[kMaxCols];
   float lsum[4][kMaxCols];  // per softmax warp: column maxima of a tile; at the end column sums
   float qs[kMaxCols][4];
@@ -795,10 +804,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         r[t] = ok ? __ldcg(reinterpret_cast<const uint4*>(a.q + row * kD) + 4 * P + t) : make_uint4(0u, 0u, 0u, 0u);
+      // The column's power of two f = 2^e, from the exponent of its largest |q|
+      // (four threads have its quarters); 2^e and 2^-e are fp32 for every bf16.
+      uint32_t top = 0u;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t v = j == 0 ? r[t].x : (j == 1 ? r[t].y : (j == 2 ? r[t].z : r[t].w));
+          top = max(top, max(v & 0x7fffu, (v >> 16) & 0x7fffu));
+        }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(100, kQueryExponent + 127 - static_cast<int>(top >> 7));
+      const float f = __int_as_float((127 + e) << 23);
+      if (P == 0) sm.scale[c] = 2.f * (a.scale_log2 * __int_as_float((127 - e) << 23));  // K entered halved
       float sum = 0.f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        constexpr float f = 1.f / 128.f;
         const uint32_t y[4] = {
             pack_f16x2(f * bf16_lo(r[t].x), f * bf16_lo(r[t].z)), pack_f16x2(f * bf16_hi(r[t].x), f * bf16_hi(r[t].z)),
             pack_f16x2(f * bf16_lo(r[t].y), f * bf16_lo(r[t].w)), pack_f16x2(f * bf16_hi(r[t].y), f * bf16_hi(r[t].w))};
@@ -835,7 +858,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     named_bar(1, kSoftmaxThreads);
     if (lane == 0) mbar_arrive(&sm.q_ready);
 
-    const float sl2 = a.scale_log2 * kOperandScale;
     // this thread's position of a tile (a TMEM lane) and its columns [ch, ce)
     const int lp = 32 * (warp & 3) + lane;
     const int ch = (N / 2 + 15) / 16 * 16 * (warp >> 2), ce = warp < 4 ? min(N, (N / 2 + 15) / 16 * 16) : N;
@@ -843,7 +865,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     uint64_t l2[kHalfCols / 2];  // sums of its columns, in pairs
 #pragma unroll
     for (int c = 0; c < kHalfCols / 2; ++c) l2[c] = 0ull;
-    const uint64_t scale2 = pair_of(sl2, sl2);
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const int n = i - i0, buf = n & 1;
@@ -868,8 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
           const ulonglong2 mm = *reinterpret_cast<const ulonglong2*>(&sm.neg_m[c0 + k]);
-          unpair(fma_pair(pair_of(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, mm.x), x[k], x[k + 1]);
-          unpair(fma_pair(pair_of(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), scale2, mm.y), x[k + 2], x[k + 3]);
+          const ulonglong2 ss = *reinterpret_cast<const ulonglong2*>(&sm.scale[c0 + k]);
+          unpair(fma_pair(pair_of(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), ss.x, mm.x), x[k], x[k + 1]);
+          unpair(fma_pair(pair_of(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), ss.y, mm.y), x[k + 2], x[k + 3]);
         }
       };
       auto hide16 = [&](int c0, float (&x)[16]) {
@@ -894,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             tmem_ld16(sb + c0, s);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]) * sl2;
+            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]) * sm.scale[c0 + k];
             if (!whole) hide16(c0, x);
             float mine = -INFINITY;  // lane k: the maximum of column c0 + k over the warp's positions
 #pragma unroll

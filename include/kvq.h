@@ -370,8 +370,10 @@ kvq_status kvq_sensitivity_probe(const kvq_layout* L, const void* cache, const v
  *             on entry are ignored; overlapping calls must not share it
  * A token that attends nothing (empty context, empty mask) gets output zero
  * and lse -inf.  Drafted rows that no token of their sequence attends may
- * hold anything; all other values are finite, |x| <= 65504, and scores
- * softmax_scale * q.k stay below 2^20 in size (they are fp32).
+ * hold anything; all other values are finite, K and V |x| <= 65504, and scores
+ * softmax_scale * q.k stay below 2^20 in size (they are fp32).  q may be of any
+ * size.  V passes through fp16: it is rounded to 2^-11 of itself and, below
+ * 2^-14, to steps of 2^-24.
  * kvq_decode_tree_workspace_bytes returns 0 for an invalid layout or n_q.
  */
 size_t kvq_decode_tree_workspace_bytes(const kvq_layout* L, int32_t n_q);

@@ -1,0 +1,89 @@
+"""The serving calls away from unit scale: small queries against large keys,
+large against small, columns of very different size in one call, and small
+values."""
+import numpy as np
+import pytest
+import torch
+
+import bit_mixed_precision_kvq_gb300 as kvq
+import oracle
+from gpu_helpers import Case, bits
+from serving_ref import SCALE, Filled, bf16, f64, masks_to, random_tree, score_error, tree_reference
+
+pytestmark = pytest.mark.gpu
+
+
+def _tree(F, q, kd, vd, masks, T, dev):
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full(q.shape[:3], 9.0, device=dev)
+    ws = torch.zeros(kvq.decode_tree_workspace_bytes(F.L, q.shape[1]), dtype=torch.uint8, device=dev)
+    kvq.decode_attention_tree(F.L, F.cache, q, kd, vd, masks_to(dev, masks), T, out, SCALE, lse, ws)
+    torch.cuda.synchronize()
+    assert kvq.workspace_status(ws) == 0
+    return out, lse
+
+
+def _scaled(c, seed, dev, n_q, qs, ks, vs):
+    """A cache, drafts and queries of the given sizes (qs: one per token),
+    below 6e4 in size, and what the cache stands for."""
+    F = Filled(c, seed, dev)
+    clip = lambda x, s: (x.float() * s).clamp(-6e4, 6e4).to(torch.bfloat16)  # noqa: E731
+    k, v = clip(F.k, ks), clip(F.v, vs)
+    kvq.quantize_append(F.L, F.cache, k, v, 0)
+    khat = oracle.reconstruct(bits(k), c.vs, c.ve, c.mask(), c.kb, c.G)[0]
+    vhat = oracle.reconstruct(bits(v), c.vs, c.ve, [1 if x == 1 else 0 for x in c.mask()], c.vb, c.G)[0]
+    x = bf16((2, c.B, n_q, c.H_kv, 128), seed + 2, dev)
+    kd, vd = clip(x[0], ks).transpose(1, 2), clip(x[1], vs).transpose(1, 2)
+    per_token = torch.tensor([qs[i % len(qs)] for i in range(n_q)], device=dev)[:, None, None]
+    q = clip(bf16((c.B, n_q, c.H_q, 128), seed + 3, dev), per_token)
+    return F, khat, vhat, q, kd, vd
+
+
+# sizes of the queries (in turn over the tokens) and of the keys
+SIZES = [([5e-4], 2e4), ([1e-3], 1e3), ([1e-2], 1e2), ([1e2], 0.1), ([1.0, 1e-6, 5e-4, 1e2, 0.0], 1e2),
+         ([3e-9, 1e-30, 3e-3], 1e4)]
+
+
+def _check_scores(c, seed, dev, qs, ks):
+    """lse and output within the bounds of unit scale, plus what K's smallest
+    step in the operands (an element of K is off by 2^-23 at most, its zero
+    point included) makes of a score."""
+    n_q, T = 6, 321
+    F, khat, vhat, q, kd, vd = _scaled(c, seed, dev, n_q, qs, ks, 1.0)
+    masks = random_tree(n_q, 1, 5)
+    out, lse = _tree(F, q, kd, vd, masks, T, dev)
+    qf, kdf, vdf = f64(q), f64(kd), f64(vd)
+    ref, lr = tree_reference(c, qf, khat, vhat, kdf, vdf, masks, [T])
+    se = score_error(qf, khat, kdf) + 2.0 ** -23 * SCALE * np.abs(qf).sum(-1)
+    le = np.abs(f64(lse) - lr) / (se + 2.0 ** -22 * (1 + np.abs(lr)))
+    assert le.max() <= 1, f"lse: worst err / tol {le.max():.3g}"
+    vmax = np.repeat(np.maximum(np.abs(vhat).max(axis=(2, 3)), np.abs(vdf).max(axis=(2, 3))), 3, axis=1)[:, None, :, None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 330 * 2.0 ** -28 + 2 * se[..., None]) * vmax
+    oe = np.abs(f64(out) - ref) / tol
+    assert oe.max() <= 1, f"out: worst err / tol {oe.max():.3g}"
+
+
+@pytest.mark.parametrize("kb", [2, 4, 8, 16])
+@pytest.mark.parametrize("si", range(len(SIZES)))
+def test_tree_scores_of_any_size(cuda_dev, kvq, si, kb):
+    _check_scores(Case(1, 9, 3, 330, 13, 300, kb, 4, 32, [1], konly=[2]), 8000 + 10 * si, cuda_dev, *SIZES[si])
+
+
+@pytest.mark.parametrize("vs", [1e-6, 1e-3, 1.0, 2e4])
+@pytest.mark.parametrize("vb", [2, 4, 8, 16])
+def test_tree_values_of_any_size(cuda_dev, kvq, vb, vs):
+    """Values are rounded to 2^-11 of themselves or, below 2^-14, to steps of
+    2^-24; a weighted mean of them is off by no more than one of them, plus
+    the weights' own 2^-11."""
+    c = Case(1, 9, 3, 330, 13, 300, 4, vb, 32, [1], konly=[2])
+    n_q, T = 6, 321
+    F, khat, vhat, q, kd, vd = _scaled(c, 8200, cuda_dev, n_q, [1.0], 1.0, vs)
+    masks = random_tree(n_q, 1, 5)
+    out, lse = _tree(F, q, kd, vd, masks, T, cuda_dev)
+    qf, kdf, vdf = f64(q), f64(kd), f64(vd)
+    ref, lr = tree_reference(c, qf, khat, vhat, kdf, vdf, masks, [T])
+    se = score_error(qf, khat, kdf)[..., None]
+    vmax = np.repeat(np.maximum(np.abs(vhat).max(axis=(2, 3)), np.abs(vdf).max(axis=(2, 3))), 3, axis=1)[:, None, :, None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 330 * 2.0 ** -28 + 2 * se) * vmax + 2.0 ** -24
+    oe = np.abs(f64(out) - ref) / tol
+    assert oe.max() <= 1, f"out: worst err / tol {oe.max():.3g}"
