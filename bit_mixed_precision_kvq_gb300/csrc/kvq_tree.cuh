@@ -37,8 +37,7 @@
 // group sums (22 bits).  K operands carry a factor 1/2, so that values up to
 // 65504 do not overflow.  fp16 holds bf16's 8 bits down to 2^-17, so K is exact
 // from 2^-16 up, and off by at most 2^-24 below (2^-23 with its zero point),
-// which is where the stored scales and zeros, fp16 too, have their last bits
-// (halved scales below 2^-13 lose theirs).
+// which is where the stored scales and zeros, fp16 too, have their last bits.
 // Every column of queries has a power of two of its own, by which its largest
 // element lands in [2^8, 2^9) (128 of them sum to 65280 at most): exact down to
 // 2^-25 of that element, off by 2^-33 of it below.  It is undone by the column's
@@ -201,11 +200,11 @@ __device__ __forceinline__ uint32_t h2(float x) {  // both halves
   return pack_f16x2(x, x);
 }
 
-template <int P2>  // code at bit P2 of each half of x -> code - off
+template <int P2, int H = 0>  // code at bit P2 of each half of x -> (code - off) / 2^H
 __device__ __forceinline__ uint32_t code_at(uint32_t x, uint32_t mask, float off) {
   const uint32_t v = and_or(x, mask << P2, 0x64006400u);
-  if constexpr (P2 == 0) return hsub2_u(v, h2(1024.f + off));
-  return hfma2_u(v, h2(1.f / (1 << P2)), h2(-(1024.f / (1 << P2) + off)));
+  if constexpr (P2 + H == 0) return hsub2_u(v, h2(1024.f + off));
+  return hfma2_u(v, h2(1.f / (1 << (P2 + H))), h2(-(1024.f / (1 << P2) + off) / (1 << H)));
 }
 
 template <int KB>
@@ -213,7 +212,7 @@ __device__ __forceinline__ constexpr float k_center() {
   return KB == 2 ? 1.f : (KB == 4 ? 8.f : 128.f);
 }
 
-// c' of the 16 pairs (4 P + i) of slice t of a K row, from its words.
+// c' / 2 of the 16 pairs (4 P + i) of slice t of a K row, from its words.
 template <int KB>
 __device__ __forceinline__ void k_codes(const uint32_t* x, uint32_t (&c)[16]) {
   constexpr float off = k_center<KB>();
@@ -222,23 +221,23 @@ __device__ __forceinline__ void k_codes(const uint32_t* x, uint32_t (&c)[16]) {
     for (int h = 0; h < 2; ++h) {
       const uint32_t w = x[h], y = w >> 6;
       uint32_t* o = c + 2 * h;  // i = 2 h, 2 h + 1
-      o[0] = code_at<8>(w, 0x00030003u, off);
-      o[1] = code_at<8>(y, 0x00030003u, off);
-      o[4] = code_at<6>(w, 0x00030003u, off);
-      o[5] = code_at<6>(y, 0x00030003u, off);
-      o[8] = code_at<4>(w, 0x00030003u, off);
-      o[9] = code_at<4>(y, 0x00030003u, off);
-      o[12] = code_at<0>(w, 0x00030003u, off);
-      o[13] = code_at<2>(w, 0x00030003u, off);
+      o[0] = code_at<8, 1>(w, 0x00030003u, off);
+      o[1] = code_at<8, 1>(y, 0x00030003u, off);
+      o[4] = code_at<6, 1>(w, 0x00030003u, off);
+      o[5] = code_at<6, 1>(y, 0x00030003u, off);
+      o[8] = code_at<4, 1>(w, 0x00030003u, off);
+      o[9] = code_at<4, 1>(y, 0x00030003u, off);
+      o[12] = code_at<0, 1>(w, 0x00030003u, off);
+      o[13] = code_at<2, 1>(w, 0x00030003u, off);
     }
   } else if constexpr (KB == 4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = x[i], y = w >> 8;
-      c[i] = code_at<0>(w, 0x000F000Fu, off);
-      c[4 + i] = code_at<4>(w, 0x000F000Fu, off);
-      c[8 + i] = code_at<0>(y, 0x000F000Fu, off);
-      c[12 + i] = code_at<4>(y, 0x000F000Fu, off);
+      c[i] = code_at<0, 1>(w, 0x000F000Fu, off);
+      c[4 + i] = code_at<4, 1>(w, 0x000F000Fu, off);
+      c[8 + i] = code_at<0, 1>(y, 0x000F000Fu, off);
+      c[12 + i] = code_at<4, 1>(y, 0x000F000Fu, off);
     }
   } else if constexpr (KB == 8) {
 #pragma unroll
@@ -246,7 +245,7 @@ __device__ __forceinline__ void k_codes(const uint32_t* x, uint32_t (&c)[16]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t w = x[2 * P + (i >> 1)];
-        c[4 * P + i] = code_at<0>((i & 1) ? w >> 8 : w, 0x00FF00FFu, off);
+        c[4 * P + i] = code_at<0, 1>((i & 1) ? w >> 8 : w, 0x00FF00FFu, off);
       }
   }
 }
@@ -424,7 +423,7 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// c' -> the high (and low) fp16 parts of c' s / 2, in place and in lo.
+// c' / 2 -> the high (and low) fp16 parts of c' s / 2, in place and in lo.
 template <int KB>
 __device__ __forceinline__ void k_parts(uint32_t (&c)[16], const uint32_t (&s2)[4], uint32_t (&lo)[16]) {
 #pragma unroll
@@ -438,7 +437,7 @@ __device__ __forceinline__ void k_parts(uint32_t (&c)[16], const uint32_t (&s2)[
 }
 
 // The zero points' A row: z' / 2 as (high, low, high) of each group, groups
-// in pairs (words 0-1, 2-3, 4-5); and s / 2 of the four 32-element blocks.
+// in pairs (words 0-1, 2-3, 4-5).
 template <int KB, int G>
 __device__ __forceinline__ void z_parts(const uint4& sz, uint32_t (&zz)[8]) {
 #pragma unroll
@@ -460,22 +459,19 @@ __device__ __forceinline__ void z_parts(const uint4& sz, uint32_t (&zz)[8]) {
     zz[2 + w] = pack_f16x2(z0 - h0, z1 - h1);
   }
 }
+// s of the four 32-element blocks, twice in a word.
 template <int G>
 __device__ __forceinline__ void k_scales(const uint4& sz, uint32_t (&s2)[4]) {
-  constexpr uint32_t half = 0x38003800u;
   if constexpr (G == 32) {
-    const uint32_t a = hmul2_u(sz.z, half), b = hmul2_u(sz.w, half);
-    s2[0] = prmt(a, a, 0x1010u);
-    s2[1] = prmt(a, a, 0x3232u);
-    s2[2] = prmt(b, b, 0x1010u);
-    s2[3] = prmt(b, b, 0x3232u);
+    s2[0] = prmt(sz.z, sz.z, 0x1010u);
+    s2[1] = prmt(sz.z, sz.z, 0x3232u);
+    s2[2] = prmt(sz.w, sz.w, 0x1010u);
+    s2[3] = prmt(sz.w, sz.w, 0x3232u);
   } else if constexpr (G == 64) {
-    const uint32_t a = hmul2_u(sz.y, half);
-    s2[0] = s2[1] = prmt(a, a, 0x1010u);
-    s2[2] = s2[3] = prmt(a, a, 0x3232u);
+    s2[0] = s2[1] = prmt(sz.y, sz.y, 0x1010u);
+    s2[2] = s2[3] = prmt(sz.y, sz.y, 0x3232u);
   } else {
-    const uint32_t a = hmul2_u(sz.x, half);
-    s2[0] = s2[1] = s2[2] = s2[3] = prmt(a, a, 0x3232u);
+    s2[0] = s2[1] = s2[2] = s2[3] = prmt(sz.x, sz.x, 0x3232u);
   }
 }
 

@@ -69,6 +69,13 @@ def test_tree_scores_of_any_size(cuda_dev, kvq, si, kb):
     _check_scores(Case(1, 9, 3, 330, 13, 300, kb, 4, 32, [1], konly=[2]), 8000 + 10 * si, cuda_dev, *SIZES[si])
 
 
+@pytest.mark.parametrize("kb,G", [(kb, G) for kb in (2, 4, 8, 16) for G in (32, 64, 128)])
+def test_tree_small_keys(cuda_dev, kvq, kb, G):
+    """Scales below fp16's normal numbers."""
+    for ks in (1e-3, 2e-2):
+        _check_scores(Case(1, 9, 3, 330, 13, 300, kb, 4, G, [1], konly=[2]), 8100, cuda_dev, [10.0 / ks], ks)
+
+
 @pytest.mark.parametrize("vs", [1e-6, 1e-3, 1.0, 2e4])
 @pytest.mark.parametrize("vb", [2, 4, 8, 16])
 def test_tree_values_of_any_size(cuda_dev, kvq, vb, vs):
