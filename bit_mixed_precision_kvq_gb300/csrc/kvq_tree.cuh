@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
           const int cg = col0 + c, tok = cg / a.c.g;
           const int64_t row = (static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g);
-          const float inv = bad ? nan : (L > 0.f ? 1.f / L : 0.f);
+          const float inv = bad || L != L ? nan : (L > 0.f ? 1.f / L : 0.f);
           a.out[row * kD + lp] = f32_to_bf16_bits(__uint_as_float(o[k]) * inv);
         }
       }
@@ -1055,12 +1055,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (tid < ncols) {
       const int c = tid, cg = col0 + c, tok = cg / a.c.g;
       const float L = (sm.lsum[0][c] + sm.lsum[1][c]) + (sm.lsum[2][c] + sm.lsum[3][c]);
-      const float M = bad ? nan : (L > 0.f ? -sm.neg_m[c] : -INFINITY);
+      // a sum that is NaN (a query that is) marks its row, also through the partials
+      const float M = bad || L != L ? nan : (L > 0.f ? -sm.neg_m[c] : -INFINITY);
       if (w.S > 1) {
         *reinterpret_cast<float2*>(slot + N * kD + 2 * c) = make_float2(M, L);
       } else if (a.lse) {
         a.lse[(static_cast<int64_t>(w.b) * a.n_q + tok) * a.c.Hq + hq0 + (cg - tok * a.c.g)] =
-            bad ? nan : 0.69314718055994531f * (M + log2f(L));
+            0.69314718055994531f * (M + log2f(L));
       }
     }
     tc_fence_before();

@@ -372,9 +372,11 @@ kvq_status kvq_sensitivity_probe(const kvq_layout* L, const void* cache, const v
  * and lse -inf.  Drafted rows that no token of their sequence attends may
  * hold anything; all other values are finite, K and V |x| <= 65504, and scores
  * softmax_scale * q.k stay below 2^20 in size (they are fp32).  q may be of any
- * size.  K and V pass through fp16: K is exact from 2^-16 up and off by at most
- * 2^-23 below; V is rounded to 2^-11 of itself and, below 2^-14, to steps of
- * 2^-24 (the stored scales and zeros, fp16 too, have their last bit there).
+ * size; a NaN in it makes its own row and lse NaN (where it attends anything)
+ * and no other.  K and V pass through fp16: K is exact from 2^-16 up and off by
+ * at most 2^-23 below; V is rounded to 2^-11 of itself and, below 2^-14, to
+ * steps of 2^-24 (the stored scales and zeros, fp16 too, have their last bit
+ * there).
  * kvq_decode_tree_workspace_bytes returns 0 for an invalid layout or n_q.
  */
 size_t kvq_decode_tree_workspace_bytes(const kvq_layout* L, int32_t n_q);

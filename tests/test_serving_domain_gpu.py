@@ -94,3 +94,24 @@ def test_tree_values_of_any_size(cuda_dev, kvq, vb, vs):
     tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 330 * 2.0 ** -28 + 2 * se) * vmax + 2.0 ** -24
     oe = np.abs(f64(out) - ref) / tol
     assert oe.max() <= 1, f"out: worst err / tol {oe.max():.3g}"
+
+
+@pytest.mark.parametrize("T", [90, 2300])   # one CTA per unit, and units split over several
+def test_tree_query_that_is_not_finite(cuda_dev, kvq, T):
+    """NaN in a token's query: NaN in that token's rows and lse, nowhere else."""
+    c = Case(1, 8, 2, 2400, 10, 2200, 4, 4, 64, [1])
+    F = Filled(c, 8300, cuda_dev)
+    n_q = 5
+    q, x = bf16((1, n_q, 8, 128), 8301, cuda_dev), bf16((2, 1, n_q, 2, 128), 8302, cuda_dev)
+    kd, vd = x[0].transpose(1, 2), x[1].transpose(1, 2)
+    want = f64(q)
+    q[:, 3, :, 77] = float("nan")
+    masks = random_tree(n_q, 1, 9)
+    out, lse = _tree(F, q, kd, vd, masks, T, cuda_dev)
+    assert torch.isnan(out[:, 3].float()).all() and torch.isnan(lse[:, 3]).all()
+    ok = [0, 1, 2, 4]
+    khat, vhat = F.khat, F.vhat
+    ref, lr = tree_reference(c, want, khat, vhat, f64(kd), f64(vd), masks, [T])
+    vmax = np.abs(vhat).max()
+    assert np.abs(f64(out)[:, ok] - ref[:, ok]).max() <= (2.0 ** -8 + 2.0 ** -10 + 2400 * 2.0 ** -28 + 1e-3) * vmax
+    assert np.abs(f64(lse)[:, ok] - lr[:, ok]).max() <= 1e-3
