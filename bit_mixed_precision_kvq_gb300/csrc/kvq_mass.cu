@@ -13,7 +13,12 @@
 // as exact fp16 subnormals (one AND per operand register) with the group
 // scales applied in fp32 and the zero points as one more K step (z against the
 // high and low fp16 parts of the query's group sums), as in the split kernel;
-// bf16 rows and queries go to the bf16 MMA as they are stored.
+// bf16 rows and queries go to the bf16 MMA as they are stored.  The fp16 queries
+// have a power of two of their own per column, by which the largest element
+// lands in [2^8, 2^9) (128 of them sum to 65280 at most): elements are exact
+// down to 2^-25 of it and off by 2^-33 of it below, and so are the group sums.
+// The scale of a column undoes it (one scale for all columns: 172 us in place
+// of 176 with 32 columns, the same with 4; scale and lse in one 16-byte load: 179).
 //
 // With few columns the pass would be bound by the K bytes, with many by the MMA
 // rate (9 MMAs of 8 cycles per 16 positions and 8 columns), so the operands of
@@ -23,13 +28,13 @@
 // 128 positions take 1.0 us of an SM (the tree kernel's tile, V included, 1.6).
 //
 // Measured (GB300): 32K positions x 8 after a decode step (172 MB) 54 us, 3.2
-// TB/s; 32 tokens over 2,972 positions x 32 x 40 heads (421 MB, 31 GFLOP) 172
-// us; a LLaVA-OneVision layer 4.7 us.  Bound by instruction issue and latency
+// TB/s; 32 tokens over 2,972 positions x 32 x 40 heads (421 MB, 31 GFLOP) 176
+// us; a LLaVA-OneVision layer 4.9 us.  Bound by instruction issue and latency
 // (about 250 instructions a block and tile of columns).  A warp's packed blocks
 // come through shared memory, two under way (three or five take the same): one
 // ahead in registers, behind prefetches into L2, took 70 and 199 us.  fp32
-// arithmetic in pairs is 3% of the first, 0 of the second; 3 CTAs of 80
-// registers an SM instead of 2 take 54 and 165.
+// arithmetic in pairs was 3% of the first, 0 of the second; 3 CTAs of 80
+// registers an SM instead of 2 took 54 and 165 (all with one scale for all columns).
 #include "kvq_split.cuh"
 
 #include "kvq_geom.cuh"
@@ -65,7 +70,8 @@ struct MassSmem {
   uint4 qh[kMaxTiles][4][32];   // fp16 operand: [tile][32-element block][lane], see q_factor
   uint4 qb[kMaxTiles][4][32];   // bf16 operand
   uint32_t zb[kMaxTiles][32];   // group sums, high then low
-  float2 lse2[kMaxTiles][4];    // minus lse in log2 units of columns 2 tig, 2 tig + 1
+  // columns 2 tig, 2 tig + 1: minus lse in log2 units; what takes S to log2 units
+  float2 lse2[kMaxTiles][4], scl[kMaxTiles][4];
   int2 lim[kMaxTiles][4];       // those columns see the positions below
   float qs[kMaxTiles * 8][4];
 };
@@ -77,9 +83,11 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // A code of block P sits at bit kKShift(P) of its half, i.e. is 2^(p - 24) c;
-// the fp16 query elements of the block carry 2^(p0 - p), p0 the smallest p, so
-// that the blocks of a group share one accumulator.  (|q| below 2^-8 may lose
-// bits of fp16's subnormal range: 2^-19 at most, 3e-7 of a score of unit keys.)
+// the fp16 query elements of the block carry 2^(6 + p0 - p), p0 the smallest p,
+// so that the blocks of a group share one accumulator (and 2^6, so that the
+// factor is 1 or more and costs small elements nothing: 2^15 at most).
+constexpr int kQueryExponent = 8;  // a column's largest |q| lands in [2^8, 2^9)
+constexpr int kLiftQ = 6;
 template <int KB>
 __device__ __forceinline__ constexpr int k_first_shift() {
   return KB == 2 ? 2 : 0;
@@ -87,7 +95,7 @@ __device__ __forceinline__ constexpr int k_first_shift() {
 template <int KB>
 __device__ __forceinline__ float q_factor(int P) {
   const int p = KB == 2 ? 8 - 2 * P : (KB == 4 ? 4 * (P & 1) : 0);
-  return __int_as_float((127 + k_first_shift<KB>() - p) << 23);
+  return __int_as_float((127 + kLiftQ + k_first_shift<KB>() - p) << 23);
 }
 
 // D = A * B (a fresh accumulator).
@@ -125,8 +133,22 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
     if (l != INFINITY) r = __ldcg(reinterpret_cast<const uint4*>(a.q + row * kD) + 4 * P + tig);
     const int t = c >> 3, lane = 4 * (c & 7) + tig;
     sm.qb[t][P][lane] = r;
-    const uint32_t y[4] = {bf16pair_f16(r.x, false, r.z, false), bf16pair_f16(r.x, true, r.z, true),
-                           bf16pair_f16(r.y, false, r.w, false), bf16pair_f16(r.y, true, r.w, true)};
+    // the column's power of two 2^e (its 16 threads are neighbours); 2^e and
+    // 2^-e are fp32 for every bf16
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = i == 0 ? r.x : (i == 1 ? r.y : (i == 2 ? r.z : r.w));
+      top = max(top, max(v & 0x7fffu, (v >> 16) & 0x7fffu));
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = min(100, kQueryExponent + 127 - static_cast<int>(top >> 7));
+    const float norm = __int_as_float((127 + e) << 23);
+    auto pair = [&](uint32_t lo, uint32_t hi, bool upper) {
+      return pack_f16x2(norm * (upper ? bf16_hi(lo) : bf16_lo(lo)), norm * (upper ? bf16_hi(hi) : bf16_lo(hi)));
+    };
+    const uint32_t y[4] = {pair(r.x, r.z, false), pair(r.x, r.z, true), pair(r.y, r.w, false), pair(r.y, r.w, true)};
     const float f = q_factor<KB>(P);
     const uint32_t f2 = pack_f16x2(f, f);
     sm.qh[t][P][lane] = make_uint4(hmul2_u(y[0], f2), hmul2_u(y[1], f2), hmul2_u(y[2], f2), hmul2_u(y[3], f2));
@@ -142,10 +164,9 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
     if (tig == 0) {
       sm.qs[c][P] = sum;
       if (P == 0) {
-        float* l2 = reinterpret_cast<float*>(&sm.lse2[t][0]);
-        int* lm = reinterpret_cast<int*>(&sm.lim[t][0]);
-        l2[c & 7] = -l * 1.4426950408889634f;
-        lm[c & 7] = len - n + 1 + k;
+        reinterpret_cast<float*>(&sm.lse2[t][0])[c & 7] = -l * 1.4426950408889634f;
+        reinterpret_cast<float*>(&sm.scl[t][0])[c & 7] = a.scale_log2 * __int_as_float((127 - e) << 23);
+        reinterpret_cast<int*>(&sm.lim[t][0])[c & 7] = len - n + 1 + k;
       }
     }
   }
@@ -160,7 +181,6 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
       if (g < NG) {
 #pragma unroll
         for (int i = 0; i < 4 / NG; ++i) s[e] += sm.qs[c][g * (4 / NG) + i];
-        s[e] *= a.scale_log2 / kZbScale;
       }
     }
     uint32_t z = pack_f16x2(s[0], s[1]);
@@ -453,7 +473,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
             h2_to_f2(r0.sz.x, z, s0[0]);
             h2_to_f2(r1.sz.x, z, s1[0]);
           }
-          const float kf = a.scale_log2 * (pow2i(24 - k_first_shift<KB>()) / kZbScale);
+          const float kf = pow2i(24 - kLiftQ - k_first_shift<KB>());
           uint64_t s0p[NG], s1p[NG];
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
@@ -482,8 +502,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __g
               x0 = fma_pair(s0p[g], pair_of(C[g][0], C[g][1]), x0);
               x1 = fma_pair(s1p[g], pair_of(C[g][2], C[g][3]), x1);
             }
-            const uint64_t l2 = *reinterpret_cast<const uint64_t*>(&sm.lse2[t][tig]), z2 = pair_of(kZbScale, kZbScale);
-            add(t, fma_pair(x0, z2, l2), fma_pair(x1, z2, l2), t0, late);
+            const uint64_t l2 = *reinterpret_cast<const uint64_t*>(&sm.lse2[t][tig]);
+            const uint64_t s2 = *reinterpret_cast<const uint64_t*>(&sm.scl[t][tig]);
+            add(t, fma_pair(x0, s2, l2), fma_pair(x1, s2, l2), t0, late);
           }
           store(t0, m, m_in);
         }

@@ -433,6 +433,8 @@ kvq_status kvq_tree_commit(const kvq_layout* L, void* cache, const void* k_draft
  *   mass_in, mass   device fp32 [B][H_kv][T_cap]; mass_in may be mass itself,
  *             or NULL (zeros); otherwise they must not overlap
  *   decay     finite
+ * K, q (where its lse is finite) and masses are finite, q and K of any size with
+ * scores below 2^20 (they are fp32).
  * Positions t >= len_b are left as they were.  A sequence whose length is
  * outside [1, T], or whose token count is outside [0, min(len_b, n_q or
  * max_path)], is inactive: its rows are left as they were.

@@ -115,3 +115,51 @@ def test_tree_query_that_is_not_finite(cuda_dev, kvq, T):
     vmax = np.abs(vhat).max()
     assert np.abs(f64(out)[:, ok] - ref[:, ok]).max() <= (2.0 ** -8 + 2.0 ** -10 + 2400 * 2.0 ** -28 + 1e-3) * vmax
     assert np.abs(f64(lse)[:, ok] - lr[:, ok]).max() <= 1e-3
+
+
+@pytest.mark.parametrize("kb,G", [(2, 32), (4, 64), (8, 128), (16, 32)])
+@pytest.mark.parametrize("si", range(len(SIZES) + 1))
+def test_mass_scores_of_any_size(cuda_dev, kvq, si, kb, G):
+    """Every weight within the error of its own score: the sum of a score's
+    products in fp32 (2^-19 of their sizes) and the rounding of its exponent."""
+    qs, ks = (SIZES + [([1e4], 1e-3)])[si]
+    c = Case(1, 9, 3, 330, 13, 300, kb, 4, G, [1], konly=[2])
+    n_q, T = 6, 321
+    F, khat, _, q, _, _ = _scaled(c, 8400 + 10 * si, cuda_dev, n_q, qs, ks, 1.0)
+    qf = f64(q)
+    lse = np.zeros(qf.shape[:3], np.float32)
+    for k in range(n_q):
+        for hq in range(9):
+            s = SCALE * (khat[0, hq // 3, :T - n_q + 1 + k] @ qf[0, k, hq])
+            lse[0, k, hq] = s.max() + np.log(np.exp(s - s.max()).sum())
+    mass = torch.full((1, 3, 330), -3.0, device=cuda_dev)
+    kvq.attention_mass(F.L, F.cache, q, torch.from_numpy(lse).to(cuda_dev), T, mass, None, SCALE)
+    torch.cuda.synchronize()
+    want, tol = np.zeros((3, T)), np.zeros((3, T))
+    se = score_error(qf, khat)
+    for k in range(n_q):
+        for hq in range(9):
+            end = T - n_q + 1 + k
+            w = np.exp(SCALE * (khat[0, hq // 3, :end] @ qf[0, k, hq]) - lse[0, k, hq])
+            want[hq // 3, :end] += w
+            tol[hq // 3, :end] += w * (2 * (se[0, k, hq] + 2.0 ** -21 * (1 + abs(lse[0, k, hq]))) + 2.0 ** -20)
+    tol += 2.0 ** -22 * want + 1e-37
+    err = np.abs(f64(mass)[0, :, :T] - want) / tol
+    assert err.max() <= 1, f"mass: worst err / tol {err.max():.3g}"
+    assert (mass[:, :, T:] == -3.0).all()
+
+
+def test_mass_of_queries_past_fp16(cuda_dev, kvq):
+    """Queries above 65504 (and keys so small that the scores are not)."""
+    c = Case(1, 4, 2, 300, 10, 250, 4, 4, 64, [1])
+    F, khat, _, q, _, _ = _scaled(c, 8600, cuda_dev, 1, [1.0], 1e-5, 1.0)
+    q = (q.float() * 1e6).to(torch.bfloat16)
+    qf = f64(q)
+    s = np.stack([SCALE * (khat[0, hq // 2, :280] @ qf[0, 0, hq]) for hq in range(4)])
+    lse = (s.max(1) + np.log(np.exp(s - s.max(1, keepdims=True)).sum(1))).astype(np.float32)
+    mass = torch.zeros(1, 2, 300, device=cuda_dev)
+    kvq.attention_mass(F.L, F.cache, q, torch.from_numpy(lse).to(cuda_dev).view(1, 1, 4), 280, mass, None, SCALE)
+    torch.cuda.synchronize()
+    w = np.exp(s - lse[:, None]).reshape(2, 2, 280).sum(1)
+    rel = 2 * (score_error(qf, khat).max() + 2.0 ** -21 * (1 + np.abs(lse).max())) + 2.0 ** -19
+    assert np.all(np.abs(f64(mass)[0, :, :280] - w) <= rel * w)
