@@ -168,11 +168,12 @@ __device__ __forceinline__ int context_len(const Args& a, int b) {
 }
 
 // A wait that gives up marks the CTA (its outputs become NaN) and the status
-// word; every later wait of the CTA then polls once.
+// word; every later wait of the CTA then polls once.  A limit of one poll asks
+// without suspending: the first wait that is not over already gives up.
 __device__ __forceinline__ void wait_for(const Args& a, Smem& sm, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
+  if (a.polls > 1 ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return;
   if (*static_cast<volatile int*>(&sm.abort)) return;
-  if (mbar_wait(bar, parity, a.polls)) return;
+  if (mbar_wait(bar, parity, a.polls - 1)) return;
   sm.abort = 1;
   atomicOr(a.status, KVQ_STATUS_TILE_WAIT);
 }

@@ -527,6 +527,8 @@ kvq_status kvq_workspace_status(const void* workspace, uint32_t* status, void* s
  * (peer_polls; each poll followed by a ~32 ns sleep) before the wait gives
  * up.  0 restores the default (2^24 and 2^21).  The defaults are far beyond
  * any healthy wait; shorter limits exist for testing the failure path.
+ * tile_polls also limits the waits of kvq_decode_attention_tree inside a CTA,
+ * where a limit of 1 asks once without suspending.
  */
 void kvq_set_wait_limits(uint32_t tile_polls, uint32_t peer_polls);
 

@@ -1,7 +1,7 @@
 """The serving calls beside and after one another: evicted rows seen by a
 decode that copies early, evictions in flight together against their own calls
-alone, accepted root-to-node paths of the tree, and faint weights at the tree
-kernel's own resolution."""
+alone, accepted root-to-node paths of the tree, waits that give up for
+certain, and faint weights at the tree kernel's own resolution."""
 import numpy as np
 import pytest
 import torch
@@ -193,3 +193,41 @@ def test_calls_in_flight_together_equal_their_calls_alone(cuda_dev, kvq):
         for k in range(2):
             for got, want in zip(rounds[r][k][:5], alone[k][:5]):
                 assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("c,T", [
+    (Case(2, 8, 2, 2000, 10, 1900, 4, 2, 64, [0]), 1950),     # split units: marks pass through the partials
+    (Case(2, 8, 2, 200, 10, 150, 4, 2, 64, [0]), 100),        # one CTA per unit
+], ids=str)
+def test_waits_give_up_for_certain(cuda_dev, kvq, c, T):
+    """A limit of one poll asks once, without suspending: the first wait on
+    the queries gives up.  The status is set, every row is either right or NaN
+    as a whole, some are NaN, and the next call is right again."""
+    F = Filled(c, 9400, cuda_dev)
+    n_q = 12
+    q, kd, vd = _tree_inputs(c, n_q, 9401, cuda_dev)
+    m = random_tree(n_q, 1, 5)
+    mask = masks_to(cuda_dev, m)
+    out, lse = torch.zeros_like(q), torch.zeros(2, n_q, 8, device=cuda_dev)
+    ws = torch.zeros(kvq.decode_tree_workspace_bytes(F.L, n_q), dtype=torch.uint8, device=cuda_dev)
+    ref, lr, tol, lt = tight_tree(c, f64(q), F.khat, F.vhat, f64(kd), f64(vd), m, [T, T])
+
+    def rows():
+        o, l = f64(out), f64(lse)
+        nan = np.isnan(l)
+        assert np.array_equal(np.isnan(o), np.repeat(nan[..., None], 128, -1))
+        assert np.all(np.abs(o - ref)[~nan] <= tol[~nan]) and np.all(np.abs(l - lr)[~nan] <= lt[~nan])
+        return int(nan.sum())
+
+    try:
+        kvq.set_wait_limits(1, 0)
+        kvq.decode_attention_tree(F.L, F.cache, q, kd, vd, mask, T, out, SCALE, lse, ws)
+        torch.cuda.synchronize()
+    finally:
+        kvq.set_wait_limits(0, 0)
+    assert kvq.workspace_status(ws) == kvq.STATUS_TILE_WAIT
+    assert rows() > 0
+    ws.zero_()
+    kvq.decode_attention_tree(F.L, F.cache, q, kd, vd, mask, T, out, SCALE, lse, ws)
+    torch.cuda.synchronize()
+    assert kvq.workspace_status(ws) == 0 and rows() == 0
