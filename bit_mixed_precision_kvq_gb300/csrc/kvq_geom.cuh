@@ -11,6 +11,9 @@
 
 // Lets a kernel have `bytes` of dynamic shared memory (kvq_tree.cu).
 kvq_status kvq_allow_smem(const void* fn, int bytes);
+// Checks of the drafted rows of the tree's entry points (kvq_tree.cu).
+kvq_status kvq_check_drafts(const kvq_layout* L, const void* cache, const void* k, const void* v, int64_t sb, int64_t sh,
+                            int64_t st, int32_t n_q);
 
 namespace kvq {
 

@@ -57,9 +57,6 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
 }  // namespace
 }  // namespace kvq
 
-kvq_status kvq_check_drafts(const kvq_layout* L, const void* cache, const void* k, const void* v, int64_t sb, int64_t sh,
-                            int64_t st, int32_t n_q);
-
 extern "C" kvq_status kvq_tree_commit(const kvq_layout* L, void* cache, const void* k_draft_bf16,
                                       const void* v_draft_bf16, int64_t stride_b, int64_t stride_h, int64_t stride_t,
                                       int32_t n_q, const int32_t* path, int32_t max_path, const int32_t* path_len,
