@@ -16,15 +16,17 @@
 //
 // What it measures (GB300, calls back to back): 16 drafts over 16K positions
 // of 8 sequences (32/8 heads, K2/V2 G32, 161 MB, 34 GFLOP) 109 us, 1.48 TB/s
-// and 317 TFLOP/s; a LLaVA-OneVision layer with 16 drafts 19 us; 26 drafts over
+// and 318 TFLOP/s; a LLaVA-OneVision layer with 16 drafts 20 us; 26 drafts over
 // a ragged batch of 16 LLaVA-1.5 chats 90 us.  A tile takes about 1.7 us, of
 // which the MMAs are 0.35 (N = 64: 35 clocks an MMA from TMEM, 51 from shared
 // memory) and the bytes 0.25.  The rest is instructions: some 1100 a tile and
 // scheduler at 0.3 a clock, because a warp's unpacking and softmax are chains
 // of dependent steps through TMEM, shared memory and mbarriers and each of
 // the 17 warps walks its own code (4.3 of 14 warp-clocks an instruction wait
-// on loads and barriers, 2.0 on instruction fetch).  16 columns instead of 64
-// take only 12% less.  Tried and not kept, on the same case: 16 softmax warps
+// on loads and barriers, 2.0 on instruction fetch).  Spills are part of those
+// loads: registers are handed out to warps by fours, so that 17 warps count as
+// 20, which leaves 96 a thread, and every instance spills 60 to 164 bytes (K2/V2 G32 80, K4/V2 G64 92,
+// K8/V4 G32 160).  16 columns instead of 64 take only 12% less.  Tried and not kept, on the same case: 16 softmax warps
 // (113 us), 16 unpack warps (114), a CTA that walks several units (119), V
 // loaded in the same phase (122), the L2 prefetch 8 tiles ahead (118) or none
 // (136).
