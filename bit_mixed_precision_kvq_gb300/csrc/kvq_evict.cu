@@ -465,10 +465,17 @@ extern "C" kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, co
   if (T > kvq::kMaxLen || d.T_cap > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;  // the tail of mass_dst goes to T_cap
   if (n_recent < 0 || n_recent > T_dst - d.vis_end) return KVQ_ERR_INVALID_ARG;
   const int64_t bh = static_cast<int64_t>(s.B) * s.H_kv;
-  if (kvq::ranges_meet(cache, L->total_bytes, cache_dst, L_dst->total_bytes) ||
-      kvq::ranges_meet(mass, 4 * bh * s.T_cap, mass_dst, 4 * bh * d.T_cap) ||
-      kvq::ranges_meet(new_len, 4 * static_cast<int64_t>(s.B), seq_len, 4 * static_cast<int64_t>(s.B)))
-    return KVQ_ERR_INVALID_ARG;
+  // What is written shares no memory with anything else: the selection reads
+  // the masses more than once, and the copy takes its rows' places from keep.
+  const struct {
+    const void* at;
+    int64_t bytes;
+  } used[] = {{cache_dst, L_dst->total_bytes}, {keep, 4 * bh * T_dst}, {mass_dst, 4 * bh * d.T_cap},
+              {new_len, 4 * static_cast<int64_t>(s.B)}, {cache, L->total_bytes}, {mass, 4 * bh * s.T_cap},
+              {seq_len, 4 * static_cast<int64_t>(s.B)}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (kvq::ranges_meet(used[i].at, used[i].bytes, used[j].at, used[j].bytes)) return KVQ_ERR_INVALID_ARG;
   const int64_t blocks = bh * ((T_dst + kvq::kMoveRows - 1) / kvq::kMoveRows);
   if (blocks > 0x7fffffffLL || 2 * bh > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   kvq::EvictArgs a;

@@ -466,9 +466,10 @@ kvq_status kvq_attention_mass(const kvq_layout* L, const void* cache, const void
  *   keep      device int32 [B][H_kv][T_dst]: the source position of each kept
  *             one, -1 behind the last (written)
  *   mass_dst  device fp32 [B][H_kv][T_cap_dst] or NULL: the kept masses, zeros
- *             behind them; must not overlap mass
- *   new_len   device int32 [B] or NULL: the new lengths; must not share memory
- *             with seq_len
+ *             behind them
+ *   new_len   device int32 [B] or NULL: the new lengths
+ * cache_dst, keep, mass_dst and new_len must not share memory with one another
+ * or with cache, mass and seq_len.
  * Rows of cache_dst behind a sequence's new length are left as they were.  A
  * sequence whose length is outside [vis_end, T] is inactive: its keep entries
  * and new_len become -1 and its rows of cache_dst and mass_dst are left as
