@@ -25,11 +25,11 @@
 // the 17 warps walks its own code (4.3 of 14 warp-clocks an instruction wait
 // on loads and barriers, 2.0 on instruction fetch).  Spills are part of those
 // loads: registers are handed out to warps by fours, so that 17 warps count as
-// 20, which leaves 96 a thread, and every instance spills 60 to 164 bytes (K2/V2 G32 80, K4/V2 G64 92,
-// K8/V4 G32 160).  16 columns instead of 64 take only 12% less.  Tried and not kept, on the same case: 16 softmax warps
-// (113 us), 16 unpack warps (114), a CTA that walks several units (119), V
-// loaded in the same phase (122), the L2 prefetch 8 tiles ahead (118) or none
-// (136).
+// 20, which leaves 96 a thread, and every instance spills 60 to 164 bytes (K2/V2
+// G32 80, K4/V2 G64 92, K8/V4 G32 160).  16 columns instead of 64 take only 12%
+// less.  Tried and not kept, on the same case: 16 softmax warps (113 us), 16
+// unpack warps (114), a CTA that walks several units (119), V loaded in the same
+// phase (122), the L2 prefetch 8 tiles ahead (118) or none (136).
 //
 // Exactness of the scores (lse is an fp32 output): a packed K value
 // c s + z is held as c' s + z' with c' = c - 2^(b-1) (c - 1 for 2 bits) and
@@ -42,7 +42,7 @@
 // which is where the stored scales and zeros, fp16 too, have their last bits.
 // Every column of queries has a power of two of its own, by which its largest
 // element lands in [2^8, 2^9) (128 of them sum to 65280 at most): exact down to
-// 2^-25 of that element, off by 2^-33 of it below.  It is undone by the column's
+// 2^-25 of that element, off by 2^-33 of it at most below.  It is undone by the column's
 // softmax scale.  (With one factor 2^-7 for all, queries of 5e-4 against keys of
 // 2e4 gave scores off by 0.15; the scale per column takes 0.5% at 16K x 8.)
 // V is dequantised to fp16 (one rounding, 2^-11 of the value, below the
