@@ -163,3 +163,30 @@ def test_mass_of_queries_past_fp16(cuda_dev, kvq):
     w = np.exp(s - lse[:, None]).reshape(2, 2, 280).sum(1)
     rel = 2 * (score_error(qf, khat).max() + 2.0 ** -21 * (1 + np.abs(lse).max())) + 2.0 ** -19
     assert np.all(np.abs(f64(mass)[0, :, :280] - w) <= rel * w)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 3.0, 1e-30])
+def test_other_softmax_scales(cuda_dev, kvq, scale):
+    """Zero (every position alike), negative, large and tiny scales."""
+    c = Case(1, 6, 2, 330, 13, 300, 4, 4, 32, [1])
+    F = Filled(c, 8700, cuda_dev)
+    n_q, T = 5, 310
+    q, x = bf16((1, n_q, 6, 128), 8701, cuda_dev), bf16((2, 1, n_q, 2, 128), 8702, cuda_dev)
+    kd, vd = x[0].transpose(1, 2), x[1].transpose(1, 2)
+    masks = np.array([[(1 << (i + 1)) - 1 for i in range(n_q)]], np.uint64)
+    out, lse = torch.zeros_like(q), torch.zeros(1, n_q, 6, device=cuda_dev)
+    ws = torch.zeros(kvq.decode_tree_workspace_bytes(F.L, n_q), dtype=torch.uint8, device=cuda_dev)
+    kvq.decode_attention_tree(F.L, F.cache, q, kd, vd, masks_to(cuda_dev, masks), T, out, scale, lse, ws)
+    kvq.quantize_append(F.L, F.cache, kd.contiguous(), vd.contiguous(), T)   # the chain behind its context
+    mass = torch.zeros(1, 2, 330, device=cuda_dev)
+    kvq.attention_mass(F.L, F.cache, q, lse, T + n_q, mass, None, scale)
+    torch.cuda.synchronize()
+    ref, lr = tree_reference(c, f64(q), F.khat, F.vhat, f64(kd), f64(vd), masks, [T], scale)
+    se = score_error(f64(q), F.khat, f64(kd), abs(scale))
+    vmax = max(np.abs(F.vhat).max(), np.abs(f64(vd)).max())
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 330 * 2.0 ** -28 + 2 * se[..., None]) * vmax
+    assert (np.abs(f64(out) - ref) / tol).max() <= 1
+    assert (np.abs(f64(lse) - lr) / (se + 2.0 ** -22 * (1 + np.abs(lr)))).max() <= 1
+    # every token of the chain reaches what its lse is of: weights of 1 a query head
+    total = f64(mass)[0, :, :T + n_q].sum(-1)
+    assert np.abs(total - 3 * n_q).max() <= 3 * n_q * (4 * se.max() + 2.0 ** -18 * (1 + np.abs(lr).max()))
