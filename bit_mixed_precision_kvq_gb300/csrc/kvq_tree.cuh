@@ -42,9 +42,10 @@
 // which is where the stored scales and zeros, fp16 too, have their last bits.
 // Every column of queries has a power of two of its own, by which its largest
 // element lands in [2^8, 2^9) (128 of them sum to 65280 at most): exact down to
-// 2^-25 of that element, off by 2^-33 of it at most below.  It is undone by the column's
-// softmax scale.  (With one factor 2^-7 for all, queries of 5e-4 against keys of
-// 2e4 gave scores off by 0.15; the scale per column takes 0.5% at 16K x 8.)
+// 2^-25 of that element, off by 2^-33 of it at most below.  It is undone by the
+// column's softmax scale.  (With one factor 2^-7 for all, queries of 5e-4 against
+// keys of 2e4 gave scores off by up to 0.2; the scale per column takes 0.5% at
+// 16K x 8.)
 // V is dequantised to fp16 (one rounding, 2^-11 of the value, below the
 // output's 2^-8; steps of 2^-24 below 2^-14), P is fp16 (2^-11), O and the
 // softmax sums are fp32.
