@@ -26,13 +26,15 @@ __all__ = [
     "kvq_set_wait_limits", "set_cache_preload", "kvq_set_cache_preload", "STATUS_TILE_WAIT", "STATUS_PEER_WAIT", "STATUS_COUNTER",
     "decode_tree_workspace_bytes", "kvq_decode_tree_workspace_bytes", "decode_attention_tree",
     "kvq_decode_attention_tree", "tree_commit", "kvq_tree_commit", "attention_mass", "kvq_attention_mass",
-    "cache_evict", "kvq_cache_evict",
+    "cache_evict", "kvq_cache_evict", "RopeDesc", "rope_desc", "norm_rope", "kvq_norm_rope", "tree_verify",
+    "kvq_tree_verify", "decode_attention_window", "kvq_decode_attention_window", "KVQ_MAX_ROPE_AXES",
     "SEG_K_CODES", "SEG_K_SZ", "SEG_V_CODES", "SEG_V_SZ", "SEG_PROT_K", "SEG_PROT_V",
     "SEG_TEXT_K", "SEG_TEXT_V", "EXPORTED_SYMBOLS",
 ]
 
 KVQ_MAX_HEADS = 128
 KVQ_MAX_QUERY_TOKENS = 64
+KVQ_MAX_ROPE_AXES = 4
 KVQ_NSEG = 8
 (SEG_K_CODES, SEG_K_SZ, SEG_V_CODES, SEG_V_SZ, SEG_PROT_K, SEG_PROT_V, SEG_TEXT_K,
  SEG_TEXT_V) = range(8)
@@ -45,6 +47,7 @@ EXPORTED_SYMBOLS = ["kvq_cache_layout", "kvq_quantize_append", "kvq_decode_atten
                     "kvq_decode_attention_static_ws", "kvq_workspace_status", "kvq_set_wait_limits",
                     "kvq_set_cache_preload", "kvq_decode_tree_workspace_bytes", "kvq_decode_attention_tree",
                     "kvq_tree_commit", "kvq_attention_mass", "kvq_cache_evict",
+                    "kvq_norm_rope", "kvq_tree_verify", "kvq_decode_attention_window",
                     "kvq_last_cuda_error", "kvq_status_string"]
 STATUS_TILE_WAIT, STATUS_PEER_WAIT, STATUS_COUNTER = 1, 2, 4  # KVQ_STATUS_* bits
 STATIC_WS_BYTES = 16 * 1024 * 1024  # KVQ_STATIC_WS_BYTES
@@ -88,6 +91,16 @@ class Layout(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64), ("eff_bits_k", ctypes.c_double),
                 ("eff_bits_v", ctypes.c_double), ("n_konly", ctypes.c_int32),
                 ("konly_head", ctypes.c_uint8 * KVQ_MAX_HEADS)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 64)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -146,6 +159,13 @@ def load() -> ctypes.CDLL:
     lib.kvq_attention_mass.restype = ctypes.c_int
     lib.kvq_cache_evict.argtypes = [LP, P, P, P, i32, LP, P, i32, i32, P, P, P, P]
     lib.kvq_cache_evict.restype = ctypes.c_int
+    RP = ctypes.POINTER(Rows)
+    lib.kvq_norm_rope.argtypes = [LP, ctypes.POINTER(RopeDesc), RP, RP, i32, P, i64, i64, P, P, P, f32, RP, RP, P]
+    lib.kvq_norm_rope.restype = ctypes.c_int
+    lib.kvq_tree_verify.argtypes = [i32, i32, i32, P, i32, i64, i64, P, P, i64, P, i64, i64, P, P, P, P, P, P, P, P, P]
+    lib.kvq_tree_verify.restype = ctypes.c_int
+    lib.kvq_decode_attention_window.argtypes = [LP, P, P, i32, P, i32, i32, i32, f32, P, P, P]
+    lib.kvq_decode_attention_window.restype = ctypes.c_int
     lib.kvq_last_cuda_error.argtypes = []
     lib.kvq_last_cuda_error.restype = ctypes.c_int
     lib.kvq_status_string.argtypes = [ctypes.c_int]
@@ -546,6 +566,133 @@ def cache_evict(L: Layout, cache, mass, T: int, L_dst: Layout, cache_dst, T_dst:
         raise KvqError(st, "kvq_cache_evict")
 
 
+def rope_desc(rot_dim: int, axes: Sequence[int], interleaved: bool = False) -> RopeDesc:
+    """The rotation of norm_rope: the first rot_dim elements of a head in pairs
+    (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; axes names the
+    position axis of each pair ([0] * 16 + [1] * 24 + [2] * 24: time, height
+    and width in sections)."""
+    axes = [int(x) for x in axes]
+    if len(axes) * 2 != rot_dim or not 8 <= rot_dim <= 128 or rot_dim % 8:
+        raise ValueError("rot_dim must be a multiple of 8 up to 128, with rot_dim / 2 axes")
+    if min(axes) < 0 or max(axes) >= KVQ_MAX_ROPE_AXES:
+        raise ValueError(f"axes must lie in [0, {KVQ_MAX_ROPE_AXES})")
+    R = RopeDesc(rot_dim, 1 if interleaved else 0, max(axes) + 1)
+    for i, x in enumerate(axes):
+        R.axis[i] = x
+    return R
+
+
+def _rows(what: str, x, shape, dtype, dev: int):
+    """[B, n, H, D] (last dimension contiguous, any other strides) as the C call's rows."""
+    if not (x.dtype is dtype and x.shape == shape and x.get_device() == dev):
+        _refuse(what, x, "bfloat16", shape, dev)
+    s = x.stride()
+    if s[3] != 1:
+        raise ValueError("last dim must be contiguous")
+    # a dimension of one entry has no stride to speak of
+    return Rows(x.data_ptr(), s[0] if shape[0] > 1 else 0, s[2] if shape[2] > 1 else 0, s[1] if shape[1] > 1 else 0)
+
+
+def norm_rope(L: Layout, R: RopeDesc, q, k, pos, inv_freq, q_out, k_out, q_weight=None, k_weight=None,
+              eps: float = 1e-6, stream=None) -> None:
+    """kvq_norm_rope: query heads q [B, n, H_q, D] and key heads k
+    [B, n, H_kv, D] (bf16, any strides of the first three dimensions that are
+    multiples of 8; either may be None with its output), normed where a weight
+    ([D] bf16) is given and rotated by pos (int32 [n_axes, B, n], or
+    [n_axes, n] for the whole batch; more axes than R names are left alone) times inv_freq (float32 [rot_dim / 2]),
+    into q_out and k_out of the same shapes (they may be q and k themselves)."""
+    torch, dev, st = _current(stream)
+    d, bf16 = L.d, torch.bfloat16
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
+        raise ValueError("q and k (one at least) each come with their output")
+    x = q if q is not None else k
+    if x.dim() != 4:
+        raise ValueError("q and k must be [B, n, heads, D]")
+    B, n = d.B, x.shape[1]
+    args = [None if y is None else _rows(what, y, (B, n, H, d.D), bf16, dev)
+            for what, y, H in (("q", q, d.H_q), ("k", k, d.H_kv), ("q_out", q_out, d.H_q), ("k_out", k_out, d.H_kv))]
+    if pos.dtype is not torch.int32 or pos.dim() not in (2, 3) or pos.shape[0] < R.n_axes or pos.shape[1:] not in ((B, n), (n,)):
+        raise ValueError(f"pos: int32 of shape {(R.n_axes, B, n)} or {(R.n_axes, n)} expected, got {pos.dtype} {tuple(pos.shape)}")
+    if pos.get_device() != dev:
+        raise ValueError("pos must be on the current CUDA device")
+    if n == 0:
+        return
+    if n > 1 and pos.stride(-1) != 1:
+        raise ValueError("last dim must be contiguous")
+    fp = _ptr("inv_freq", inv_freq, torch.float32, (R.rot_dim // 2,), dev)
+    wq, wk = _ptr("q_weight", q_weight, bf16, (d.D,), dev), _ptr("k_weight", k_weight, bf16, (d.D,), dev)
+    ref = [None if y is None else ctypes.byref(y) for y in args]
+    st = load().kvq_norm_rope(ctypes.byref(L), ctypes.byref(R), ref[0], ref[1], _i32("n", n), pos.data_ptr(),
+                              pos.stride(0) if pos.shape[0] > 1 else 0, pos.stride(1) if pos.dim() == 3 and B > 1 else 0, fp,
+                              wq, wk, eps, ref[2], ref[3], st)
+    if st != 0:
+        raise KvqError(st, "kvq_norm_rope")
+
+
+def tree_verify(logits, tokens, tree_mask, accept, race, path, path_len, next_token, draft_prob=None, temperature=None,
+                tree_len=None, logprob=None, stream=None) -> None:
+    """kvq_tree_verify: logits [B, n_q, vocab] (bf16 or float32, last dimension
+    contiguous) of the drafted tokens (int32 [B, n_q]; token 0 is the sequence's
+    last) and their tree_mask (as in decode_attention_tree) give the accepted
+    path (int32 [B, n_q], -1 behind its end), path_len and next_token (int32
+    [B]) and logprob (float32 [B, n_q]).  accept float32 [B, n_q] and race
+    float32 [B, vocab] are uniform and exponential random numbers; draft_prob
+    float32 [B, n_q, vocab] the distributions that siblings were drawn from;
+    temperature float32 [B] (0: greedy); tree_len int32 [B] tokens of each tree."""
+    torch, dev, st = _current(stream)
+    f32, i32 = torch.float32, torch.int32
+    if logits.dim() != 3 or (draft_prob is not None and draft_prob.dim() != 3):
+        raise ValueError("logits and draft_prob must be [B, n_q, vocab]")
+    B, n_q, V = logits.shape
+    rows, per_seq = (B, n_q), (B,)
+    if logits.dtype not in (torch.bfloat16, f32):
+        _refuse("logits", logits, "float32", (B, n_q, V), dev)
+    at = []
+    for what, x in (("logits", logits), ("draft_prob", draft_prob)):
+        if x is None:
+            at.append((0, 0, 0))
+            continue
+        if x.shape != (B, n_q, V) or x.get_device() != dev or (x is draft_prob and x.dtype is not f32):
+            _refuse(what, x, "float32" if x is draft_prob else str(x.dtype)[6:], (B, n_q, V), dev)
+        if V > 1 and x.stride(2) != 1:
+            raise ValueError("last dim must be contiguous")
+        at.append((x.data_ptr(), x.stride(0) if B > 1 else 0, x.stride(1) if n_q > 1 else 0))
+    shared = tree_mask.dim() == 1 or tree_mask.shape[0] != B
+    mask = _ptr("tree_mask", tree_mask, torch.int64,
+                ((n_q,) if tree_mask.dim() == 1 else (1, n_q)) if shared else (B, n_q), dev)
+    st = load().kvq_tree_verify(
+        _i32("B", B), _i32("n_q", n_q), _i32("vocab", V), at[0][0], 1 if logits.dtype is f32 else 0, at[0][1], at[0][2],
+        _ptr("tokens", tokens, i32, rows, dev), mask, 0 if shared else n_q, at[1][0], at[1][1], at[1][2],
+        _ptr("accept", accept, f32, rows, dev), _ptr("race", race, f32, (B, V), dev),
+        _ptr("temperature", temperature, f32, per_seq, dev), _ptr("tree_len", tree_len, i32, per_seq, dev),
+        _ptr("path", path, i32, rows, dev), _ptr("path_len", path_len, i32, per_seq, dev),
+        _ptr("next_token", next_token, i32, per_seq, dev), _ptr("logprob", logprob, f32, rows, dev), st)
+    if st != 0:
+        raise KvqError(st, "kvq_tree_verify")
+
+
+def decode_attention_window(L: Layout, cache, q, T: int, n_sink: int, window: int, out,
+                            softmax_scale: Optional[float] = None, lse=None, seq_len=None, stream=None) -> None:
+    """kvq_decode_attention_window: q [B, n_q, H_q, D] bf16 (or [B, H_q, D] for
+    one token); token i stands at position len - n_q + i (len: T, or seq_len
+    int32 [B]) and attends the first n_sink positions and the window positions
+    that end at its own; out like q, lse float32 [B, n_q, H_q] (or [B, H_q])."""
+    torch, dev, st = _current(stream)
+    d = L.d
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, n_q, H_q, D] or [B, H_q, D]")
+    n_q = q.shape[1] if q.dim() == 4 else 1
+    rows = (d.B, n_q, d.H_q) if q.dim() == 4 else (d.B, d.H_q)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d.D)
+    st = load().kvq_decode_attention_window(
+        ctypes.byref(L), _cache_ptr("cache", L, cache, torch.uint8, dev), _ptr("q", q, torch.bfloat16, rows + (d.D,), dev), n_q,
+        _ptr("seq_len", seq_len, torch.int32, (d.B,), dev), _i32("T", T), _i32("n_sink", n_sink), _i32("window", window),
+        softmax_scale, _ptr("out", out, torch.bfloat16, rows + (d.D,), dev), _ptr("lse", lse, torch.float32, rows, dev), st)
+    if st != 0:
+        raise KvqError(st, "kvq_decode_attention_window")
+
+
 def workspace_status(workspace, stream=None) -> int:
     """kvq_workspace_status: the KVQ_STATUS_* bits OR-ed into the
     workspace's status word (synchronises the stream to read them)."""
@@ -593,6 +740,9 @@ kvq_decode_attention_tree = decode_attention_tree
 kvq_tree_commit = tree_commit
 kvq_attention_mass = attention_mass
 kvq_cache_evict = cache_evict
+kvq_norm_rope = norm_rope
+kvq_tree_verify = tree_verify
+kvq_decode_attention_window = decode_attention_window
 kvq_workspace_status = workspace_status
 kvq_set_wait_limits = set_wait_limits
 kvq_set_cache_preload = set_cache_preload

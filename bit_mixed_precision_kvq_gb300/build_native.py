@@ -21,9 +21,12 @@ SOURCES = ["kvq_layout.cpp", "kvq_append.cu", "kvq_decode.cu", "kvq_split_k2.cu"
            "kvq_split_cl_k8.cu", "kvq_split_cl_k16.cu", "kvq_decode_noalloc.cu",
            "kvq_probe.cu", "kvq_mq_umma_k2.cu", "kvq_mq_umma_k4.cu", "kvq_mq_umma_k8.cu",
            "kvq_mq_umma_k16.cu", "kvq_tree.cu", "kvq_tree_k2.cu", "kvq_tree_k4.cu", "kvq_tree_k8.cu",
-           "kvq_tree_k16.cu", "kvq_tree_commit.cu", "kvq_mass.cu", "kvq_evict.cu"]
+           "kvq_tree_k16.cu", "kvq_tree_commit.cu", "kvq_mass.cu", "kvq_evict.cu",
+           "kvq_norm_rope.cu", "kvq_tree_verify.cu", "kvq_window.cu", "kvq_window_k2.cu", "kvq_window_k4.cu",
+           "kvq_window_k8.cu", "kvq_window_k16.cu"]
 HEADERS = ["kvq_internal.h", "kvq_device.cuh", "kvq_ptx.cuh", "kvq_split.cuh", "kvq_split_inst.cuh", "kvq_umma.cuh",
-           "kvq_mq_umma.cuh", "kvq_geom.cuh", "kvq_tree.cuh", "kvq_tree_plan.h"]
+           "kvq_mq_umma.cuh", "kvq_geom.cuh", "kvq_tree.cuh", "kvq_tree_plan.h", "kvq_qk.cuh",
+           "kvq_window.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

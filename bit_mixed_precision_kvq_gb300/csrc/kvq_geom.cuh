@@ -11,6 +11,9 @@
 
 // Lets a kernel have `bytes` of dynamic shared memory (kvq_tree.cu).
 kvq_status kvq_allow_smem(const void* fn, int bytes);
+// Lets a kernel run in clusters of up to 16 CTAs, with `bytes` of dynamic
+// shared memory (kvq_tree_verify.cu).
+kvq_status kvq_allow_clusters(const void* fn, int bytes);
 // Checks of the drafted rows of the tree's entry points (kvq_tree.cu).
 kvq_status kvq_check_drafts(const kvq_layout* L, const void* cache, const void* k, const void* v, int64_t sb, int64_t sh,
                             int64_t st, int32_t n_q);
@@ -86,6 +89,28 @@ inline kvq_status launch_dependent(const void* fn, dim3 grid, unsigned block, si
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  void* args[1] = {arg};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  return e == cudaSuccess ? KVQ_OK : kvq_cuda_fail(e);
+}
+
+// Host: the same with the grid in clusters of `ranks` CTAs.
+inline kvq_status launch_clusters(const void* fn, dim3 grid, unsigned ranks, unsigned block, size_t smem, void* stream,
+                                  void* arg) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   void* args[1] = {arg};
   const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
   return e == cudaSuccess ? KVQ_OK : kvq_cuda_fail(e);

@@ -38,6 +38,7 @@
 #include "kvq_split.cuh"
 
 #include "kvq_geom.cuh"
+#include "kvq_qk.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -75,40 +76,6 @@ struct MassSmem {
   int2 lim[kMaxTiles][4];       // those columns see the positions below
   float qs[kMaxTiles * 8][4];
 };
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// A code of block P sits at bit kKShift(P) of its half, i.e. is 2^(p - 24) c;
-// the fp16 query elements of the block carry 2^(6 + p0 - p), p0 the smallest p,
-// so that the blocks of a group share one accumulator (and 2^6, so that the
-// factor is 1 or more and costs small elements nothing: 2^15 at most).
-constexpr int kQueryExponent = 8;  // a column's largest |q| lands in [2^8, 2^9)
-constexpr int kLiftQ = 6;
-template <int KB>
-__device__ __forceinline__ constexpr int k_first_shift() {
-  return KB == 2 ? 2 : 0;
-}
-template <int KB>
-__device__ __forceinline__ float q_factor(int P) {
-  const int p = KB == 2 ? 8 - 2 * P : (KB == 4 ? 4 * (P & 1) : 0);
-  return __int_as_float((127 + kLiftQ + k_first_shift<KB>() - p) << 23);
-}
-
-// D = A * B (a fresh accumulator).
-__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma_bf16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
 
 // The columns [col0, col0 + 8 tiles) of (b, h): token k of the n taken is
 // column k g + j.  Columns that add nothing get q = 0 and lse = +inf.
@@ -194,76 +161,6 @@ __device__ __forceinline__ void load_columns(const MassArgs& a, MassSmem& sm, in
   __syncthreads();
 }
 
-template <int KB>
-struct RawRow {
-  uint32_t w[KB < 16 ? KB : 16];  // a lane's slice (4 KB bytes), or 4 x 16 bytes of a bf16 row
-  uint4 sz;
-};
-
-template <int KB, int G>
-__device__ __forceinline__ void load_packed(const uint8_t* row, const uint8_t* sz, int tig, RawRow<KB>& r) {
-  if constexpr (KB == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * tig);
-    r.w[0] = x.x;
-    r.w[1] = x.y;
-  } else if constexpr (KB < 16) {
-#pragma unroll
-    for (int i = 0; i < KB / 4; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(row + 4 * KB * tig)[i];
-      r.w[4 * i] = x.x;
-      r.w[4 * i + 1] = x.y;
-      r.w[4 * i + 2] = x.z;
-      r.w[4 * i + 3] = x.w;
-    }
-  }
-  if constexpr (G == 32) {
-    r.sz = *reinterpret_cast<const uint4*>(sz);
-  } else if constexpr (G == 64) {
-    const uint2 x = *reinterpret_cast<const uint2*>(sz);
-    r.sz.x = x.x;
-    r.sz.y = x.y;
-  } else {
-    r.sz.x = *reinterpret_cast<const uint32_t*>(sz);
-  }
-}
-
-// Operand registers f[P][i] (pair P, register i) of a lane's slice: codes at
-// bit kKShift(P) of each half (kvq_split.cuh).
-template <int KB>
-__device__ __forceinline__ void slice_regs(const RawRow<KB>& r, uint32_t (&f)[4][4]) {
-  if constexpr (KB == 2) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t x = r.w[h], y = x >> 6, z = x << 2;
-      f[0][2 * h] = x & 0x03000300u;
-      f[0][2 * h + 1] = y & 0x03000300u;
-      f[1][2 * h] = x & 0x00C000C0u;
-      f[1][2 * h + 1] = y & 0x00C000C0u;
-      f[2][2 * h] = x & 0x00300030u;
-      f[2][2 * h + 1] = y & 0x00300030u;
-      f[3][2 * h] = z & 0x000C000Cu;
-      f[3][2 * h + 1] = x & 0x000C000Cu;
-    }
-  } else if constexpr (KB == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t y = r.w[i] >> 8;
-      f[0][i] = r.w[i] & 0x000F000Fu;
-      f[1][i] = r.w[i] & 0x00F000F0u;
-      f[2][i] = y & 0x000F000Fu;
-      f[3][i] = y & 0x00F000F0u;
-    }
-  } else if constexpr (KB == 8) {
-#pragma unroll
-    for (int P = 0; P < 4; ++P)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t v = r.w[2 * P + (i >> 1)];
-        f[P][i] = ((i & 1) ? (v >> 8) : v) & 0x00FF00FFu;
-      }
-  }
-}
-
 // A warp's blocks of packed rows on their way through shared memory.
 template <int KB, int G>
 struct Ring {
@@ -271,18 +168,6 @@ struct Ring {
   static constexpr int kStage = kCodes + kSz + kRows * 4, kStages = 3;
   static constexpr int kBytes = kStages * kStage;
 };
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <int KB, int G>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) mass_kernel(const __grid_constant__ MassArgs a) {

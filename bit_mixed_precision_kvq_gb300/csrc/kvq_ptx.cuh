@@ -189,6 +189,12 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
 // Every thread of every CTA of the cluster arrives (release) and waits
 // (acquire): shared-memory writes before it are visible to the cluster's
 // distributed-shared-memory reads after it.  All threads of a warp execute it.

@@ -1,0 +1,547 @@
+// kvq_window.cuh -- decode attention over the first positions and a sliding
+// window of the compressed cache.
+//
+// For the token at position p and query head hq of KV head h = hq / g:
+//   s_t = scale q . k_hat_t  for t <= p with t < n_sink or t > p - window,
+//   out = sum softmax(s) v_hat,  lse = ln sum e^s   (no position: out 0, lse -inf).
+//
+// A unit is a (sequence, KV head) and up to 8 NT of its (token, query head)
+// columns.  The rows that its tokens attend, [0, n_sink) and [lo, len), are cut
+// into blocks of 16 or 32 rows of one kind (bf16 text, visual), which the warps
+// of the unit's thread-block cluster take in turn: text blocks first, so that a
+// warp's accumulator changes to packed rows once.  Every warp streams its blocks
+// through a ring of its own in shared memory (cp.async, K and V rows as separate
+// pieces, so that V and the next K are under way while a block's scores are
+// made), and runs an online softmax of its own.  The warps meet in shared
+// memory, the CTAs in distributed shared memory: one launch, no workspace.
+//
+//   QK: S[t][c] = K[t] . q[c]   (mma.sync m16n8k16, positions = M, columns = N)
+//   PV: O[d][c] += V[t][d] P[t][c]   (d = M)
+// Packed rows enter as exact fp16 subnormals with their scales and zero points
+// applied as in the attention mass (K) and the split kernel (V).  bf16 rows stay
+// bf16; the weights meet bf16 V rows as a high and a low bf16 part (2^-17), and
+// packed ones as fp16, also times their scales (2^-11 each).  So that a faint
+// weight (a long window next to a first position that takes most of the mass)
+// keeps its digits in fp16, the score that sets a column's reference weighs
+// 2^(top - kSlack); the reference moves when a weight would pass 2^top, top = kTop, or
+// less where a V scale s is so large that s 2^top would pass fp16.
+//
+// mma.sync and not tcgen05: a decode step has few columns, and a unit's rows are
+// a few thousand at most, spread over the SMs.  What bounds it: bytes for large
+// batches, for small ones the chain of a warp's few blocks and the two meetings.
+#pragma once
+
+#include "kvq_split.cuh"
+
+#include "kvq_geom.cuh"
+#include "kvq_qk.cuh"
+
+namespace kvq {
+namespace win {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kPiece = 4096;  // bytes of a ring slot: 16 bf16 rows
+constexpr int kSlots = 3;
+constexpr int kMaxRanks = 16;
+constexpr int kTop = 14, kSlack = 3;  // weights are at most 2^top, and 2^(top - kSlack) where the reference was set
+constexpr int kPitch = kD + 4;  // of a column's o row in the warps' meeting
+
+struct Args {
+  Geom c;
+  const uint16_t* q;  // [B][n_q][Hq][D]
+  const int32_t* seq_len;
+  int32_t T, n_q, n_sink, window;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  int32_t nblk;  // column blocks of a (sequence, KV head)
+  uint8_t head[KVQ_MAX_HEADS];  // protected heads first: their rows are the longest
+};
+
+template <int NT>
+struct Smem {
+  alignas(128) uint8_t ring[kWarps][kSlots * kPiece];
+  Columns<NT> col;
+  int32_t at[NT * 8];  // position of a column's token (-1: none)
+  float ml[kWarps][NT * 8][2];
+  float4 recv[NT * 256];                        // [rank][its share of the unit's 8 NT x D outputs]
+  float2 recv_ml[kMaxRanks][NT * 8];
+};
+
+// 16-byte chunk c of row r of a piece of bf16 rows sits at chunk c ^ swizzle:
+// the rows of an ldmatrix (V) or of a quarter-warp's loads (K) spread over the banks.
+__device__ __forceinline__ int swz_k(int r) { return (r & 1) << 2; }
+__device__ __forceinline__ int swz_v(int r) { return r & 7; }
+
+// bytes of global memory at src into shared memory, or zeros.
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(void* dst, const void* src, bool live) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(live ? N : 0) : "memory");
+}
+
+// rows [0, n) of `cap` bf16 rows from `src` on into a piece, the others zero.
+template <bool kValue>
+__device__ __forceinline__ void copy_bf16(uint8_t* to, const uint8_t* src, int n, int lane) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 2 * k + (lane >> 4), c = lane & 15;
+    const bool live = r < n;
+    cp_async_or_zero<16>(to + r * kRowBytes + ((c ^ (kValue ? swz_v(r) : swz_k(r))) << 4),
+                         src + (live ? r : 0) * kRowBytes + 16 * c, live);
+  }
+}
+
+// rows [0, n) of RB packed rows of BITS bits and their scale/zero rows.
+template <int BITS, int G, int RB>
+__device__ __forceinline__ void copy_packed(uint8_t* to, const uint8_t* codes, const uint8_t* sz, int n, int lane) {
+  constexpr int kSz = 4 * kD / G;
+#pragma unroll
+  for (int x0 = 0; x0 < RB * BITS; x0 += 32) {
+    const int x = x0 + lane;
+    const bool live = x < n * BITS;
+    cp_async_or_zero<16>(to + 16 * x, codes + 16 * (live ? x : 0), live);
+  }
+  if (lane < RB) {
+    const bool live = lane < n;
+    cp_async_or_zero<kSz>(to + RB * BITS * 16 + kSz * lane, sz + kSz * (live ? lane : 0), live);
+  }
+}
+
+// PV of 16 bf16 rows of a piece: the weights of a column as high and low bf16.
+__device__ __forceinline__ void pv_bf16(const uint8_t* vc, const float (&P)[4], int lane, Acc& acc) {
+  const uint32_t h0 = pack_bf16x2(P[0], P[1]), h1 = pack_bf16x2(P[2], P[3]);
+  const uint32_t l0 = pack_bf16x2(P[0] - bf16_lo(h0), P[1] - bf16_hi(h0)), l1 = pack_bf16x2(P[2] - bf16_lo(h1), P[3] - bf16_hi(h1));
+  const uint32_t b0 = movmatrix_trans(h0), b1 = movmatrix_trans(h1), c0 = movmatrix_trans(l0), c1 = movmatrix_trans(l1);
+  const int row = (lane & 7) + ((lane >> 4) & 1) * 8, chunk = (lane >> 3) & 1;
+  const uint8_t* base = vc + row * kRowBytes;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    uint32_t A[4];
+    ldsm_x4_trans(base + (((2 * m + chunk) ^ swz_v(row)) << 4), A);
+    mma_bf16(acc.o[m], A, b0, b1);
+    mma_bf16(acc.o[m], A, c0, c1);
+  }
+}
+
+// A block of rows of one kind.
+struct Block {
+  int t, n;       // position of its first row, rows
+  int64_t row;    // first row among the rows of its kind
+  bool visual;
+};
+
+template <int KB, int VB, int G, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>(smem_raw);
+  const Geom& p = a.c;
+  constexpr int kKRow = KB < 16 ? 16 * KB : kRowBytes, kVRow = VB < 16 ? 16 * VB : kRowBytes;
+  constexpr int kKSz = KB < 16 ? 4 * kD / G : 0, kVSz = VB < 16 ? 4 * kD / G : 0;
+  // rows of a block whose K and V are both packed
+  constexpr int kRB = 32 * (kKRow + kKSz) <= kPiece && 32 * (kVRow + kVSz) <= kPiece ? 32 : 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = static_cast<int>(cluster_nctarank());
+  const int unit = blockIdx.x / ranks, cb = unit % a.nblk, hb = unit / a.nblk;
+  const int h = a.head[hb / p.B], b = hb % p.B;
+  cluster_arrive();  // waited for before the first store to another CTA
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();  // this kernel writes no cache row
+  int len = a.seq_len ? a.seq_len[b] : a.T;
+  if (len < 0 || len > a.T) len = 0;
+  const int p0 = len - a.n_q;  // position of token 0
+  const HeadRows hr = head_rows(p, b, h);
+  const bool kpk = KB < 16 && hr.k_packed, vpk = VB < 16 && hr.v_packed;
+  const int vrb = kpk && vpk ? kRB : 16;  // rows of a visual block
+
+  // Runs of rows of one kind, one a lane: text before the visual block (of the
+  // first positions, of the window), text behind it, visual rows.
+  int run_t, run_n, run_end, run_first;
+  {
+    int a1 = min(a.n_sink, len), b0 = max(a1, p0 - a.window + 1);
+    if (b0 <= a1) a1 = b0 = 0;
+    const int x0 = lane & 1 ? b0 : 0, x1 = lane & 1 ? len : a1, kind = lane >> 1;
+    const int k0 = kind == 0 ? 0 : (kind == 1 ? p.ve : p.vs), k1 = kind == 0 ? p.vs : (kind == 1 ? len : p.ve);
+    run_t = max(x0, k0);
+    run_n = kind < 3 ? max(0, min(x1, k1) - run_t) : 0;
+    const int rb = kind == 2 ? vrb : 16;
+    const int nb = (run_n + rb - 1) / rb;
+    run_end = nb;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run_end, o);
+      if (lane >= o) run_end += y;
+    }
+    run_first = run_end - nb;
+  }
+  const int blocks = __shfl_sync(0xffffffffu, run_end, 5);
+  auto block_of = [&](int i) {
+    const int r = __popc(__ballot_sync(0xffffffffu, lane < 6 && i >= run_end));
+    const int t = __shfl_sync(0xffffffffu, run_t, r), n = __shfl_sync(0xffffffffu, run_n, r);
+    const int off = (i - __shfl_sync(0xffffffffu, run_first, r)) * (r >= 4 ? vrb : 16);
+    Block k;
+    k.visual = r >= 4;
+    k.t = t + off;
+    k.n = min(n - off, k.visual ? vrb : 16);
+    k.row = r < 2 ? k.t : (r < 4 ? k.t - p.Tv : k.t - p.vs);
+    return k;
+  };
+  uint8_t* const ring = sm.ring[warp];
+  auto issue_k = [&](const Block& k, uint8_t* to) {
+    if (KB < 16 && k.visual && kpk) {
+      const uint8_t* src = hr.vis_k + k.row * kKRow;
+      const uint8_t* sz = hr.vis_ksz + k.row * kKSz;
+      if constexpr (KB < 16) {
+        if (kRB == 16 || vrb == 16) copy_packed<KB, G, 16>(to, src, sz, k.n, lane);
+        else copy_packed<KB, G, kRB>(to, src, sz, k.n, lane);
+      }
+    } else {
+      copy_bf16<false>(to, (k.visual ? hr.vis_k : hr.text_k) + k.row * kRowBytes, k.n, lane);
+    }
+  };
+  auto issue_v = [&](const Block& k, uint8_t* to) {
+    if (VB < 16 && k.visual && vpk) {
+      const uint8_t* src = hr.vis_v + k.row * kVRow;
+      const uint8_t* sz = hr.vis_vsz + k.row * kVSz;
+      if constexpr (VB < 16) {
+        if (kRB == 16 || vrb == 16) copy_packed<VB, G, 16>(to, src, sz, k.n, lane);
+        else copy_packed<VB, G, kRB>(to, src, sz, k.n, lane);
+      }
+    } else {
+      copy_bf16<true>(to, (k.visual ? hr.vis_v : hr.text_v) + k.row * kRowBytes, k.n, lane);
+    }
+  };
+
+  const int step = ranks * kWarps;
+  int i = rank * kWarps + warp;
+  Block now = {}, then = {};
+  if (i < blocks) {
+    now = block_of(i);
+    issue_k(now, ring);
+    cp_async_commit();
+    issue_v(now, ring + kPiece);
+  }
+  cp_async_commit();
+
+  // the queries, while the first rows are under way
+  load_columns<KB, G, NT, kThreads>(sm.col, p.Hq, p.g, a.q, a.n_q, b, h, cb * NT * 8, a.scale_log2);
+  if (threadIdx.x < NT * 8) {
+    const int tok = (cb * NT * 8 + threadIdx.x) / p.g;
+    sm.at[threadIdx.x] = tok < a.n_q ? p0 + tok : -1;
+  }
+  __syncthreads();
+
+  Acc acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    acc[t].m[0] = acc[t].m[1] = -INFINITY;
+    acc[t].l[0] = acc[t].l[1] = 0.f;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) acc[t].o[m][0] = acc[t].o[m][1] = acc[t].o[m][2] = acc[t].o[m][3] = 0.f;
+    acc[t].zo[0] = acc[t].zo[1] = acc[t].zo[2] = acc[t].zo[3] = 0.f;
+  }
+  bool packed_acc = false;
+  float top = kTop;
+  int slot = 0;  // of the block's K piece
+#pragma unroll 1
+  for (; i < blocks; i += step) {
+    const bool more = i + step < blocks;
+    const int slot_v = slot == kSlots - 1 ? 0 : slot + 1, slot_n = slot_v == kSlots - 1 ? 0 : slot_v + 1;
+    cp_async_wait<1>();
+    __syncwarp();
+    if (more) {
+      then = block_of(i + step);
+      issue_k(then, ring + slot_n * kPiece);
+    }
+    cp_async_commit();
+    const uint8_t* kc = ring + slot * kPiece;
+    const bool k_is_packed = KB < 16 && now.visual && kpk, v_is_packed = VB < 16 && now.visual && vpk;
+    const int rb = now.visual ? vrb : 16;
+    float S[NT][kRB / 16][4];
+#pragma unroll
+    for (int hf = 0; hf < kRB / 16; ++hf) {
+      if (16 * hf < rb) {
+        if constexpr (KB < 16) {
+          if (k_is_packed) qk_packed_rows<KB, G, NT>(kc, kc + rb * kKRow, 16 * hf, sm.col, lane, [&](int t, const float (&x)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][hf][e] = x[e];
+          });
+        }
+        if (!k_is_packed) {
+          const uint8_t* r0 = kc + gid * kRowBytes;
+          qk_bf16_rows<NT>([&](int P, uint4& f0, uint4& f1) {
+            const int c = (4 * P + tig) ^ swz_k(gid);
+            f0 = *reinterpret_cast<const uint4*>(r0 + (c << 4));
+            f1 = *reinterpret_cast<const uint4*>(r0 + 8 * kRowBytes + (c << 4));
+          }, sm.col, a.scale_log2, lane, [&](int t, const float (&x)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][hf][e] = x[e];
+          });
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) S[t][hf][0] = S[t][hf][1] = S[t][hf][2] = S[t][hf][3] = -INFINITY;
+      }
+    }
+    // What the columns' tokens do not see: rows past the block's last, later
+    // positions, positions between the first ones and a token's window.
+    const int last = now.t + now.n - 1;
+    if (now.n < rb || last > p0 || (last >= a.n_sink && now.t <= len - 1 - a.window) ) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int2 at = *reinterpret_cast<const int2*>(&sm.at[8 * t + 2 * tig]);
+#pragma unroll
+        for (int hf = 0; hf < kRB / 16; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = now.t + 16 * hf + gid + (e >> 1) * 8, pos = e & 1 ? at.y : at.x;
+            if (x > last || x > pos || (x >= a.n_sink && x <= pos - a.window)) S[t][hf][e] = -INFINITY;
+          }
+      }
+    }
+    // the softmax of the warp's columns; the reference moves in few blocks
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      Acc& A = acc[t];
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int hf = 0; hf < kRB / 16; ++hf) {
+        mx0 = fmaxf(mx0, fmaxf(S[t][hf][0], S[t][hf][2]));
+        mx1 = fmaxf(mx1, fmaxf(S[t][hf][1], S[t][hf][3]));
+      }
+      if (__any_sync(0xffffffffu, mx0 > A.m[0] + top || mx1 > A.m[1] + top)) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        mx0 = mx0 > A.m[0] + top ? mx0 - (top - kSlack) : A.m[0];
+        mx1 = mx1 > A.m[1] + top ? mx1 - (top - kSlack) : A.m[1];
+        const float c0 = ex2(A.m[0] - (mx0 == -INFINITY ? 0.f : mx0)), c1 = ex2(A.m[1] - (mx1 == -INFINITY ? 0.f : mx1));
+        A.m[0] = mx0;
+        A.m[1] = mx1;
+        A.l[0] *= c0;
+        A.l[1] *= c1;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          A.o[m][0] *= c0;
+          A.o[m][1] *= c1;
+          A.o[m][2] *= c0;
+          A.o[m][3] *= c1;
+        }
+        A.zo[0] *= c0;
+        A.zo[1] *= c1;
+        A.zo[2] *= c0;
+        A.zo[3] *= c1;
+      }
+      const float r0 = A.m[0] == -INFINITY ? 0.f : A.m[0], r1 = A.m[1] == -INFINITY ? 0.f : A.m[1];
+#pragma unroll
+      for (int hf = 0; hf < kRB / 16; ++hf) {
+        S[t][hf][0] = ex2(S[t][hf][0] - r0);
+        S[t][hf][1] = ex2(S[t][hf][1] - r1);
+        S[t][hf][2] = ex2(S[t][hf][2] - r0);
+        S[t][hf][3] = ex2(S[t][hf][3] - r1);
+        A.l[0] += S[t][hf][0] + S[t][hf][2];
+        A.l[1] += S[t][hf][1] + S[t][hf][3];
+      }
+    }
+    cp_async_wait<1>();
+    __syncwarp();  // V is here; the K piece's slot is free
+    if (more) issue_v(then, ring + slot * kPiece);
+    cp_async_commit();
+    const uint8_t* vc = ring + slot_v * kPiece;
+    if constexpr (VB < 16) {
+      if (v_is_packed != packed_acc) {  // text blocks come first: once a warp
+        packed_acc = v_is_packed;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (packed_acc) acc_to_packed<VB>(acc[t]);
+          else acc_to_true<VB, G>(acc[t], tig);
+        }
+      }
+      if (v_is_packed) {
+        // a row's largest scale (a lane a row): times a weight it must stay below 2^16
+        float big = 0.f;
+        if (lane < rb) {
+          const __half* z = reinterpret_cast<const __half*>(vc + rb * kVRow + kVSz * lane);
+#pragma unroll
+          for (int g = 0; g < kD / G; ++g) big = fmaxf(big, __half2float(z[kD / G + g]));
+        }
+        if (__any_sync(0xffffffffu, big >= ex2(15.9f - top))) {  // rare
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          const float to = floorf(15.9f - log2f(big)), f = ex2(to - top);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              acc[t].m[e] += top - to;
+              acc[t].l[e] *= f;
+            }
+#pragma unroll
+            for (int m = 0; m < 8; ++m) acc[t].o[m][0] *= f, acc[t].o[m][1] *= f, acc[t].o[m][2] *= f, acc[t].o[m][3] *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t].zo[e] *= f;
+#pragma unroll
+            for (int hf = 0; hf < kRB / 16; ++hf)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) S[t][hf][e] *= f;
+          }
+          top = to;
+        }
+#pragma unroll
+        for (int hf = 0; hf < kRB / 16; ++hf)
+          if (16 * hf < rb) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              pv_packed<VB, G>(vc, vc + rb * kVRow, 16 * hf, kNoLimit, movmatrix_trans(pack_f16x2(S[t][hf][0], S[t][hf][1])),
+                               movmatrix_trans(pack_f16x2(S[t][hf][2], S[t][hf][3])), gid, tig, acc[t]);
+          }
+      }
+    }
+    if (!v_is_packed) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) pv_bf16(vc, S[t][0], lane, acc[t]);
+    }
+    now = then;
+    slot = slot_n;
+  }
+  cp_async_wait<0>();
+
+  // The warps meet: m and l of every column, then the o rows over the CTA's m.
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if constexpr (VB < 16)
+      if (packed_acc) acc_to_true<VB, G>(acc[t], tig);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = acc[t].l[e];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (gid == 0) {
+        sm.ml[warp][8 * t + 2 * tig + e][0] = acc[t].m[e];
+        sm.ml[warp][8 * t + 2 * tig + e][1] = l;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int t = 0; t < NT; ++t) {  // (a warp's ring holds one tile's rows)
+    float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      if (u != t) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = 8 * u + 2 * tig + e;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][c][0]);
+        const float f = ex2(acc[u].m[e] - (M == -INFINITY ? 0.f : M));
+        float* o = mine + (2 * tig + e) * kPitch + gid;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          o[16 * m] = acc[u].o[m][e] * f;
+          o[16 * m + 8] = acc[u].o[m][2 + e] * f;
+        }
+      }
+    }
+    __syncthreads();
+    // thread (column, quad of d): the CTA's sum, sent to the rank that writes it
+    const int c = threadIdx.x >> 5, d4 = threadIdx.x & 31;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + c * kPitch + 4 * d4);
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    }
+    if (t == 0) cluster_wait();  // every CTA of the cluster has started
+    // outputs of a tile are shared out over the ranks: 256 / ranks quads each
+    const int share = 256 / ranks, to = threadIdx.x / share, at = threadIdx.x - to * share;
+    const uint32_t addr = dsmem_addr(&sm.recv[t * 256 + rank * share + at], to);
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(s.x), "f"(s.y), "f"(s.z), "f"(s.w) : "memory");
+    __syncthreads();  // the rings are written anew
+  }
+  if (threadIdx.x < NT * 8 * ranks) {
+    const int to = threadIdx.x / (NT * 8), c = threadIdx.x - to * (NT * 8);
+    float M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][c][0]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l += sm.ml[w][c][1] * ex2(sm.ml[w][c][0] - (M == -INFINITY ? 0.f : M));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dsmem_addr(&sm.recv_ml[rank][c], to)), "f"(M), "f"(l) : "memory");
+  }
+  cluster_sync();
+  // lane r of a group of `ranks` has rank r's part of a quad
+  const int share = 256 / ranks, src = threadIdx.x % ranks, at = threadIdx.x / ranks;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int quad = rank * share + at, c = quad >> 5, d4 = quad & 31;
+    const float2 ml = sm.recv_ml[src][8 * t + c];
+    float4 o = sm.recv[t * 256 + src * share + at];
+    float M = ml.x;
+    for (int x = 1; x < ranks; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+    float l = ml.y * f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+    for (int x = 1; x < ranks; x <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, x);
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+    }
+    const int cg = (cb * NT + t) * 8 + c, tok = cg / p.g;
+    if (src == 0 && tok < a.n_q) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing attended: 0 (NaN stays)
+      const int64_t row = (static_cast<int64_t>(b) * a.n_q + tok) * p.Hq + h * p.g + (cg - tok * p.g);
+      uint2 w;
+      w.x = pack_bf16x2(o.x * inv, o.y * inv);
+      w.y = pack_bf16x2(o.z * inv, o.w * inv);
+      reinterpret_cast<uint2*>(a.out + row * kD)[d4] = w;
+      if (d4 == 0 && a.lse) a.lse[row] = 0.69314718055994531f * (M + log2f(l));
+    }
+  }
+}
+
+struct Kernel {
+  const void* fn;
+  int smem, nt;
+};
+template <int KB, int VB, int G>
+Kernel kernel_of(int nt) {
+  return nt == 1 ? Kernel{reinterpret_cast<const void*>(&window_kernel<KB, VB, G, 1>), static_cast<int>(sizeof(Smem<1>)), 1}
+                 : Kernel{reinterpret_cast<const void*>(&window_kernel<KB, VB, G, 2>), static_cast<int>(sizeof(Smem<2>)), 2};
+}
+template <int KB, int VB>
+Kernel kernel_of(int G, int nt) {
+  if constexpr (KB == 16 && VB == 16) return kernel_of<16, 16, 128>(nt);
+  switch (G) {
+    case 32: return kernel_of<KB, VB, 32>(nt);
+    case 64: return kernel_of<KB, VB, 64>(nt);
+    case 128: return kernel_of<KB, VB, 128>(nt);
+  }
+  return {nullptr, 0, 0};
+}
+template <int KB>
+Kernel kernel_of(int vb, int G, int nt) {
+  switch (vb) {
+    case 2: return kernel_of<KB, 2>(G, nt);
+    case 4: return kernel_of<KB, 4>(G, nt);
+    case 8: return kernel_of<KB, 8>(G, nt);
+    case 16: return kernel_of<KB, 16>(G, nt);
+  }
+  return {nullptr, 0, 0};
+}
+// The kernel for (k_bits, v_bits, G) and nt tiles of 8 columns: one translation
+// unit for each width of K.
+Kernel window_kernel_k2(int vb, int G, int nt);
+Kernel window_kernel_k4(int vb, int G, int nt);
+Kernel window_kernel_k8(int vb, int G, int nt);
+Kernel window_kernel_k16(int vb, int G, int nt);
+
+}  // namespace win
+}  // namespace kvq

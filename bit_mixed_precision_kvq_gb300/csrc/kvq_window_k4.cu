@@ -1,0 +1,8 @@
+// kvq_window_k4.cu -- the windowed decode kernels with 4-bit K.
+#include "kvq_window.cuh"
+
+namespace kvq {
+namespace win {
+Kernel window_kernel_k4(int vb, int G, int nt) { return kernel_of<4>(vb, G, nt); }
+}  // namespace win
+}  // namespace kvq

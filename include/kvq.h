@@ -69,6 +69,7 @@ extern "C" {
 #define KVQ_MAX_CTAS 1024   /* upper bound on split-KV work chunks per call */
 #define KVQ_HEADS_PER_UNIT 8 /* query columns (query heads, or head x token pairs) handled together per KV head */
 #define KVQ_MAX_QUERY_TOKENS 64 /* query tokens per sequence of kvq_decode_attention_mq */
+#define KVQ_MAX_ROPE_AXES 4 /* position axes of kvq_norm_rope */
 
 /* Bits of the status word that the decode kernels OR into the first 4 bytes
  * of their workspace (never cleared by the library; zero it to start).  A
@@ -479,6 +480,133 @@ kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* 
                            const int32_t* seq_len, int32_t T, const kvq_layout* L_dst,
                            void* cache_dst, int32_t T_dst, int32_t n_recent, int32_t* keep,
                            float* mass_dst, int32_t* new_len, void* stream);
+
+/*
+ * kvq_norm_rope -- the query and key heads of n_tok tokens per sequence, from
+ * the projection's output to the rows that the cache's calls take (K is cached
+ * after its rotation; "VLM_KV_Quantization", section 2): per head row x
+ *   y = x / sqrt(mean_d x_d^2 + eps) * weight     (y = x without a weight)
+ * and pair i of its first rot_dim elements is turned by
+ *   a_i = pos[axis[i]] * inv_freq[i]:  (y_p cos a - y_q sin a, y_q cos a + y_p sin a),
+ * with (p, q) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.  The
+ * other elements keep y.  Positions have up to KVQ_MAX_ROPE_AXES axes (time,
+ * height and width of video patches; one axis for text).
+ *   L         gives B, H_q, H_kv and D
+ *   R         the rotation (host pointer, copied by value)
+ *   q, k      rows of the query and key heads: bf16, element (b, h, i, d) at
+ *             data[b*stride_b + h*stride_h + i*stride_t + d] (strides in elements,
+ *             >= 0, multiples of 8; 16-byte aligned).  Either may be NULL with
+ *             its output: only the other is made then
+ *   n_tok     tokens per sequence, >= 0 (0 is a no-op)
+ *   pos       device int32, entry (axis, b, i) at index axis*pos_stride_axis +
+ *             b*pos_stride_b + i, any value
+ *   inv_freq  device fp32 [rot_dim / 2], finite
+ *   q_weight, k_weight   device bf16 [D], 16-byte aligned, or NULL: those heads
+ *             are not normed
+ *   eps       finite, >= 0
+ *   q_out, k_out   as q and k, every row in memory of its own; each may be its
+ *             input (same data and strides), else the two must lie apart.
+ *             q_out must share no row with k, nor k_out with q or q_out
+ * Arithmetic is fp32 (angles are taken modulo a turn exactly, whatever the
+ * position), rounded to bf16 once.  A NaN or infinity in a row stays in it.
+ */
+typedef struct kvq_rope_desc {
+  int32_t rot_dim;     /* elements turned: a multiple of 8, 8..D */
+  int32_t interleaved; /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+  int32_t n_axes;      /* 1..KVQ_MAX_ROPE_AXES */
+  uint8_t axis[64];    /* position axis of pair i < rot_dim / 2, below n_axes */
+} kvq_rope_desc;
+
+typedef struct kvq_rows { /* rows of heads on the device, bf16 [D] each */
+  void* data;
+  int64_t stride_b, stride_h, stride_t;
+} kvq_rows;
+
+kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R, const kvq_rows* q, const kvq_rows* k,
+                         int32_t n_tok, const int32_t* pos, int64_t pos_stride_axis, int64_t pos_stride_b,
+                         const float* inv_freq, const void* q_weight, const void* k_weight, float eps,
+                         const kvq_rows* q_out, const kvq_rows* k_out, void* stream);
+
+/*
+ * kvq_tree_verify -- which drafted tokens of each tree the target accepts,
+ * between kvq_decode_attention_tree (whose hidden rows gave the logits) and
+ * kvq_tree_commit (which takes path and path_len as they are written here).
+ * Token 0 of a tree is the last token of the sequence itself: it is always on
+ * the path.  The parent of token j is the highest token below j in its mask;
+ * a token that names none is never reached.  From token 0 on, the children of
+ * the path's last token x are tried in index order.  With p the softmax of
+ * x's logits / temperature, child j (token id c, random number u) is accepted if
+ *   without draft_prob (the children were not sampled):
+ *     u * (1 - sum of p over the refused siblings) < p(c); a token id that a
+ *     refused sibling had is refused;
+ *   with draft_prob (the children were drawn one by one, with replacement, from
+ *     q = draft_prob of x):  u * q(c) < r(c), with r = p at first and
+ *     r = max(r - q, 0) / sum max(r - q, 0) after each refusal (where nothing
+ *     is left, r stays);
+ *   temperature <= 0 or NaN (greedy): c is the token id of x's largest logit.
+ * The first accepted child is the path's next token.  When none is left,
+ * next_token is the v of largest r(v) / race(v) (without draft_prob r is p with
+ * the refused token ids out); greedy, or where no such value is above 0, the
+ * token id of the largest logit.  With u uniform in [0, 1) and race exponential
+ * the tokens are distributed as the target's samples.  Ties go to the lowest v.
+ *   B         sequences, >= 1 (KVQ_ERR_UNSUPPORTED above 65535)
+ *   n_q       tokens of a tree, 1 <= n_q <= KVQ_MAX_QUERY_TOKENS
+ *   vocab     1 <= vocab <= 2^30
+ *   logits    device bf16 (logits_fp32 = 0) or fp32 (1), entry (b, i, v) at index
+ *             b*logits_stride_b + i*logits_stride_t + v (strides >= 0; aligned to
+ *             its type)
+ *   tokens    device int32 [B][n_q]; an id outside [0, vocab) is refused
+ *   tree_mask, mask_stride_b   as in kvq_decode_attention_tree
+ *   draft_prob  device fp32, entry (b, i, v) at index b*draft_stride_b +
+ *             i*draft_stride_t + v, or NULL; a token id whose entry is NaN
+ *             is refused and not picked after a refusal
+ *   accept    device fp32 [B][n_q]: u of each token (entry 0 is unread)
+ *   race      device fp32 [B][vocab]: a v whose entry is not above 0 is not picked
+ *   temperature  device fp32 [B] or NULL (1 for all); finite, and so is
+ *             logit / temperature for the finite logits
+ *   tree_len  device int32 [B]: tokens of each tree (only these are read), or
+ *             NULL (n_q); an entry outside [1, n_q] marks an inactive sequence
+ *   path      device int32 [B][n_q]: the tokens on the path, -1 behind the last
+ *   path_len  device int32 [B], >= 1
+ *   next_token  device int32 [B]
+ *   logprob   device fp32 [B][n_q] or NULL: entry k is ln p of the token id that
+ *             follows path[k] (next_token behind the last), 0 behind it; the
+ *             softmax of greedy sequences has temperature 1
+ * Logits of -inf are tokens that cannot be.  A sequence whose walk meets a row
+ * of logits with NaN, +inf or nothing above -inf is inactive.  Inactive
+ * sequences get path and next_token -1, logprob 0 and path_len -1 (which
+ * kvq_tree_commit and kvq_attention_mass take as inactive).
+ * The outputs must not share memory with one another or with an input.
+ */
+kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, const void* logits, int32_t logits_fp32,
+                           int64_t logits_stride_b, int64_t logits_stride_t, const int32_t* tokens,
+                           const uint64_t* tree_mask, int64_t mask_stride_b, const float* draft_prob,
+                           int64_t draft_stride_b, int64_t draft_stride_t, const float* accept, const float* race,
+                           const float* temperature, const int32_t* tree_len, int32_t* path, int32_t* path_len,
+                           int32_t* next_token, float* logprob, void* stream);
+
+/*
+ * kvq_decode_attention_window -- decode attention over the first n_sink
+ * positions and a sliding window: query token i of n_q stands at position
+ * p = len_b - n_q + i (its own row is in the cache) and attends the positions
+ * t <= p with t < n_sink or t > p - window.  Cost follows n_sink + window, not
+ * the length.
+ *   q_bf16    device bf16 [B][n_q][H_q][D], 16-byte aligned; n_q as above
+ *   seq_len   device int32 [B] of lengths, or NULL: every len_b is T.  An entry
+ *             outside [0, T] marks an inactive sequence (outputs zero, lse -inf)
+ *   T         1 <= T <= T_cap: the (largest) length (KVQ_ERR_UNSUPPORTED above
+ *             2^31 - 2^16)
+ *   n_sink    >= 0;  window  >= 1 (a window of T or more hides nothing)
+ *   out_bf16  device bf16 [B][n_q][H_q][D];  lse  fp32 [B][n_q][H_q] or NULL
+ * A token that attends nothing (p < 0) gets output zero and lse -inf.  Positions
+ * may be visual or text, the tokens' own ones too.  Rows that no token attends
+ * may hold anything.  Values: K, V and q as in kvq_decode_attention_tree, with
+ * bf16 rows of K and V of any size (they are not passed through fp16).  No
+ * workspace: a unit's CTAs meet in a thread-block cluster.
+ */
+kvq_status kvq_decode_attention_window(const kvq_layout* L, const void* cache, const void* q_bf16, int32_t n_q,
+                                       const int32_t* seq_len, int32_t T, int32_t n_sink, int32_t window,
+                                       float softmax_scale, void* out_bf16, float* lse, void* stream);
 
 /* Size in bytes of the device scratch array used by
  * kvq_decode_attention_static_ws (16 MiB).  A layout fits when
