@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Sequence
 
 __all__ = [
@@ -98,9 +99,9 @@ class RopeDesc(ctypes.Structure):
                 ("axis", ctypes.c_uint8 * 64)]
 
 
-class Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
-                ("stride_t", ctypes.c_int64)]
+# kvq_rows as bytes (data, stride_b, stride_h, stride_t): a Structure takes
+# several times as long to make, and norm_rope needs four a call
+_ROWS = struct.Struct("=Qqqq").pack
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -159,8 +160,7 @@ def load() -> ctypes.CDLL:
     lib.kvq_attention_mass.restype = ctypes.c_int
     lib.kvq_cache_evict.argtypes = [LP, P, P, P, i32, LP, P, i32, i32, P, P, P, P]
     lib.kvq_cache_evict.restype = ctypes.c_int
-    RP = ctypes.POINTER(Rows)
-    lib.kvq_norm_rope.argtypes = [LP, ctypes.POINTER(RopeDesc), RP, RP, i32, P, i64, i64, P, P, P, f32, RP, RP, P]
+    lib.kvq_norm_rope.argtypes = [LP, ctypes.POINTER(RopeDesc), P, P, i32, P, i64, i64, P, P, P, f32, P, P, P]
     lib.kvq_norm_rope.restype = ctypes.c_int
     lib.kvq_tree_verify.argtypes = [i32, i32, i32, P, i32, i64, i64, P, P, i64, P, i64, i64, P, P, P, P, P, P, P, P, P]
     lib.kvq_tree_verify.restype = ctypes.c_int
@@ -586,11 +586,11 @@ def _rows(what: str, x, shape, dtype, dev: int):
     """[B, n, H, D] (last dimension contiguous, any other strides) as the C call's rows."""
     if not (x.dtype is dtype and x.shape == shape and x.get_device() == dev):
         _refuse(what, x, "bfloat16", shape, dev)
-    s = x.stride()
-    if s[3] != 1:
+    sb, st, sh, sd = x.stride()
+    if sd != 1:
         raise ValueError("last dim must be contiguous")
     # a dimension of one entry has no stride to speak of
-    return Rows(x.data_ptr(), s[0] if shape[0] > 1 else 0, s[2] if shape[2] > 1 else 0, s[1] if shape[1] > 1 else 0)
+    return _ROWS(x.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[2] > 1 else 0, st if shape[1] > 1 else 0)
 
 
 def norm_rope(L: Layout, R: RopeDesc, q, k, pos, inv_freq, q_out, k_out, q_weight=None, k_weight=None,
@@ -605,26 +605,33 @@ def norm_rope(L: Layout, R: RopeDesc, q, k, pos, inv_freq, q_out, k_out, q_weigh
     d, bf16 = L.d, torch.bfloat16
     if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
         raise ValueError("q and k (one at least) each come with their output")
-    x = q if q is not None else k
-    if x.dim() != 4:
+    x = (k if q is None else q).shape
+    if len(x) != 4:
         raise ValueError("q and k must be [B, n, heads, D]")
-    B, n = d.B, x.shape[1]
-    args = [None if y is None else _rows(what, y, (B, n, H, d.D), bf16, dev)
-            for what, y, H in (("q", q, d.H_q), ("k", k, d.H_kv), ("q_out", q_out, d.H_q), ("k_out", k_out, d.H_kv))]
-    if pos.dtype is not torch.int32 or pos.dim() not in (2, 3) or pos.shape[0] < R.n_axes or pos.shape[1:] not in ((B, n), (n,)):
-        raise ValueError(f"pos: int32 of shape {(R.n_axes, B, n)} or {(R.n_axes, n)} expected, got {pos.dtype} {tuple(pos.shape)}")
+    B, n, D = d.B, x[1], d.D
+    qi = qo = ki = ko = None
+    if q is not None:
+        x = (B, n, d.H_q, D)
+        qi, qo = _rows("q", q, x, bf16, dev), _rows("q_out", q_out, x, bf16, dev)
+    if k is not None:
+        x = (B, n, d.H_kv, D)
+        ki, ko = _rows("k", k, x, bf16, dev), _rows("k_out", k_out, x, bf16, dev)
+    at = pos.shape
+    if pos.dtype is not torch.int32 or len(at) not in (2, 3) or at[0] < R.n_axes or at[1:] != ((B, n) if len(at) == 3 else (n,)):
+        raise ValueError(f"pos: int32 of shape {(R.n_axes, B, n)} or {(R.n_axes, n)} expected, got {pos.dtype} {tuple(at)}")
     if pos.get_device() != dev:
         raise ValueError("pos must be on the current CUDA device")
     if n == 0:
         return
-    if n > 1 and pos.stride(-1) != 1:
+    if n >> 31:
+        raise ValueError(f"n must be an int32, got {n}")
+    ps = pos.stride()
+    if n > 1 and ps[-1] != 1:
         raise ValueError("last dim must be contiguous")
     fp = _ptr("inv_freq", inv_freq, torch.float32, (R.rot_dim // 2,), dev)
-    wq, wk = _ptr("q_weight", q_weight, bf16, (d.D,), dev), _ptr("k_weight", k_weight, bf16, (d.D,), dev)
-    ref = [None if y is None else ctypes.byref(y) for y in args]
-    st = load().kvq_norm_rope(ctypes.byref(L), ctypes.byref(R), ref[0], ref[1], _i32("n", n), pos.data_ptr(),
-                              pos.stride(0) if pos.shape[0] > 1 else 0, pos.stride(1) if pos.dim() == 3 and B > 1 else 0, fp,
-                              wq, wk, eps, ref[2], ref[3], st)
+    wq, wk = _ptr("q_weight", q_weight, bf16, (D,), dev), _ptr("k_weight", k_weight, bf16, (D,), dev)
+    st = load().kvq_norm_rope(ctypes.byref(L), ctypes.byref(R), qi, ki, n, pos.data_ptr(), ps[0] if at[0] > 1 else 0,
+                              ps[1] if len(at) == 3 and B > 1 else 0, fp, wq, wk, eps, qo, ko, st)
     if st != 0:
         raise KvqError(st, "kvq_norm_rope")
 
@@ -644,6 +651,8 @@ def tree_verify(logits, tokens, tree_mask, accept, race, path, path_len, next_to
     if logits.dim() != 3 or (draft_prob is not None and draft_prob.dim() != 3):
         raise ValueError("logits and draft_prob must be [B, n_q, vocab]")
     B, n_q, V = logits.shape
+    if (B | n_q | V) >> 31:
+        raise ValueError(f"the sizes of logits must be int32, got {(B, n_q, V)}")
     rows, per_seq = (B, n_q), (B,)
     if logits.dtype not in (torch.bfloat16, f32):
         _refuse("logits", logits, "float32", (B, n_q, V), dev)
@@ -661,7 +670,7 @@ def tree_verify(logits, tokens, tree_mask, accept, race, path, path_len, next_to
     mask = _ptr("tree_mask", tree_mask, torch.int64,
                 ((n_q,) if tree_mask.dim() == 1 else (1, n_q)) if shared else (B, n_q), dev)
     st = load().kvq_tree_verify(
-        _i32("B", B), _i32("n_q", n_q), _i32("vocab", V), at[0][0], 1 if logits.dtype is f32 else 0, at[0][1], at[0][2],
+        B, n_q, V, at[0][0], 1 if logits.dtype is f32 else 0, at[0][1], at[0][2],
         _ptr("tokens", tokens, i32, rows, dev), mask, 0 if shared else n_q, at[1][0], at[1][1], at[1][2],
         _ptr("accept", accept, f32, rows, dev), _ptr("race", race, f32, (B, V), dev),
         _ptr("temperature", temperature, f32, per_seq, dev), _ptr("tree_len", tree_len, i32, per_seq, dev),

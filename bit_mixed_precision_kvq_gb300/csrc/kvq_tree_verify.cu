@@ -3,8 +3,9 @@
 //
 // One thread-block cluster a sequence walks the tree.  At the path's last token
 // x the cluster's CTAs share out the row of logits l: one pass gives
-//   m = max l,  S = sum 2^((l - m) log2(e) / T),  p(v) = 2^((l_v - m) log2(e) / T) / S
-// and the lowest v of the maximum.  Then each child is held against p as kvq.h
+//   m = max l,  s = sum 2^((l - m) log2(e) / T),  p(v) = 2^((l_v - m) log2(e) / T) / (1 + s)
+// and the lowest v of the maximum, which s leaves out: ln p of a token that is
+// all but certain keeps its digits as log1p(s).  Then each child is held against p as kvq.h
 // says; a refusal with draft probabilities is one more pass, over
 //   r_k = max(r_{k-1} / Z_{k-1} - q, 0),  Z_k = sum r_k   (r_0 = p, Z_0 = 1),
 // and the end one more: argmax r(v) / race(v).  Rows are read again from L1 and
@@ -41,17 +42,20 @@ struct VerifyArgs {
   const int32_t* tree_len;
   int32_t *path, *path_len, *next;
   float* logprob;
+  uint32_t polls;  // limit of a wait for the cluster's other CTAs
 };
 
 // What CTAs exchange: a row's maximum (or the best race key), a sum, an index.
-struct Part {
+struct alignas(16) Part {
   float m, s;
   int32_t at;
 };
 
 struct VerifySmem {
   Part slot[2][kMaxRanks];  // by exchange parity and rank
-  Part warp[kVerifyWarps];
+  uint64_t bar[2];          // the ranks' parts have come (transaction bytes)
+  int late;                 // a wait gave up
+  Part warp[kVerifyWarps], joined;
   uint64_t kids[KVQ_MAX_QUERY_TOKENS];  // children of each token
   int32_t token[KVQ_MAX_QUERY_TOKENS];
   float u[KVQ_MAX_QUERY_TOKENS];
@@ -62,65 +66,131 @@ struct VerifySmem {
   float logp[KVQ_MAX_QUERY_TOKENS];
 };
 
-__device__ __forceinline__ void st_cluster_part(uint32_t addr, const Part& p) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(p.m) : "memory");
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr + 4), "f"(p.s) : "memory");
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr + 8), "r"(p.at) : "memory");
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
-// Softmax statistics of a and b together: 2^0 = 1 for the one whose maximum
-// stays.  at: the lowest index of the maximum.
-__device__ __forceinline__ Part join_rows(const Part& a, const Part& b, float sc) {
-  Part r;
-  r.m = fmaxf(a.m, b.m);
-  const float base = r.m == -INFINITY ? 0.f : r.m;
-  r.s = a.s * exp2f((a.m - base) * sc) + b.s * exp2f((b.m - base) * sc);
-  r.at = a.m > b.m ? a.at : (b.m > a.m ? b.at : min(a.at, b.at));
-  return r;
-}
-__device__ __forceinline__ Part join_sums(const Part& a, const Part& b, float) { return {0.f, a.s + b.s, 0}; }
-__device__ __forceinline__ Part join_best(const Part& a, const Part& b, float) {
-  return {fmaxf(a.m, b.m), 0.f, a.m > b.m ? a.at : (b.m > a.m ? b.at : min(a.at, b.at))};
-}
+// The parts of a warp's lanes joined, in every lane.
+// Softmax statistics: s counts all but the maximum at `at` (the lowest index of
+// it); the maxima of the lanes but one that has it are added.
+struct JoinRows {
+  float sc;
+  static __device__ __forceinline__ Part none() { return {-INFINITY, 0.f, INT_MAX}; }
+  __device__ __forceinline__ Part operator()(const Part& p) const {
+    const float m = warp_max(p.m);
+    const int lead = __ffs(__ballot_sync(0xffffffffu, p.m == m)) - 1;  // its maximum stays out
+    const float others = static_cast<int>(threadIdx.x & 31) == lead ? 0.f : 1.f;
+    return {m, warp_sum((p.s + others) * ex2((p.m - (m == -INFINITY ? 0.f : m)) * sc)),
+            __reduce_min_sync(0xffffffffu, p.m == m ? p.at : INT_MAX)};
+  }
+};
+struct JoinSums {
+  static __device__ __forceinline__ Part none() { return {0.f, 0.f, 0}; }
+  __device__ __forceinline__ Part operator()(const Part& p) const { return {0.f, warp_sum(p.s), 0}; }
+};
+struct JoinBest {
+  static __device__ __forceinline__ Part none() { return {0.f, 0.f, INT_MAX}; }
+  __device__ __forceinline__ Part operator()(const Part& p) const {
+    const float m = warp_max(p.m);
+    return {m, 0.f, __reduce_min_sync(0xffffffffu, p.m == m ? p.at : INT_MAX)};
+  }
+};
 
 // Every thread's part joined over the CTA and the cluster, the same to all.
+// Exchange t: warp 0 of each rank stores its CTA's part into slot t mod 2 of every
+// rank, asynchronous stores counted on that rank's barrier (a cluster barrier
+// around plain stores took 1,400 to 1,800 cycles, these about half).  Slots and
+// barriers alternate: a rank sends t + 2 only with every rank's t + 1 in hand,
+// which those send behind arming the barrier for t + 2.  A wait that gives up sets
+// sm.late, the same for the whole CTA: the walk ends there, and the other ranks'
+// waits give up in their turn.
+struct Exchange {
+  int rank, ranks;
+  uint32_t polls, turn;
+};
 template <typename Join>
-__device__ __forceinline__ Part join_all(VerifySmem& sm, Part p, float sc, int rank, int ranks, uint32_t& turn, Join&& join) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Part q = {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
-                    __shfl_xor_sync(0xffffffffu, p.at, o)};
-    p = lane & o ? join(q, p, sc) : join(p, q, sc);  // one order for both lanes
-  }
+__device__ __forceinline__ Part join_all(VerifySmem& sm, Part p, Exchange& x, const Join& join) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, s = x.turn & 1;
+  p = join(p);
   if (lane == 0) sm.warp[warp] = p;
   __syncthreads();
+  if (x.turn == 0) cluster_wait();  // every CTA of the cluster has started and armed its barriers
   if (warp == 0) {
-    p = sm.warp[lane % kVerifyWarps];
-#pragma unroll
-    for (int o = kVerifyWarps / 2; o > 0; o >>= 1) {
-      const Part q = {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
-                      __shfl_xor_sync(0xffffffffu, p.at, o)};
-      p = lane & o ? join(q, p, sc) : join(p, q, sc);
+    p = join(lane < kVerifyWarps ? sm.warp[lane] : Join::none());
+    if (lane < x.ranks)
+      st_async_v4(dsmem_addr(&sm.slot[s][x.rank], lane), make_float4(p.m, p.s, __int_as_float(p.at), 0.f), dsmem_addr(&sm.bar[s], lane));
+    const bool late = __any_sync(0xffffffffu, !mbar_wait_cluster(&sm.bar[s], (x.turn >> 1) & 1, x.polls));
+    if (lane == 0 && !late) mbar_arrive_expect_tx(&sm.bar[s], 16 * x.ranks);
+    p = join(lane < x.ranks && !late ? sm.slot[s][lane] : Join::none());
+    if (lane == 0) {
+      sm.joined = p;
+      if (late) sm.late = 1;
     }
-    if (lane < ranks) st_cluster_part(dsmem_addr(&sm.slot[turn & 1][rank], lane), p);
   }
-  // Slots alternate: a rank writes these again after the next exchange, which
-  // it passes only when every rank has come to it, i.e. has read them here.
-  cluster_sync();
-  p = sm.slot[turn & 1][0];
-  for (int r = 1; r < ranks; ++r) p = join(p, sm.slot[turn & 1][r], sc);
-  ++turn;
-  return p;
+  __syncthreads();
+  ++x.turn;
+  return sm.joined;
 }
 
-// The CTA's share of a row of V elements of type X: f(v0, values, count) for
-// groups of up to kGroup = 16 bytes of consecutive ones, aligned groups first
-// loaded kAhead at a time.
+// Asks for the CTA's share of a row of V elements of type X, or the first
+// megabyte of it, in L2 (one thread).
 template <typename X>
-struct Row {
-  static constexpr int kGroup = 16 / sizeof(X), kAhead = 4;
-  static __device__ __forceinline__ void values(uint4 w, float (&x)[kGroup]) {
+__device__ __forceinline__ void prefetch_share(const X* row, int V, int rank, int ranks) {
+  const int log = 31 - __clz(ranks);
+  const X* lo = row + (static_cast<int64_t>(V) * rank >> log);
+  const X* hi = row + (static_cast<int64_t>(V) * (rank + 1) >> log);
+  const uintptr_t a = (reinterpret_cast<uintptr_t>(lo) + 15) & ~uintptr_t{15}, b = reinterpret_cast<uintptr_t>(hi) & ~uintptr_t{15};
+  if (a < b) prefetch_l2(reinterpret_cast<const void*>(a), static_cast<uint32_t>(min(b - a, uintptr_t{1} << 20)));
+}
+
+// A thread's groups on their way through shared memory (cp.async): kAhead of them
+// under way, of a row of logits (16 bytes a group) and of up to two rows of fp32.
+constexpr int kAhead = 3, kRing = kAhead + 1;
+template <int kBytes>  // of a group's fp32 values: 16 or 32
+struct Ring {
+  uint4 x[kRing][kVerifyThreads];
+  uint4 e[kRing][kBytes / 16][kVerifyThreads];
+  uint4 q[kRing][kBytes / 16][kVerifyThreads];  // (with draft probabilities)
+};
+
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// A CTA's share of a row of V elements of type X: groups of kGroup = 16 bytes,
+// and in rank 0, one by one, the elements before the row's first 16-byte
+// boundary and behind its last.
+template <typename X>
+struct Share {
+  static constexpr int kGroup = 16 / sizeof(X);
+  using R = Ring<4 * kGroup>;
+  const X* row;
+  int V, from, n;       // the thread's groups: n of them, kVerifyThreads apart, the first at index `from`
+  int before, behind;   // its single elements (-1: none)
+
+  __device__ __forceinline__ Share(const X* r, int V_, int rank, int ranks) : row(r), V(V_) {
+    const int tid = threadIdx.x, log = 31 - __clz(ranks);  // a power of two
+    const int head = min(V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / sizeof(X)));
+    const int all = (V - head) / kGroup;
+    const int lo = static_cast<int>(static_cast<int64_t>(all) * rank >> log), hi = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) >> log);
+    from = head + (lo + tid) * kGroup;
+    n = max(0, hi - lo - tid + kVerifyThreads - 1) / kVerifyThreads;
+    before = rank == 0 && tid < head ? tid : -1;
+    behind = rank == 0 && head + all * kGroup + tid < V ? head + all * kGroup + tid : -1;
+  }
+  __device__ __forceinline__ static float value(const X* p) {
+    if constexpr (sizeof(X) == 2) return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
+    else return *p;
+  }
+  __device__ __forceinline__ static void values(const uint4& w, float (&x)[kGroup]) {
     if constexpr (sizeof(X) == 2) {
       x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
       x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
@@ -128,115 +198,223 @@ struct Row {
       x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
     }
   }
-  static __device__ __forceinline__ float value(const X* p) {
-    if constexpr (sizeof(X) == 2) return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
-    else return *p;
+  // one element, with -inf behind it
+  __device__ __forceinline__ static uint4 single(const X* p) {
+    constexpr uint32_t kNone = sizeof(X) == 2 ? 0xff80ff80u : 0xff800000u;
+    uint4 w = make_uint4(kNone, kNone, kNone, kNone);
+    if constexpr (sizeof(X) == 2) w.x = 0xff800000u | *reinterpret_cast<const uint16_t*>(p);
+    else w.x = *reinterpret_cast<const uint32_t*>(p);
+    return w;
   }
-  template <typename F>
-  static __device__ __forceinline__ void each(const X* row, int V, int rank, int ranks, F&& f) {
-    const int head = min(V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / sizeof(X)));
-    const int n = (V - head) / kGroup, lo = static_cast<int>(static_cast<int64_t>(n) * rank / ranks),
-              hi = static_cast<int>(static_cast<int64_t>(n) * (rank + 1) / ranks);
-    const uint4* at = reinterpret_cast<const uint4*>(row + head);
-    float x[kGroup];
-    for (int i = lo + threadIdx.x; i < hi; i += kAhead * kVerifyThreads) {
-      uint4 w[kAhead];
+  // Asks for the thread's first groups of the row, and of a row of fp32.
+  __device__ __forceinline__ void begin(R& ring) const {
+#pragma unroll 1
+    for (int i = 0; i < min(n, kAhead); ++i) copy_async(&ring.x[i][threadIdx.x], row + from + i * kVerifyThreads * kGroup, 16);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void begin_e(R& ring, const float* e_row) const {
+#pragma unroll 1
+    for (int i = 0; i < min(n, kAhead); ++i) bring(&ring.e[i][0][threadIdx.x], e_row + from + i * kVerifyThreads * kGroup);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // a group's fp32 values, in pieces kVerifyThreads apart
+  __device__ __forceinline__ static void bring(uint4* to, const float* src) {
+    if (reinterpret_cast<uintptr_t>(src) % 16 == 0) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (i + k * kVerifyThreads < hi) w[k] = at[i + k * kVerifyThreads];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (i + k * kVerifyThreads < hi) {
-          values(w[k], x);
-          f(head + (i + k * kVerifyThreads) * kGroup, x, kGroup);
-        }
+      for (int k = 0; k < kGroup / 4; ++k) copy_async(to + k * kVerifyThreads, src + 4 * k, 16);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kGroup; ++k) copy_async(reinterpret_cast<float*>(to + k / 4 * kVerifyThreads) + k % 4, src + k, 4);
     }
-    if (rank == 0) {  // what lies before the first 16-byte boundary and behind the last
-      const int tail = head + n * kGroup, v = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
-      if (v < V) {
-        x[0] = value(row + v);
-        f(v, x, 1);
+  }
+  // f(v, logits, e, q) for every group of the thread in increasing order of v;
+  // e and q: rows of V fp32, or null (zeros come).  x_here, e_here: begin (or a
+  // pass over at most kAhead groups) has brought the row's first groups,
+  // begin_e e's.
+  template <bool kE, bool kQ, typename F>
+  __device__ __forceinline__ void each(R& ring, bool x_here, const float* e_row, bool e_here, const float* q_row, F&& f) const {
+    constexpr int kStep = kVerifyThreads * kGroup;
+    const int tid = threadIdx.x;
+    auto issue = [&](int i, bool with_x, bool with_e) {
+      if (i < n) {
+        const int s = i % kRing, v = from + i * kStep;
+        if (with_x) copy_async(&ring.x[s][tid], row + v, 16);
+        if (kE && with_e) bring(&ring.e[s][0][tid], e_row + v);
+        if (kQ && q_row) bring(&ring.q[s][0][tid], q_row + v);
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i) issue(i, !x_here, !e_here);
+    const int last = n + (behind >= 0 ? 1 : 0);
+#pragma unroll 1
+    for (int i = before >= 0 ? -1 : 0; i < last; ++i) {
+      uint4 w;
+      float e[kGroup] = {}, q[kGroup] = {};
+      int v;
+      if (i >= 0 && i < n) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const int s = i % kRing;
+        v = from + i * kStep;
+        w = ring.x[s][tid];
+#pragma unroll
+        for (int k = 0; k < kGroup / 4; ++k) {
+          if (kE) reinterpret_cast<float4*>(e)[k] = reinterpret_cast<const float4&>(ring.e[s][k][tid]);
+          if (kQ && q_row) reinterpret_cast<float4*>(q)[k] = reinterpret_cast<const float4&>(ring.q[s][k][tid]);
+        }
+        issue(i + kAhead, true, true);  // into the slot that the group before this one had
+      } else {
+        v = i < 0 ? before : behind;
+        w = single(row + v);
+        if (kE) e[0] = e_row[v];
+        if (kQ && q_row) q[0] = q_row[v];
+      }
+      f(v, w, e, q);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 };
 
-// count values of a row of fp32 from index v on.
-template <int N>
-__device__ __forceinline__ void fetch(const float* row, int v, int count, float (&x)[N]) {
-  if (count == N && reinterpret_cast<uintptr_t>(row + v) % 16 == 0) {
+__device__ __forceinline__ float fast_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Softmax statistics of the thread's elements (begin has been called).  The sum of the group that holds
+// the maximum is kept apart and taken anew without it at the end.
+template <typename X>
+__device__ __forceinline__ Part row_part(const Share<X>& row, typename Share<X>::R& ring, float sc) {
+  constexpr int kGroup = Share<X>::kGroup;
+  float m = -INFINITY, rest = 0.f, own = 0.f;
+  int at = INT_MAX;  // first index of the group with the maximum
+  uint4 best = {};   // and the group
+  auto sum_of = [&](const float (&x)[kGroup], float base) {
+    float s = 0.f, r = 0.f;
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float4 w = reinterpret_cast<const float4*>(row + v)[i];
-      x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
+    for (int i = 0; i < kGroup; i += 2) {
+      s += ex2((x[i] - base) * sc);
+      r += ex2((x[i + 1] - base) * sc);
     }
-  } else {
+    return s + r;
+  };
+  row.template each<false, false>(ring, true, nullptr, false, nullptr, [&](int v, const uint4& w, const float (&)[kGroup], const float (&)[kGroup]) {
+    float x[kGroup];
+    Share<X>::values(w, x);
+    float top = x[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = i < count ? row[v + i] : 0.f;
-  }
+    for (int i = 1; i < kGroup; ++i) top = fmaxf(top, x[i]);
+    const bool more = top > m;
+    const float f = more ? ex2((m - top) * sc) : 1.f;
+    m = more ? top : m;
+    const float s = sum_of(x, m == -INFINITY ? 0.f : m);
+    rest = more ? (rest + own) * f : rest + s;
+    own = more ? s : own;
+    at = more ? v : at;
+    best.x = more ? w.x : best.x;
+    best.y = more ? w.y : best.y;
+    best.z = more ? w.z : best.z;
+    best.w = more ? w.w : best.w;
+  });
+  if (m == -INFINITY) return {m, rest + own, INT_MAX};  // (NaN stays)
+  float x[kGroup];
+  Share<X>::values(best, x);
+  int first = 0;
+#pragma unroll
+  for (int i = kGroup - 1; i >= 0; --i)
+    if (x[i] == m) first = i;
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i)
+    if (i == first) x[i] = -INFINITY;
+  return {m, rest + sum_of(x, m), at + first};
 }
 
 template <typename X, bool kDraft>
 __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ VerifySmem sm;
-  constexpr int kGroup = Row<X>::kGroup;
+  typename Share<X>::R& ring = *reinterpret_cast<typename Share<X>::R*>(ring_smem);
+  constexpr int kGroup = Share<X>::kGroup;
   const int rank = static_cast<int>(cluster_ctarank()), ranks = static_cast<int>(cluster_nctarank());
   const int b = blockIdx.x / ranks, tid = threadIdx.x;
+  Exchange xc = {rank, ranks, a.polls, 0u};
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.bar[i], 1);
+    fence_barrier_init();
+    for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.bar[i], 16 * ranks);
+    sm.late = 0;
+  }
+  __syncwarp();
+  cluster_arrive();  // waited for at the first exchange
+  if (tid < KVQ_MAX_QUERY_TOKENS) sm.kids[tid] = 0ull;
   pdl_wait();
   if (tid == 0) pdl_launch_dependents();
+  const X* const rows = static_cast<const X*>(a.logits) + b * a.lsb;
+  const float* const race = a.race + static_cast<int64_t>(b) * a.V;
+  Share<X> row(rows, a.V, rank, ranks);
+  row.begin(ring);
   const int n = a.tree_len ? a.tree_len[b] : a.n_q;
   const float temp = a.temp ? a.temp[b] : 1.f;
+  uint64_t above = 0;
+  if (tid < a.n_q) {
+    sm.token[tid] = a.tokens[static_cast<int64_t>(b) * a.n_q + tid];
+    sm.u[tid] = a.accept[static_cast<int64_t>(b) * a.n_q + tid];
+    above = a.mask[b * a.mask_sb + tid] & ((1ull << tid) - 1ull);
+  }
   const bool greedy = !(temp > 0.f);
   const float sc = greedy ? kLog2e : kLog2e / temp;
   bool good = n >= 1 && n <= a.n_q;
-  if (tid < KVQ_MAX_QUERY_TOKENS) sm.kids[tid] = 0ull;
   __syncthreads();
-  if (good && tid < n) {
-    sm.token[tid] = a.tokens[static_cast<int64_t>(b) * a.n_q + tid];
-    sm.u[tid] = a.accept[static_cast<int64_t>(b) * a.n_q + tid];
-    const uint64_t above = a.mask[b * a.mask_sb + tid] & ((1ull << tid) - 1ull);
-    if (above) atomicOr(reinterpret_cast<unsigned long long*>(&sm.kids[63 - __clzll(above)]), 1ull << tid);
-  }
-  cluster_sync();  // every CTA runs (its shared memory may be written); sm is set up
+  if (above && tid < n)
+    atomicOr(reinterpret_cast<unsigned long long*>(&sm.kids[63 - __clzll(above)]), 1ull << tid);
+  // The race row while the walk goes on: its first groups stay in the ring where
+  // every row has the same groups (16-byte boundaries at the same places).
+  const bool whole_race = good && !greedy && a.lst * sizeof(X) % 16 == 0;
+  if (whole_race) row.begin_e(ring, race);
+  if (tid == kVerifyThreads - 1 && good && !greedy) prefetch_share(race, a.V, rank, ranks);
+  __syncthreads();
+  if (!good) cluster_wait();  // (no exchange comes)
 
-  uint32_t turn = 0;
   int cur = 0, count = 1, next = -1;
   while (good) {
-    const X* row = static_cast<const X*>(a.logits) + b * a.lsb + cur * a.lst;
     const float* drow = kDraft ? a.draft + b * a.dsb + cur * a.dst : nullptr;
     uint64_t kids = sm.kids[cur];
+    if (kids && tid == kVerifyThreads - 1) {  // what is likely to be read next
+      prefetch_share(rows + (__ffsll(kids) - 1) * a.lst, a.V, rank, ranks);
+      if (kDraft && !greedy) prefetch_share(drow, a.V, rank, ranks);
+    }
+    float kid_l = -INFINITY, kid_q = 0.f;  // on their way during the pass
     if (tid < 64 && (kids >> tid & 1ull)) {
       const int c = sm.token[tid];
-      const bool is = c >= 0 && c < a.V;
-      sm.kid_l[tid] = is ? Row<X>::value(row + c) : -INFINITY;
-      if (kDraft) sm.kid_q[tid] = is ? drow[c] : 0.f;
-    }
-    Part p = {-INFINITY, 0.f, INT_MAX};
-    Row<X>::each(row, a.V, rank, ranks, [&](int v, const float (&x)[kGroup], int c) {
-      float top = x[0];
-      int at = 0;
-#pragma unroll
-      for (int i = 1; i < kGroup; ++i)
-        if (i < c && x[i] > top) top = x[i], at = i;
-      if (top > p.m) {
-        p.s *= exp2f((p.m - top) * sc);
-        p.m = top;
-        p.at = v + at;
-      } else if (top == p.m) {
-        p.at = min(p.at, v + at);
+      if (c >= 0 && c < a.V) {
+        kid_l = Share<X>::value(row.row + c);
+        if (kDraft) kid_q = drow[c];
       }
-      const float base = p.m == -INFINITY ? 0.f : p.m;
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i)
-        if (i < c) p.s += exp2f((x[i] - base) * sc);
-    });
-    p = join_all(sm, p, sc, rank, ranks, turn, join_rows);
-    const float m = p.m, inv_s = 1.f / p.s, log_s = logf(p.s);
+    }
+    const Part mine = row_part(row, ring, sc);
+    if (tid < 64) {
+      sm.kid_l[tid] = kid_l;
+      sm.kid_q[tid] = kid_q;
+    }
+    const Part p = join_all(sm, mine, xc, JoinRows{sc});
+    const float m = p.m, inv_s = 1.f / (1.f + p.s), log_s = log1pf(p.s);
     const int best = p.at;
-    good = p.s > 0.f && p.s < INFINITY && m > -INFINITY && m < INFINITY;
+    good = !sm.late && p.s >= 0.f && p.s < INFINITY && m > -INFINITY && m < INFINITY;
     if (!good) break;
-    auto prob = [&](float l) { return exp2f((l - m) * sc) * inv_s; };
+    auto prob = [&](float l) { return ex2((l - m) * sc) * inv_s; };
     auto log_prob = [&](float l) { return (l - m) * (sc * kLn2) - log_s; };
+    // r_k of a group: `chain` steps of the residual
+    auto residual = [&](const uint4& w, const float (&q)[kGroup], int chain, float (&y)[kGroup]) {
+      float x[kGroup];
+      Share<X>::values(w, x);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) y[i] = prob(x[i]);
+      for (int k = 0; k < chain; ++k) {
+        const float z = sm.inv_z[k];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) y[i] = fmaxf(y[i] * z - q[i], 0.f);
+      }
+    };
 
     // the children, in index order: the same decisions in every thread
     int took = -1, refused = 0;  // refused: entries of inv_z or out
@@ -265,88 +443,87 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
       if (greedy) continue;
       if constexpr (kDraft) {
         // r_k = max(r_{k-1} / Z_{k-1} - q, 0) with the sum of the last one
-        const float inv = 1.f / total;
-        __syncthreads();  // all have read the earlier entries' state of this loop
-        if (tid == 0) sm.inv_z[refused] = inv;
+        __syncthreads();  // all have read what the last refusal wrote
+        if (tid == 0) sm.inv_z[refused] = 1.f / total;
         __syncthreads();
-        Part z = {0.f, 0.f, 0};
-        Row<X>::each(row, a.V, rank, ranks, [&](int v, const float (&x)[kGroup], int cnt) {
-          float q[kGroup];
-          fetch(drow, v, cnt, q);
+        Part z = JoinSums::none();
+        row.template each<false, true>(ring, row.n <= kAhead, nullptr, false, drow, [&](int, const uint4& w, const float (&)[kGroup], const float (&q)[kGroup]) {
+          float y[kGroup];
+          residual(w, q, refused + 1, y);
+          float s = 0.f;
 #pragma unroll
-          for (int i = 0; i < kGroup; ++i)
-            if (i < cnt) {
-              float y = prob(x[i]);
-              for (int k = 0; k <= refused; ++k) y = fmaxf(y * sm.inv_z[k] - q[i], 0.f);
-              z.s += y;
-            }
+          for (int i = 0; i < kGroup; ++i) s += y[i];
+          z.s += s;
         });
-        z = join_all(sm, z, 0.f, rank, ranks, turn, join_sums);
+        z = join_all(sm, z, xc, JoinSums());
+        if (sm.late) break;
         if (z.s > 0.f) {  // else nothing is left and r stays
           total = z.s;
           ++refused;
         }
-      } else {
-        if (c >= 0 && c < a.V && r > 0.f) {
-          __syncthreads();
-          if (tid == 0) sm.out[refused] = c;
-          __syncthreads();
-          total = fmaxf(total - r, 0.f);
-          ++refused;
-        }
+      } else if (c >= 0 && c < a.V && r > 0.f) {
+        __syncthreads();
+        if (tid == 0) sm.out[refused] = c;
+        __syncthreads();
+        total = fmaxf(total - r, 0.f);
+        ++refused;
       }
     }
+    if (sm.late) break;
     if (tid == 0) sm.path[count - 1] = cur;
     if (took >= 0) {
       if (tid == 0) sm.logp[count - 1] = log_prob(sm.kid_l[took]);
       cur = took;
       ++count;
+      row = Share<X>(rows + cur * a.lst, a.V, rank, ranks);
+      row.begin(ring);
       __syncthreads();  // kid_l is written anew
       continue;
     }
     // the token behind the path
     next = best;
     if (!greedy) {
-      const float* race = a.race + static_cast<int64_t>(b) * a.V;
-      Part w = {0.f, 0.f, INT_MAX};
-      Row<X>::each(row, a.V, rank, ranks, [&](int v, const float (&x)[kGroup], int cnt) {
-        float e[kGroup], q[kGroup];
-        fetch(race, v, cnt, e);
-        if (kDraft && refused) fetch(drow, v, cnt, q);
-        bool cut = false;
-        if constexpr (!kDraft)
-          for (int k = 0; k < refused; ++k) cut |= sm.out[k] >= v && sm.out[k] < v + cnt;
+      Part k = JoinBest::none();
+      row.template each<true, kDraft>(ring, row.n <= kAhead, race, whole_race, refused ? drow : nullptr, [&](int v, const uint4& w, const float (&e)[kGroup], const float (&q)[kGroup]) {
+        float y[kGroup];
+        residual(w, q, kDraft ? refused : 0, y);
+        if constexpr (!kDraft) {
+          for (int g = 0; g < refused; ++g) {
+            const int d = sm.out[g] - v;
+            if (d >= 0 && d < kGroup) {
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-          if (i < cnt) {
-            float y = prob(x[i]);
-            if constexpr (kDraft) {
-              for (int k = 0; k < refused; ++k) y = fmaxf(y * sm.inv_z[k] - q[i], 0.f);
-            } else if (cut) {
-              for (int k = 0; k < refused; ++k)
-                if (sm.out[k] == v + i) y = 0.f;
+              for (int i = 0; i < kGroup; ++i) y[i] = i == d ? 0.f : y[i];
             }
-            const float key = e[i] > 0.f ? __fdividef(y, e[i]) : 0.f;
-            if (key > w.m || (key == w.m && key > 0.f && v + i < w.at)) w.m = key, w.at = v + i;
           }
+        }
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          const float y_e = y[i] * fast_inverse(e[i]), key = e[i] > 0.f ? y_e : 0.f;
+          k.at = key > k.m ? v + i : k.at;
+          k.m = key > k.m ? key : k.m;
+        }
       });
-      w = join_all(sm, w, 0.f, rank, ranks, turn, join_best);
-      if (w.m > 0.f) next = w.at;
+      k = join_all(sm, k, xc, JoinBest());
+      if (k.m > 0.f) next = k.at;
     }
-    if (tid == 0) sm.logp[count - 1] = log_prob(Row<X>::value(row + next));
+    if (tid == 0) sm.logp[count - 1] = log_prob(Share<X>::value(row.row + next));
     break;
   }
-  if (rank != 0) return;  // the last exchange is behind every rank
+  // No CTA ends while another may still send to it, or with copies under way.
+  cluster_arrive_relaxed();
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if (tid == 0) {
+  if (sm.late) good = false;
+  if (rank == 0 && tid == 0) {
     a.path_len[b] = good ? count : -1;
     a.next[b] = good ? next : -1;
   }
-  if (tid < a.n_q) {
+  if (rank == 0 && tid < a.n_q) {
     const int64_t i = static_cast<int64_t>(b) * a.n_q + tid;
     a.path[i] = good && tid < count ? sm.path[tid] : -1;
     if (a.logprob) a.logprob[i] = good && tid < count ? sm.logp[tid] : 0.f;
   }
+  cluster_wait();
 }
 
 }  // namespace
@@ -426,7 +603,8 @@ extern "C" kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, con
                                              : reinterpret_cast<const void*>(&kvq::verify_kernel<float, false>))
                                : (draft_prob ? reinterpret_cast<const void*>(&kvq::verify_kernel<uint16_t, true>)
                                              : reinterpret_cast<const void*>(&kvq::verify_kernel<uint16_t, false>));
-  const kvq_status st = kvq_allow_clusters(fn, 0);
+  const int smem = logits_fp32 ? sizeof(kvq::Ring<16>) : sizeof(kvq::Ring<32>);
+  const kvq_status st = kvq_allow_clusters(fn, smem);
   if (st != KVQ_OK) return st;
   // As many CTAs a sequence as one wave holds, but none below 16 bytes a thread.
   int ranks = 1;
@@ -453,5 +631,6 @@ extern "C" kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, con
   a.path_len = path_len;
   a.next = next_token;
   a.logprob = logprob;
-  return kvq::launch_clusters(fn, dim3(static_cast<unsigned>(B * ranks)), ranks, kvq::kVerifyThreads, 0, stream, &a);
+  a.polls = kvq_tile_polls();
+  return kvq::launch_clusters(fn, dim3(static_cast<unsigned>(B * ranks)), ranks, kvq::kVerifyThreads, smem, stream, &a);
 }
