@@ -96,7 +96,7 @@ struct JoinSums {
   __device__ __forceinline__ Part operator()(const Part& p) const { return {0.f, warp_sum(p.s), 0}; }
 };
 struct JoinBest {
-  static __device__ __forceinline__ Part none() { return {0.f, 0.f, INT_MAX}; }
+  static __device__ __forceinline__ Part none() { return {-INFINITY, 0.f, INT_MAX}; }
   __device__ __forceinline__ Part operator()(const Part& p) const {
     const float m = warp_max(p.m);
     return {m, 0.f, __reduce_min_sync(0xffffffffu, p.m == m ? p.at : INT_MAX)};
@@ -161,7 +161,7 @@ struct Ring {
 };
 
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
-  if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  if (bytes == 16) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
@@ -275,9 +275,9 @@ struct Share {
   }
 };
 
-__device__ __forceinline__ float fast_inverse(float x) {
+__device__ __forceinline__ float fast_log2(float x) {  // 2^-22 of itself; -inf for 0
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -290,13 +290,17 @@ __device__ __forceinline__ Part row_part(const Share<X>& row, typename Share<X>:
   int at = INT_MAX;  // first index of the group with the maximum
   uint4 best = {};   // and the group
   auto sum_of = [&](const float (&x)[kGroup], float base) {
-    float s = 0.f, r = 0.f;
+    const uint64_t neg = pair_of(-base, -base), scale = pair_of(sc, sc);
+    uint64_t sum = 0ull;
 #pragma unroll
     for (int i = 0; i < kGroup; i += 2) {
-      s += ex2((x[i] - base) * sc);
-      r += ex2((x[i + 1] - base) * sc);
+      float u, v;
+      unpair(mul_pair(add_pair(pair_of(x[i], x[i + 1]), neg), scale), u, v);
+      sum = add_pair(sum, pair_of(ex2(u), ex2(v)));
     }
-    return s + r;
+    float u, v;
+    unpair(sum, u, v);
+    return u + v;
   };
   row.template each<false, false>(ring, true, nullptr, false, nullptr, [&](int v, const uint4& w, const float (&)[kGroup], const float (&)[kGroup]) {
     float x[kGroup];
@@ -351,28 +355,34 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
   if (tid == 0) pdl_launch_dependents();
   const X* const rows = static_cast<const X*>(a.logits) + b * a.lsb;
   const float* const race = a.race + static_cast<int64_t>(b) * a.V;
-  Share<X> row(rows, a.V, rank, ranks);
-  row.begin(ring);
   const int n = a.tree_len ? a.tree_len[b] : a.n_q;
   const float temp = a.temp ? a.temp[b] : 1.f;
+  int32_t token = 0;
+  float u = 0.f;
   uint64_t above = 0;
   if (tid < a.n_q) {
-    sm.token[tid] = a.tokens[static_cast<int64_t>(b) * a.n_q + tid];
-    sm.u[tid] = a.accept[static_cast<int64_t>(b) * a.n_q + tid];
+    token = a.tokens[static_cast<int64_t>(b) * a.n_q + tid];
+    u = a.accept[static_cast<int64_t>(b) * a.n_q + tid];
     above = a.mask[b * a.mask_sb + tid] & ((1ull << tid) - 1ull);
   }
+  Share<X> row(rows, a.V, rank, ranks);
+  row.begin(ring);
   const bool greedy = !(temp > 0.f);
   const float sc = greedy ? kLog2e : kLog2e / temp;
   bool good = n >= 1 && n <= a.n_q;
-  __syncthreads();
-  if (above && tid < n)
-    atomicOr(reinterpret_cast<unsigned long long*>(&sm.kids[63 - __clzll(above)]), 1ull << tid);
+  __syncthreads();  // kids is zero
+  if (tid < KVQ_MAX_QUERY_TOKENS) {
+    sm.token[tid] = token;
+    sm.u[tid] = u;
+    if (above && tid < n)
+      atomicOr(reinterpret_cast<unsigned long long*>(&sm.kids[63 - __clzll(above)]), 1ull << tid);
+  }
   // The race row while the walk goes on: its first groups stay in the ring where
   // every row has the same groups (16-byte boundaries at the same places).
   const bool whole_race = good && !greedy && a.lst * sizeof(X) % 16 == 0;
-  if (whole_race) row.begin_e(ring, race);
   if (tid == kVerifyThreads - 1 && good && !greedy) prefetch_share(race, a.V, rank, ranks);
   __syncthreads();
+  if (whole_race) row.begin_e(ring, race);
   if (!good) cluster_wait();  // (no exchange comes)
 
   int cur = 0, count = 1, next = -1;
@@ -485,26 +495,35 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
     if (!greedy) {
       Part k = JoinBest::none();
       row.template each<true, kDraft>(ring, row.n <= kAhead, race, whole_race, refused ? drow : nullptr, [&](int v, const uint4& w, const float (&e)[kGroup], const float (&q)[kGroup]) {
+        // log2 of r / race up to a constant; -inf for what cannot be picked
         float y[kGroup];
-        residual(w, q, kDraft ? refused : 0, y);
+        if (kDraft && refused) {
+          residual(w, q, refused, y);
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) y[i] = fast_log2(y[i]);
+        } else {
+          Share<X>::values(w, y);
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) y[i] = (y[i] - m) * sc;
+        }
         if constexpr (!kDraft) {
           for (int g = 0; g < refused; ++g) {
             const int d = sm.out[g] - v;
             if (d >= 0 && d < kGroup) {
 #pragma unroll
-              for (int i = 0; i < kGroup; ++i) y[i] = i == d ? 0.f : y[i];
+              for (int i = 0; i < kGroup; ++i) y[i] = i == d ? -INFINITY : y[i];
             }
           }
         }
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          const float y_e = y[i] * fast_inverse(e[i]), key = e[i] > 0.f ? y_e : 0.f;
+          const float late = y[i] - fast_log2(e[i]), key = e[i] > 0.f ? late : -INFINITY;
           k.at = key > k.m ? v + i : k.at;
           k.m = key > k.m ? key : k.m;
         }
       });
       k = join_all(sm, k, xc, JoinBest());
-      if (k.m > 0.f) next = k.at;
+      if (k.m > -INFINITY) next = k.at;
     }
     if (tid == 0) sm.logp[count - 1] = log_prob(Share<X>::value(row.row + next));
     break;
@@ -606,10 +625,10 @@ extern "C" kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, con
   const int smem = logits_fp32 ? sizeof(kvq::Ring<16>) : sizeof(kvq::Ring<32>);
   const kvq_status st = kvq_allow_clusters(fn, smem);
   if (st != KVQ_OK) return st;
-  // As many CTAs a sequence as one wave holds, but none below 16 bytes a thread.
+  // As many CTAs a sequence as one wave holds, but none below 8 bytes a thread.
   int ranks = 1;
   while (ranks < kvq::kMaxRanks && 2 * ranks * static_cast<int64_t>(B) <= n_sm &&
-         2 * ranks * 16 * kvq::kVerifyThreads <= static_cast<int64_t>(vocab) * elt)
+         ranks * 16 * kvq::kVerifyThreads <= static_cast<int64_t>(vocab) * elt)
     ranks *= 2;
   kvq::VerifyArgs a;
   a.n_q = n_q;
