@@ -6,22 +6,29 @@
 //   a_i = pos[axis_i] * inv_freq_i:
 //     (y_p, y_q) -> (y_p cos a_i - y_q sin a_i, y_q cos a_i + y_p sin a_i)
 //
-// Every row is read once and written once (512 bytes), with some 60 fp32
-// operations a lane in between: bound by memory once there are enough rows.
-// 16 lanes hold a row of 128, each the elements of 4 pairs (8 beyond the
-// rotated part), so that a pair never crosses lanes and the mean takes 4
-// shuffles.  A lane's angles depend on the token alone: 16 lanes take `heads`
-// heads of one token, with the loads of kFlight rows issued before any is used.
+// Every row is read once and written once (512 bytes), with some 55 instructions
+// a lane in between: bound by memory once there are enough rows.  16 lanes hold a
+// row of 128, each the elements of 4 pairs (8 beyond the rotated part), so that a
+// pair never crosses lanes and the mean takes 4 shuffles.  A lane's angles depend
+// on the token alone: 16 lanes take up to 8 heads of one token, load all their
+// rows at once, make the weights times cosines and sines meanwhile, and end
+// (short-lived CTAs overlap their phases; a CTA that went from token to token
+// with 4 rows under way took 234 us where this takes 162).
 //
 // Angles.  A position may be large (a product with a frequency near 1 loses
 // all its digits in fp32 from 2^24 on), so the turn is taken modulo 1 in
 // integers: inv_freq / 2 pi modulo 1 as a 64-bit binary fraction, times the
 // position modulo 2^64.  Its top 32 bits, rounded to fp32, are the angle to
-// 2^-25 of a turn.  The rest is fp32, rounded once to bf16.
+// 2^-25 of a turn, and the fast sine and cosine of it are off by 2^-21.  The rest
+// is fp32, in pairs, rounded once to bf16.
+//
+// Measured (GB300): 8 x 2940 tokens, 40 + 40 heads with norms (963 MB) 162 us, 5.9
+// TB/s, 0.88 of a copy; 16 x 26 tokens, 32 + 32 heads 5.0 us; one token 2.1 us.
 #include "kvq_geom.cuh"
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace kvq {
 namespace {
@@ -34,7 +41,7 @@ struct RopeSide {
   uint16_t* out;
   int64_t sb, sh, st, ob, oh, ot;
   const uint16_t* weight;  // bf16 [D] or null: no norm
-  int32_t H, groups;       // heads, and groups of `heads` of them
+  int32_t H, groups;       // heads, and groups of them
 };
 
 struct RopeArgs {
@@ -43,133 +50,159 @@ struct RopeArgs {
   int64_t pos_axis, pos_b;
   const float* freq;  // [rot / 2]
   float eps;
-  int32_t n, rot, heads;
-  bool interleaved;
-  int64_t tokens;  // B n
+  int32_t n, tokens, rot;  // tokens: B n
   uint8_t axis[kD / 2];
 };
 
-__device__ __forceinline__ void bf16x4(uint2 w, float (&x)[4]) {
-  x[0] = bf16_lo(w.x);
-  x[1] = bf16_hi(w.x);
-  x[2] = bf16_lo(w.y);
-  x[3] = bf16_hi(w.y);
+// Pairs of fp32 from four bf16 and back.
+__device__ __forceinline__ void wide(uint2 w, uint64_t& x, uint64_t& y) {
+  x = pair_of(bf16_lo(w.x), bf16_hi(w.x));
+  y = pair_of(bf16_lo(w.y), bf16_hi(w.y));
 }
-__device__ __forceinline__ uint2 bf16x4_of(const float (&x)[4]) {
-  return make_uint2(f32_to_bf16_bits(x[0]) | (static_cast<uint32_t>(f32_to_bf16_bits(x[1])) << 16),
-                    f32_to_bf16_bits(x[2]) | (static_cast<uint32_t>(f32_to_bf16_bits(x[3])) << 16));
+__device__ __forceinline__ uint32_t narrow(uint64_t x) {
+  float u, v;
+  unpair(x, u, v);
+  return pack_bf16x2(u, v);
+}
+__device__ __forceinline__ uint64_t neg_pair(uint64_t x) { return x ^ 0x8000000080000000ull; }
+
+// A row's two chunks of 4 as (first, second) elements of its pairs: they are
+// the chunks themselves when pairs lie apart, else neighbours.
+template <bool kNeighbours>
+__device__ __forceinline__ void split(uint64_t& x0, uint64_t& x1, uint64_t& y0, uint64_t& y1) {
+  if constexpr (kNeighbours) {
+    float a, b, c, d, e, f, g, h;
+    unpair(x0, a, b);
+    unpair(x1, c, d);
+    unpair(y0, e, f);
+    unpair(y1, g, h);
+    x0 = pair_of(a, c);
+    x1 = pair_of(e, g);
+    y0 = pair_of(b, d);
+    y1 = pair_of(f, h);
+  }
+}
+template <bool kNeighbours>
+__device__ __forceinline__ void join(uint64_t& x0, uint64_t& x1, uint64_t& y0, uint64_t& y1) {
+  if constexpr (kNeighbours) {
+    float a, b, c, d, e, f, g, h;
+    unpair(x0, a, b);
+    unpair(x1, c, d);
+    unpair(y0, e, f);
+    unpair(y1, g, h);
+    x0 = pair_of(a, e);
+    x1 = pair_of(b, f);
+    y0 = pair_of(c, g);
+    y1 = pair_of(d, h);
+  }
 }
 
-template <int kFlight>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+// f / 2 pi modulo 1 in units of 2^-64, to 2 of them for |f| < 2.
+__device__ __forceinline__ uint64_t turn_of(float f) {
+  const uint32_t u = __float_as_uint(f), e = (u >> 23) & 0xff;
+  uint64_t t;
+  if (e <= 127) {  // m 2^(e - 150) / 2 pi, m the 24 bits of f: one product by the 64 bits of 1 / 2 pi
+    const uint32_t m = e ? (u & 0x7fffffu) | 0x800000u : (u & 0x7fffffu) << 1;
+    constexpr uint64_t kInv = 0x28be60db9391054aull;  // 2^64 / 2 pi
+    const uint64_t lo = static_cast<uint64_t>(m) * static_cast<uint32_t>(kInv), hi = static_cast<uint64_t>(m) * static_cast<uint32_t>(kInv >> 32) + (lo >> 32);
+    const int s = 150 - static_cast<int>(e);  // 23 and more; the product is hi 2^32 + low half of lo
+    t = s < 32 ? (hi << (32 - s)) | (static_cast<uint32_t>(lo) >> s) : (s < 96 ? hi >> (s - 32) : 0ull);
+  } else {
+    double d = static_cast<double>(fabsf(f)) * 0.15915494309189533577;
+    d -= floor(d);
+    t = d < 1.0 ? static_cast<uint64_t>(d * 18446744073709551616.0) : 0ull;
+  }
+  return u >> 31 ? 0ull - t : t;
+}
+
+// blockIdx.y: the group of at most kHeads heads; 16 lanes take them for one
+// token, all rows loaded before any is used.
+template <int kHeads, bool kNeighbours>
+__global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 3 : 4) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   const int j = threadIdx.x & (kRowLanes - 1);
-  const int half = a.rot / 2;
   const bool turns = 8 * j < a.rot;
   // first elements of the lane's two chunks of 4
-  const bool apart = turns && !a.interleaved;
-  const int e0 = apart ? 4 * j : 8 * j, e1 = apart ? half + 4 * j : 8 * j + 4;
+  const bool apart = turns && !kNeighbours;
+  const int e0 = apart ? 4 * j : 8 * j, gap = apart ? a.rot / 2 : 4;
+  const bool key = static_cast<int>(blockIdx.y) >= a.side[0].groups;
+  const RopeSide& s = a.side[key];
+  const int h0 = (static_cast<int>(blockIdx.y) - (key ? a.side[0].groups : 0)) * kHeads, rows = min(kHeads, s.H - h0);
+  const int token = static_cast<int>(blockIdx.x) * (kRopeThreads / kRowLanes) + static_cast<int>(threadIdx.x) / kRowLanes;
+  const bool live = token < a.tokens;  // (the other half of the warp may be)
+  const int b = live ? token / a.n : 0, t = live ? token - b * a.n : 0;
+  const uint16_t* from = s.in + b * s.sb + t * s.st + h0 * s.sh + e0;
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  uint64_t turn[4] = {};  // inv_freq / 2 pi of pairs 4j .. 4j + 3, modulo 1
-  if (turns) {
+  uint2 x[kHeads], y[kHeads];
+  {
+    const int64_t sh = s.sh;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      double f = static_cast<double>(a.freq[4 * j + i]) * 0.15915494309189533577;
-      f -= floor(f);
-      turn[i] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0ull;
+    for (int k = 0; k < kHeads; ++k) {
+      x[k] = y[k] = make_uint2(0u, 0u);
+      if (live && k < rows) {
+        x[k] = *reinterpret_cast<const uint2*>(from);
+        y[k] = *reinterpret_cast<const uint2*>(from + gap);
+      }
+      from += sh;
     }
   }
-  const int groups = a.side[0].groups + a.side[1].groups;
-  const int64_t items = a.tokens * groups;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRopeThreads / kRowLanes);
-  const int upper = threadIdx.x / kRowLanes % 2;  // which half of the warp
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / kRowLanes) + threadIdx.x / kRowLanes;
-       it - upper < items; it += step) {
-    const bool live = it < items;  // the lower half may have rows when the upper has none
-    const int64_t token = (live ? it : 0) / groups;
-    int grp = static_cast<int>((live ? it : 0) - token * groups);
-    const int b = static_cast<int>(token / a.n), t = static_cast<int>(token - static_cast<int64_t>(b) * a.n);
-    const bool key = grp >= a.side[0].groups;
-    if (key) grp -= a.side[0].groups;
-    const RopeSide& s = a.side[key];
-    const int h0 = grp * a.heads, h1 = live ? min(h0 + a.heads, s.H) : h0;
-    const uint16_t* in = s.in + b * s.sb + t * s.st;
-    uint16_t* out = s.out + b * s.ob + t * s.ot;
-    uint2 x0[kFlight], x1[kFlight];
-    auto load = [&](int h) {
+  const bool norm = s.weight != nullptr;
+  const uint64_t one = pair_of(1.f, 1.f);
+  uint64_t p0 = one, p1 = one, q0 = one, q1 = one;  // the weight's elements of the pairs
+  if (norm) {
+    wide(*reinterpret_cast<const uint2*>(s.weight + e0), p0, p1);
+    wide(*reinterpret_cast<const uint2*>(s.weight + e0 + gap), q0, q1);
+    if (turns) split<kNeighbours>(p0, p1, q0, q1);
+  }
+  // (first, second) -> (first A - second B, second C + first D) times the row's norm
+  uint64_t A0 = p0, A1 = p1, B0 = 0, B1 = 0, C0 = q0, C1 = q1, D0 = 0, D1 = 0;
+  if (turns) {
+    const int32_t* pos = a.pos + b * a.pos_b + t;
+    float cs[4], sn[4];
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        x0[k] = x1[k] = make_uint2(0u, 0u);
-        if (h + k < h1) {
-          x0[k] = *reinterpret_cast<const uint2*>(in + (h + k) * s.sh + e0);
-          x1[k] = *reinterpret_cast<const uint2*>(in + (h + k) * s.sh + e1);
-        }
-      }
-    };
-    load(h0);
-    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {};
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = pos[a.axis[4 * j + i] * a.pos_axis];
+      const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(at) * turn_of(a.freq[4 * j + i])) >> 32);
+      // radians in [-pi, pi): the fast functions are off by 2^-21 there
+      __sincosf(static_cast<float>(frac) * 1.46291807926715968e-9f, &sn[i], &cs[i]);  // pi / 2^31
+    }
+    const uint64_t c0 = pair_of(cs[0], cs[1]), c1 = pair_of(cs[2], cs[3]), s0 = pair_of(sn[0], sn[1]), s1 = pair_of(sn[2], sn[3]);
+    A0 = mul_pair(p0, c0), A1 = mul_pair(p1, c1);
+    B0 = neg_pair(mul_pair(q0, s0)), B1 = neg_pair(mul_pair(q1, s1));
+    C0 = mul_pair(q0, c0), C1 = mul_pair(q1, c1);
+    D0 = mul_pair(p0, s0), D1 = mul_pair(p1, s1);
+  }
+  uint16_t* to = s.out + b * s.ob + t * s.ot + h0 * s.oh + e0;
+  const int64_t oh = s.oh;
+#pragma unroll
+  for (int k = 0; k < kHeads; ++k) {
+    uint64_t u0, u1, v0, v1;
+    wide(x[k], u0, u1);
+    wide(y[k], v0, v1);
+    if (norm) {
+      float lo, hi;
+      unpair(fma_pair(u0, u0, fma_pair(u1, u1, fma_pair(v0, v0, mul_pair(v1, v1)))), lo, hi);
+      float sum = lo + hi;
+#pragma unroll
+      for (int o = 1; o < kRowLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float f = rsqrtf(fmaf(sum, 1.f / kD, a.eps));
+      const uint64_t ff = pair_of(f, f);
+      u0 = mul_pair(u0, ff), u1 = mul_pair(u1, ff), v0 = mul_pair(v0, ff), v1 = mul_pair(v1, ff);
+    }
     if (turns) {
-      const int32_t* pos = a.pos + b * a.pos_b + t;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t p = pos[a.axis[4 * j + i] * a.pos_axis];
-        const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(p) * turn[i]) >> 32);
-        sincospif(static_cast<float>(frac) * 4.656612873077392578125e-10f, &sn[i], &cs[i]);  // 2^-31: half turns
-      }
+      split<kNeighbours>(u0, u1, v0, v1);
+      const uint64_t w0 = fma_pair(u0, A0, mul_pair(v0, B0)), w1 = fma_pair(u1, A1, mul_pair(v1, B1));
+      v0 = fma_pair(v0, C0, mul_pair(u0, D0)), v1 = fma_pair(v1, C1, mul_pair(u1, D1));
+      u0 = w0, u1 = w1;
+      join<kNeighbours>(u0, u1, v0, v1);
+    } else if (norm) {
+      u0 = mul_pair(u0, p0), u1 = mul_pair(u1, p1), v0 = mul_pair(v0, q0), v1 = mul_pair(v1, q1);
     }
-    float w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
-    if (s.weight) {
-      bf16x4(*reinterpret_cast<const uint2*>(s.weight + e0), w0);
-      bf16x4(*reinterpret_cast<const uint2*>(s.weight + e1), w1);
+    if (live && k < rows) {
+      *reinterpret_cast<uint2*>(to) = make_uint2(narrow(u0), narrow(u1));
+      *reinterpret_cast<uint2*>(to + gap) = make_uint2(narrow(v0), narrow(v1));
     }
-    const int rounds = (a.heads + kFlight - 1) / kFlight;  // the same for both halves of a warp
-    for (int r = 0; r < rounds; ++r) {
-      const int h = h0 + r * kFlight;
-      if (r > 0) load(h);
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        float u[4], v[4];
-        bf16x4(x0[k], u);
-        bf16x4(x1[k], v);
-        if (a.side[0].weight || a.side[1].weight) {
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum = fmaf(u[i], u[i], fmaf(v[i], v[i], sum));
-#pragma unroll
-          for (int o = 1; o < kRowLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float f = s.weight ? rsqrtf(fmaf(sum, 1.f / kD, a.eps)) : 1.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u[i] *= f * w0[i];
-            v[i] *= f * w1[i];
-          }
-        }
-        if (turns) {
-          if (a.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float p = u[2 * i], q = u[2 * i + 1];
-              u[2 * i] = p * cs[i] - q * sn[i];
-              u[2 * i + 1] = q * cs[i] + p * sn[i];
-              const float y = v[2 * i], z = v[2 * i + 1];
-              v[2 * i] = y * cs[2 + i] - z * sn[2 + i];
-              v[2 * i + 1] = z * cs[2 + i] + y * sn[2 + i];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p = u[i], q = v[i];
-              u[i] = p * cs[i] - q * sn[i];
-              v[i] = q * cs[i] + p * sn[i];
-            }
-          }
-        }
-        if (h + k < h1) {
-          *reinterpret_cast<uint2*>(out + (h + k) * s.oh + e0) = bf16x4_of(u);
-          *reinterpret_cast<uint2*>(out + (h + k) * s.oh + e1) = bf16x4_of(v);
-        }
-      }
-    }
+    to += oh;
   }
 }
 
@@ -267,6 +300,7 @@ extern "C" kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R,
   if (q && k && (kvq::rows_meet(*q_out, H[0], *k, H[1], B, n_tok) || kvq::rows_meet(*q, H[0], *k_out, H[1], B, n_tok) ||
                  kvq::rows_meet(*q_out, H[0], *k_out, H[1], B, n_tok)))
     return KVQ_ERR_INVALID_ARG;
+  if (B * n_tok > 0x7ff00000LL) return KVQ_ERR_UNSUPPORTED;  // (past the last token by a stride of the grid)
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
   a.pos = pos;
@@ -275,26 +309,33 @@ extern "C" kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R,
   a.freq = inv_freq;
   a.eps = eps;
   a.n = n_tok;
+  a.tokens = static_cast<int32_t>(B * n_tok);
   a.rot = R->rot_dim;
-  a.interleaved = R->interleaved != 0;
-  a.tokens = B * n_tok;
   for (int i = 0; i < R->rot_dim / 2; ++i) a.axis[i] = R->axis[i];
-  // Few rows: one a lane group, for latency; else as many as share the angles well.
-  const int64_t rows = a.tokens * (H[0] + H[1]);
+  // Heads a lane group: one when there are few rows, for latency (one token of 32
+  // heads 2.1 us, 2.8 with 8), else 8 to share the angles (16 x 26 tokens of 64
+  // heads 5.0 us, 5.4 with 4, 8.6 with 1; 8 x 2940 of 80: 162, 184, 549).
+  const int64_t rows = static_cast<int64_t>(a.tokens) * (H[0] + H[1]);
   const int64_t resident = static_cast<int64_t>(n_sm) * 1024 / kvq::kRowLanes;
-  a.heads = rows <= resident ? 1 : (rows <= 4 * resident ? 4 : 8);
+  const int heads = rows <= resident ? 1 : (rows <= 2 * resident ? 4 : 8);
   const void* weights[2] = {q_weight, k_weight};
   for (int i = 0; i < 2; ++i) {
     kvq::RopeSide& s = a.side[i];
     if (!in[i]) continue;
     s = {static_cast<const uint16_t*>(in[i]->data), static_cast<uint16_t*>(out[i]->data),
          in[i]->stride_b, in[i]->stride_h, in[i]->stride_t, out[i]->stride_b, out[i]->stride_h, out[i]->stride_t,
-         static_cast<const uint16_t*>(weights[i]), H[i], (H[i] + a.heads - 1) / a.heads};
+         static_cast<const uint16_t*>(weights[i]), H[i], (H[i] + heads - 1) / heads};
   }
-  const int64_t items = a.tokens * (a.side[0].groups + a.side[1].groups);
+  const int groups = a.side[0].groups + a.side[1].groups;
+  if (groups > 65535) return KVQ_ERR_UNSUPPORTED;
   const int64_t per = kvq::kRopeThreads / kvq::kRowLanes;
-  const int64_t grid = std::min<int64_t>((items + per - 1) / per, static_cast<int64_t>(n_sm) * 32);
-  const void* fn = a.heads == 1 ? reinterpret_cast<const void*>(&kvq::norm_rope_kernel<1>)
-                                : reinterpret_cast<const void*>(&kvq::norm_rope_kernel<4>);
-  return kvq::launch_dependent(fn, dim3(static_cast<unsigned>(grid)), kvq::kRopeThreads, 0, stream, &a);
+  const int64_t grid = (a.tokens + per - 1) / per;
+  auto kernel = [&](auto pair) -> const void* {
+    constexpr bool kPair = decltype(pair)::value;
+    if (heads == 1) return reinterpret_cast<const void*>(&kvq::norm_rope_kernel<1, kPair>);
+    if (heads == 4) return reinterpret_cast<const void*>(&kvq::norm_rope_kernel<4, kPair>);
+    return reinterpret_cast<const void*>(&kvq::norm_rope_kernel<8, kPair>);
+  };
+  const void* fn = R->interleaved ? kernel(std::true_type()) : kernel(std::false_type());
+  return kvq::launch_dependent(fn, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(groups)), kvq::kRopeThreads, 0, stream, &a);
 }

@@ -124,13 +124,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// fp32 (lo, hi) -> bf16x2 with lo in bits 0-15, round to nearest even.
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
 // 8 NT query columns as MMA operands: fp16 with a power of two of each
 // column's own (its largest element lands in [2^8, 2^9), so that the others are
 // exact down to 2^-25 of it), and bf16 as stored.
