@@ -19,16 +19,19 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
   if (n_sink < 0 || window < 1 || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
   if (T > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;
   const int64_t cols = static_cast<int64_t>(L->g) * n_q;
-  const int nt = cols > 8 ? 2 : 1;
-  const int64_t nblk = (cols + 8 * nt - 1) / (8 * nt);
+  kvq::win::Form f;
+  f.nt = cols > 8 ? 2 : 1;
+  const int64_t nblk = (cols + 8 * f.nt - 1) / (8 * f.nt);
   const int64_t units = static_cast<int64_t>(L->d.B) * L->d.H_kv * nblk;
-  if (units > 0x7ffffff || cols > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;  // 16 CTAs a unit at most
+  if (units > 0x3ffffff || cols > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;  // 16 CTAs a unit at most
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
-  const kvq::win::Kernel k = L->d.k_bits == 2   ? kvq::win::window_kernel_k2(L->d.v_bits, L->d.group_size, nt)
-                             : L->d.k_bits == 4 ? kvq::win::window_kernel_k4(L->d.v_bits, L->d.group_size, nt)
-                             : L->d.k_bits == 8 ? kvq::win::window_kernel_k8(L->d.v_bits, L->d.group_size, nt)
-                                                : kvq::win::window_kernel_k16(L->d.v_bits, L->d.group_size, nt);
+  // Units enough for every SM: small CTAs, one a unit; else more warps a CTA.
+  f.warps = f.nt == 2 || units >= 2 * n_sm ? 4 : 8;
+  const kvq::win::Kernel k = L->d.k_bits == 2   ? kvq::win::window_kernel_k2(L->d.v_bits, L->d.group_size, f)
+                             : L->d.k_bits == 4 ? kvq::win::window_kernel_k4(L->d.v_bits, L->d.group_size, f)
+                             : L->d.k_bits == 8 ? kvq::win::window_kernel_k8(L->d.v_bits, L->d.group_size, f)
+                                                : kvq::win::window_kernel_k16(L->d.v_bits, L->d.group_size, f);
   if (!k.fn) return KVQ_ERR_UNSUPPORTED;
   st = kvq_allow_clusters(k.fn, k.smem);
   if (st != KVQ_OK) return st;
@@ -45,13 +48,41 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
   a.lse = lse;
   a.nblk = static_cast<int32_t>(nblk);
   int h = 0;
-  for (int i = 0; i < L->n_prot; ++i) a.head[h++] = L->prot_head[i];
-  for (int i = 0; i < L->n_konly; ++i) a.head[h++] = L->konly_head[i];
-  for (int i = 0; i < L->n_packed; ++i) a.head[h++] = L->packed_head[i];
-  // CTAs a unit: one wave of resident ones, none without a block for its warps.
+  const int n_heads[3] = {L->n_prot, L->n_konly, L->n_packed};
+  const uint8_t* heads[3] = {L->prot_head, L->konly_head, L->packed_head};
+  for (int k = 0; k < 3; ++k) {
+    a.head0[k] = static_cast<uint8_t>(h);
+    for (int i = 0; i < n_heads[k]; ++i) a.head[h++] = heads[k][i];
+    a.U[k] = static_cast<int32_t>(static_cast<int64_t>(L->d.B) * n_heads[k] * nblk);
+  }
+  // CTAs a unit: those of the class with the longest share double while one
+  // wave holds them all and no CTA is without a block for its warps.  A row costs
+  // its bytes and some work (kPosCost); the longest call counts.
   const int64_t rows = std::min<int64_t>(T, static_cast<int64_t>(a.n_sink) + a.window + n_q - 1);
-  const int64_t wave = static_cast<int64_t>(n_sm) * (nt == 1 ? 2 : 1);
-  int ranks = 1;
-  while (ranks < kvq::win::kMaxRanks && 2 * ranks * units <= wave && ranks * kvq::win::kWarps * 16 < rows) ranks *= 2;
-  return kvq::launch_clusters(k.fn, dim3(static_cast<unsigned>(units * ranks)), ranks, kvq::win::kThreads, k.smem, stream, &a);
+  const int64_t vis = std::min<int64_t>(rows, L->Tv), v = L->row_bytes[KVQ_SEG_V_CODES] + L->row_bytes[KVQ_SEG_V_SZ];
+  const int64_t text = (rows - vis) * kvq::kBf16PosCost;
+  const int64_t cost[3] = {text + vis * kvq::kBf16PosCost, text + vis * (kvq::kRowBytes + v + kvq::kPosCost),
+                           text + vis * (L->row_bytes[KVQ_SEG_K_CODES] + L->row_bytes[KVQ_SEG_K_SZ] + v + kvq::kPosCost)};
+  const int64_t wave = static_cast<int64_t>(n_sm) * (f.warps == 4 ? 3 : 2);
+  int S[3] = {1, 1, 1};
+  for (;;) {
+    int worst = -1;
+    for (int k = 0; k < 3; ++k)
+      if (a.U[k] && (worst < 0 || cost[k] * S[worst] > cost[worst] * S[k])) worst = k;
+    if (worst < 0 || S[worst] >= kvq::win::kMaxRanks || S[worst] * f.warps * 16 >= rows) break;
+    int64_t used = 0;
+    for (int k = 0; k < 3; ++k) used += static_cast<int64_t>(a.U[k]) * S[k] * (k == worst ? 2 : 1);
+    if (used > wave) break;
+    S[worst] *= 2;
+  }
+  a.cluster = std::max({S[0], S[1], S[2]});
+  int64_t grid = 0;
+  for (int k = 0; k < 3; ++k) {
+    a.lg[k] = 0;
+    while (1 << a.lg[k] < S[k]) ++a.lg[k];
+    a.first[k] = static_cast<int32_t>(grid);
+    grid += (static_cast<int64_t>(a.U[k]) * S[k] + a.cluster - 1) / a.cluster * a.cluster;
+  }
+  return kvq::launch_clusters(k.fn, dim3(static_cast<unsigned>(grid)), a.cluster, 32 * f.warps,
+                              a.cluster > 1 ? k.smem : k.alone, stream, &a);
 }

@@ -8,8 +8,10 @@
 // A unit is a (sequence, KV head) and up to 8 NT of its (token, query head)
 // columns.  The rows that its tokens attend, [0, n_sink) and [lo, len), are cut
 // into blocks of 16 or 32 rows of one kind (bf16 text, visual), which the warps
-// of the unit's thread-block cluster take in turn: text blocks first, so that a
-// warp's accumulator changes to packed rows once.  Every warp streams its blocks
+// of the unit's CTAs take in turn: text blocks first, so that a warp's
+// accumulator changes to packed rows once.  A thread-block cluster holds the CTAs
+// of one or more units: units of heads that keep bf16 rows get more of them than
+// those of packed heads.  Every warp streams its blocks
 // through a ring of its own in shared memory (cp.async, K and V rows as separate
 // pieces, so that V and the next K are under way while a block's scores are
 // made), and runs an online softmax of its own.  The warps meet in shared
@@ -31,6 +33,8 @@
 // batches, for small ones the chain of a warp's few blocks and the two meetings.
 #pragma once
 
+#include <cstddef>
+
 #include "kvq_split.cuh"
 
 #include "kvq_geom.cuh"
@@ -39,8 +43,6 @@
 namespace kvq {
 namespace win {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kPiece = 4096;  // bytes of a ring slot: 16 bf16 rows
 constexpr int kSlots = 3;
 constexpr int kMaxRanks = 16;
@@ -56,15 +58,21 @@ struct Args {
   uint16_t* out;
   float* lse;
   int32_t nblk;  // column blocks of a (sequence, KV head)
-  uint8_t head[KVQ_MAX_HEADS];  // protected heads first: their rows are the longest
+  // Units of class k (0 both bf16, 1 K bf16, 2 packed): U[k], of 2^lg[k] CTAs
+  // each; the grid's CTAs from first[k] on, whole clusters.
+  int32_t U[3], lg[3], first[3], cluster;
+  uint8_t head[KVQ_MAX_HEADS];  // heads of the classes in order
+  uint8_t head0[3];             // where a class begins among them
 };
 
-template <int NT>
+// W warps a CTA, NT tiles of 8 columns.
+template <int NT, int W>
 struct Smem {
-  alignas(128) uint8_t ring[kWarps][kSlots * kPiece];
+  alignas(128) uint8_t ring[W][kSlots * kPiece];
   Columns<NT> col;
   int32_t at[NT * 8];  // position of a column's token (-1: none)
-  float ml[kWarps][NT * 8][2];
+  float ml[W][NT * 8][2];
+  // (units of several CTAs only)
   float4 recv[NT * 256];                        // [rank][its share of the unit's 8 NT x D outputs]
   float2 recv_ml[kMaxRanks][NT * 8];
 };
@@ -112,18 +120,118 @@ __device__ __forceinline__ void copy_packed(uint8_t* to, const uint8_t* codes, c
 }
 
 // PV of 16 bf16 rows of a piece: the weights of a column as high and low bf16.
-__device__ __forceinline__ void pv_bf16(const uint8_t* vc, const float (&P)[4], int lane, Acc& acc) {
-  const uint32_t h0 = pack_bf16x2(P[0], P[1]), h1 = pack_bf16x2(P[2], P[3]);
-  const uint32_t l0 = pack_bf16x2(P[0] - bf16_lo(h0), P[1] - bf16_hi(h0)), l1 = pack_bf16x2(P[2] - bf16_lo(h1), P[3] - bf16_hi(h1));
-  const uint32_t b0 = movmatrix_trans(h0), b1 = movmatrix_trans(h1), c0 = movmatrix_trans(l0), c1 = movmatrix_trans(l1);
+template <int NT, typename Weights>
+__device__ __forceinline__ void pv_bf16(const uint8_t* vc, Weights&& P, int lane, Acc (&acc)[NT]) {
+  uint32_t b[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float* w = P(t);
+    const uint32_t h0 = pack_bf16x2(w[0], w[1]), h1 = pack_bf16x2(w[2], w[3]);
+    b[t][0] = movmatrix_trans(h0);
+    b[t][1] = movmatrix_trans(h1);
+    b[t][2] = movmatrix_trans(pack_bf16x2(w[0] - bf16_lo(h0), w[1] - bf16_hi(h0)));
+    b[t][3] = movmatrix_trans(pack_bf16x2(w[2] - bf16_lo(h1), w[3] - bf16_hi(h1)));
+  }
   const int row = (lane & 7) + ((lane >> 4) & 1) * 8, chunk = (lane >> 3) & 1;
   const uint8_t* base = vc + row * kRowBytes;
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
     uint32_t A[4];
     ldsm_x4_trans(base + (((2 * m + chunk) ^ swz_v(row)) << 4), A);
-    mma_bf16(acc.o[m], A, b0, b1);
-    mma_bf16(acc.o[m], A, c0, c1);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      mma_bf16(acc[t].o[m], A, b[t][0], b[t][1]);
+      mma_bf16(acc[t].o[m], A, b[t][2], b[t][3]);
+    }
+  }
+}
+
+// PV of 16 packed rows (pv_packed of the split kernel, the unpacked codes
+// shared by the tiles): per group the scales meet the weights, the zero points
+// have an MMA of their own.
+template <int VB, int G, int NT, typename Weights>
+__device__ __forceinline__ void pv_packed_rows(const uint8_t* vc, const uint8_t* vsz, int r0, Weights&& P, int gid, int tig, Acc (&acc)[NT]) {
+  constexpr int kRow = 16 * VB, kSlice = 2 * VB, NG = kD / G, kSz = 4 * NG;
+  const int row[4] = {r0 + 2 * tig, r0 + 2 * tig + 1, r0 + 2 * tig + 8, r0 + 2 * tig + 9};
+  uint32_t sz[4][(2 * NG + 1) / 2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t* p = vsz + row[i] * kSz;
+    if constexpr (NG == 4) {
+      const uint4 a = lds128(p);
+      sz[i][0] = a.x, sz[i][1] = a.y, sz[i][2] = a.z, sz[i][3] = a.w;
+    } else if constexpr (NG == 2) {
+      const uint2 a = lds64(p);
+      sz[i][0] = a.x, sz[i][1] = a.y;
+    } else {
+      sz[i][0] = lds32(p);
+    }
+  }
+  // fp16 halves: z_g at half g, s_g at half NG + g
+  auto half_of = [](int h) { return (h & 1) ? 0x7632u : 0x5410u; };
+  uint32_t b0[NT][NG], b1[NT][NG], pb[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float* w = P(t);
+    pb[t][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+    pb[t][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+  }
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int hs = NG + g;
+    const uint32_t sa = prmt(sz[0][hs >> 1], sz[1][hs >> 1], half_of(hs)), sc = prmt(sz[2][hs >> 1], sz[3][hs >> 1], half_of(hs));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      b0[t][g] = hmul2_u(pb[t][0], sa);
+      b1[t][g] = hmul2_u(pb[t][1], sc);
+    }
+  }
+  {  // zero points: rows = groups
+    uint32_t za = 0u, zc = 0u;
+    if (gid < NG) {
+      const bool up = NG == 4 && gid >= 2;
+      za = prmt(up ? sz[0][NG / 4] : sz[0][0], up ? sz[1][NG / 4] : sz[1][0], half_of(gid));
+      zc = prmt(up ? sz[2][NG / 4] : sz[2][0], up ? sz[3][NG / 4] : sz[3][0], half_of(gid));
+    }
+    const uint32_t Z[4] = {za, 0u, zc, 0u};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mma_f16(acc[t].zo, Z, pb[t][0], pb[t][1]);
+  }
+  constexpr int kWords = VB / 2;  // of a lane's slice
+  uint32_t cw[4][kWords];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t* p = vc + row[i] * kRow + kSlice * gid;
+    if constexpr (VB == 2) {
+      cw[i][0] = lds32(p);
+    } else if constexpr (VB == 4) {
+      const uint2 a = lds64(p);
+      cw[i][0] = a.x, cw[i][1] = a.y;
+    } else {
+      const uint4 a = lds128(p);
+      cw[i][0] = a.x, cw[i][1] = a.y, cw[i][2] = a.z, cw[i][3] = a.w;
+    }
+  }
+  constexpr int kTiles = 8 / VB;  // m-tiles of a half-word (one of 8 bits)
+#pragma unroll
+  for (int h = 0; h < VB; ++h) {  // half-words of the slice
+    const uint32_t xa = prmt(cw[0][h >> 1], cw[1][h >> 1], half_of(h)), xc = prmt(cw[2][h >> 1], cw[3][h >> 1], half_of(h));
+    const uint32_t ya = VB == 2 ? (xa >> 6) : (xa >> 8), yc = VB == 2 ? (xc >> 6) : (xc >> 8);
+#pragma unroll
+    for (int mm = 0; mm < kTiles; ++mm) {
+      const int m = h * kTiles + mm;
+      uint32_t A[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int c = 2 * mm + r;  // code of the half-word
+        const bool hi = VB == 2 ? (c >= 5) : (VB == 4 ? (c >= 2) : (c >= 1));
+        const uint32_t mask = (VB == 2 ? 0x00030003u : (VB == 4 ? 0x000F000Fu : 0x00FF00FFu)) << kVShift<VB>(m, r);
+        A[r] = (hi ? ya : xa) & mask;
+        A[2 + r] = (hi ? yc : xc) & mask;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma_f16(acc[t].o[m], A, b0[t][(16 * m) / G], b1[t][(16 * m) / G]);
+    }
   }
 }
 
@@ -134,24 +242,28 @@ struct Block {
   bool visual;
 };
 
-template <int KB, int VB, int G, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_kernel(const __grid_constant__ Args a) {
+template <int KB, int VB, int G, int NT, int W>
+__global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>(smem_raw);
+  Smem<NT, W>& sm = *reinterpret_cast<Smem<NT, W>*>(smem_raw);
+  constexpr int kWarps = W, kThreads = 32 * W;
   const Geom& p = a.c;
   constexpr int kKRow = KB < 16 ? 16 * KB : kRowBytes, kVRow = VB < 16 ? 16 * VB : kRowBytes;
   constexpr int kKSz = KB < 16 ? 4 * kD / G : 0, kVSz = VB < 16 ? 4 * kD / G : 0;
   // rows of a block whose K and V are both packed
   constexpr int kRB = 32 * (kKRow + kKSz) <= kPiece && 32 * (kVRow + kVSz) <= kPiece ? 32 : 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const int rank = static_cast<int>(cluster_ctarank()), ranks = static_cast<int>(cluster_nctarank());
-  const int unit = blockIdx.x / ranks, cb = unit % a.nblk, hb = unit / a.nblk;
-  const int h = a.head[hb / p.B], b = hb % p.B;
+  const int cta = blockIdx.x, cls = cta >= a.first[2] ? 2 : (cta >= a.first[1] ? 1 : 0);
+  const int lg = a.lg[cls], ranks = 1 << lg, unit = (cta - a.first[cls]) >> lg, rank = (cta - a.first[cls]) & (ranks - 1);
+  const bool idle = unit >= a.U[cls];  // (fills a cluster)
+  const int hb = a.nblk == 1 ? unit : unit / a.nblk, cb = unit - hb * a.nblk;
+  const int hi = p.B == 1 ? hb : hb / p.B, b = hb - hi * p.B;
+  const int h = idle ? 0 : a.head[a.head0[cls] + hi];
   cluster_arrive();  // waited for before the first store to another CTA
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();  // this kernel writes no cache row
   int len = a.seq_len ? a.seq_len[b] : a.T;
-  if (len < 0 || len > a.T) len = 0;
+  if (len < 0 || len > a.T || idle) len = 0;
   const int p0 = len - a.n_q;  // position of token 0
   const HeadRows hr = head_rows(p, b, h);
   const bool kpk = KB < 16 && hr.k_packed, vpk = VB < 16 && hr.v_packed;
@@ -395,17 +507,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_kernel(const
 #pragma unroll
         for (int hf = 0; hf < kRB / 16; ++hf)
           if (16 * hf < rb) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              pv_packed<VB, G>(vc, vc + rb * kVRow, 16 * hf, kNoLimit, movmatrix_trans(pack_f16x2(S[t][hf][0], S[t][hf][1])),
-                               movmatrix_trans(pack_f16x2(S[t][hf][2], S[t][hf][3])), gid, tig, acc[t]);
+            pv_packed_rows<VB, G, NT>(vc, vc + rb * kVRow, 16 * hf, [&](int t) { return S[t][hf]; }, gid, tig, acc);
           }
       }
     }
-    if (!v_is_packed) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) pv_bf16(vc, S[t][0], lane, acc[t]);
-    }
+    if (!v_is_packed) pv_bf16<NT>(vc, [&](int t) { return S[t][0]; }, lane, acc);
     now = then;
     slot = slot_n;
   }
@@ -428,6 +534,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_kernel(const
     }
   }
   __syncthreads();
+  // a column's reference and sum over the CTA's warps
+  auto cta_ml = [&](int c) {
+    float M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][c][0]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l += sm.ml[w][c][1] * ex2(sm.ml[w][c][0] - (M == -INFINITY ? 0.f : M));
+    return make_float2(M, l);
+  };
+  auto put = [&](int t, int c, int d4, const float4& o, float M, float l) {
+    const int cg = (cb * NT + t) * 8 + c, tok = cg / p.g;
+    if (idle || tok >= a.n_q) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing attended: 0 (NaN stays)
+    const int64_t row = (static_cast<int64_t>(b) * a.n_q + tok) * p.Hq + h * p.g + (cg - tok * p.g);
+    reinterpret_cast<uint2*>(a.out + row * kD)[d4] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (d4 == 0 && a.lse) a.lse[row] = 0.69314718055994531f * (M + log2f(l));
+  };
+  const uint32_t base = cluster_ctarank() - rank;  // of the unit's CTAs in the cluster
 #pragma unroll 1
   for (int t = 0; t < NT; ++t) {  // (a warp's ring holds one tile's rows)
     float* mine = reinterpret_cast<float*>(ring);
@@ -450,98 +574,106 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_kernel(const
       }
     }
     __syncthreads();
-    // thread (column, quad of d): the CTA's sum, sent to the rank that writes it
-    const int c = threadIdx.x >> 5, d4 = threadIdx.x & 31;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    // (column, quad of d) of the CTA: written here, or sent to the rank that writes it
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + c * kPitch + 4 * d4);
-      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    for (int quad = threadIdx.x; quad < 256; quad += kThreads) {
+      const int c = quad >> 5, d4 = quad & 31;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + c * kPitch + 4 * d4);
+        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+      }
+      if (ranks == 1) {
+        const float2 ml = cta_ml(8 * t + c);
+        put(t, c, d4, s, ml.x, ml.y);
+      } else {
+        // outputs of a tile are shared out over the ranks: 256 / ranks quads each
+        if (t == 0 && quad == static_cast<int>(threadIdx.x)) cluster_wait();  // every CTA of the cluster has started
+        const int share = 256 >> lg, to = quad >> (8 - lg), at = quad & (share - 1);
+        const uint32_t addr = dsmem_addr(&sm.recv[t * 256 + rank * share + at], base + to);
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(s.x), "f"(s.y), "f"(s.z), "f"(s.w) : "memory");
+      }
     }
-    if (t == 0) cluster_wait();  // every CTA of the cluster has started
-    // outputs of a tile are shared out over the ranks: 256 / ranks quads each
-    const int share = 256 / ranks, to = threadIdx.x / share, at = threadIdx.x - to * share;
-    const uint32_t addr = dsmem_addr(&sm.recv[t * 256 + rank * share + at], to);
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(s.x), "f"(s.y), "f"(s.z), "f"(s.w) : "memory");
-    __syncthreads();  // the rings are written anew
+    if (t + 1 < NT) __syncthreads();  // the rings are written anew
   }
-  if (threadIdx.x < NT * 8 * ranks) {
-    const int to = threadIdx.x / (NT * 8), c = threadIdx.x - to * (NT * 8);
-    float M = -INFINITY, l = 0.f;
+  if (ranks == 1) {
+    cluster_wait();
+    if (a.cluster > 1) cluster_sync();  // (other units' CTAs meet there)
+    return;
+  }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][c][0]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) l += sm.ml[w][c][1] * ex2(sm.ml[w][c][0] - (M == -INFINITY ? 0.f : M));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dsmem_addr(&sm.recv_ml[rank][c], to)), "f"(M), "f"(l) : "memory");
+  for (int x = threadIdx.x; x < NT * 8 * ranks; x += kThreads) {
+    const int to = x / (NT * 8), c = x - to * (NT * 8);
+    const float2 ml = cta_ml(c);
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dsmem_addr(&sm.recv_ml[rank][c], base + to)), "f"(ml.x), "f"(ml.y) : "memory");
   }
   cluster_sync();
   // lane r of a group of `ranks` has rank r's part of a quad
-  const int share = 256 / ranks, src = threadIdx.x % ranks, at = threadIdx.x / ranks;
+  const int share = 256 >> lg, src = threadIdx.x & (ranks - 1);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int quad = rank * share + at, c = quad >> 5, d4 = quad & 31;
-    const float2 ml = sm.recv_ml[src][8 * t + c];
-    float4 o = sm.recv[t * 256 + src * share + at];
-    float M = ml.x;
-    for (int x = 1; x < ranks; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
-    float l = ml.y * f;
-    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-    for (int x = 1; x < ranks; x <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, x);
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
-      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
-      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+  for (int t = 0; t < NT; ++t)
+    for (int at = threadIdx.x >> lg; at < share; at += kThreads >> lg) {
+      const int quad = rank * share + at, c = quad >> 5, d4 = quad & 31;
+      const float2 ml = sm.recv_ml[src][8 * t + c];
+      float4 o = sm.recv[t * 256 + src * share + at];
+      float M = ml.x;
+      for (int x = 1; x < ranks; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+      float l = ml.y * f;
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+      for (int x = 1; x < ranks; x <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, x);
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+      }
+      if (src == 0) put(t, c, d4, o, M, l);
     }
-    const int cg = (cb * NT + t) * 8 + c, tok = cg / p.g;
-    if (src == 0 && tok < a.n_q) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing attended: 0 (NaN stays)
-      const int64_t row = (static_cast<int64_t>(b) * a.n_q + tok) * p.Hq + h * p.g + (cg - tok * p.g);
-      uint2 w;
-      w.x = pack_bf16x2(o.x * inv, o.y * inv);
-      w.y = pack_bf16x2(o.z * inv, o.w * inv);
-      reinterpret_cast<uint2*>(a.out + row * kD)[d4] = w;
-      if (d4 == 0 && a.lse) a.lse[row] = 0.69314718055994531f * (M + log2f(l));
-    }
-  }
 }
 
 struct Kernel {
   const void* fn;
-  int smem, nt;
+  int smem, alone;  // alone: shared memory of units of one CTA
 };
+struct Form {
+  int nt, warps;  // tiles of 8 columns (1 or 2); warps a CTA (4 or 8; 4 with two tiles)
+};
+template <int KB, int VB, int G, int NT, int W>
+Kernel kernel_with() {
+  using S = Smem<NT, W>;
+  return {reinterpret_cast<const void*>(&window_kernel<KB, VB, G, NT, W>), static_cast<int>(sizeof(S)), static_cast<int>(offsetof(S, recv))};
+}
 template <int KB, int VB, int G>
-Kernel kernel_of(int nt) {
-  return nt == 1 ? Kernel{reinterpret_cast<const void*>(&window_kernel<KB, VB, G, 1>), static_cast<int>(sizeof(Smem<1>)), 1}
-                 : Kernel{reinterpret_cast<const void*>(&window_kernel<KB, VB, G, 2>), static_cast<int>(sizeof(Smem<2>)), 2};
+Kernel kernel_of(Form f) {
+  return f.nt == 2 ? kernel_with<KB, VB, G, 2, 4>() : (f.warps == 4 ? kernel_with<KB, VB, G, 1, 4>() : kernel_with<KB, VB, G, 1, 8>());
 }
 template <int KB, int VB>
-Kernel kernel_of(int G, int nt) {
-  if constexpr (KB == 16 && VB == 16) return kernel_of<16, 16, 128>(nt);
+Kernel kernel_of(int G, Form f) {
+  if constexpr (KB == 16 && VB == 16) return kernel_of<16, 16, 128>(f);
   switch (G) {
-    case 32: return kernel_of<KB, VB, 32>(nt);
-    case 64: return kernel_of<KB, VB, 64>(nt);
-    case 128: return kernel_of<KB, VB, 128>(nt);
+    case 32: return kernel_of<KB, VB, 32>(f);
+    case 64: return kernel_of<KB, VB, 64>(f);
+    case 128: return kernel_of<KB, VB, 128>(f);
   }
   return {nullptr, 0, 0};
 }
 template <int KB>
-Kernel kernel_of(int vb, int G, int nt) {
+Kernel kernel_of(int vb, int G, Form f) {
   switch (vb) {
-    case 2: return kernel_of<KB, 2>(G, nt);
-    case 4: return kernel_of<KB, 4>(G, nt);
-    case 8: return kernel_of<KB, 8>(G, nt);
-    case 16: return kernel_of<KB, 16>(G, nt);
+    case 2: return kernel_of<KB, 2>(G, f);
+    case 4: return kernel_of<KB, 4>(G, f);
+    case 8: return kernel_of<KB, 8>(G, f);
+    case 16: return kernel_of<KB, 16>(G, f);
   }
   return {nullptr, 0, 0};
 }
-// The kernel for (k_bits, v_bits, G) and nt tiles of 8 columns: one translation
-// unit for each width of K.
-Kernel window_kernel_k2(int vb, int G, int nt);
-Kernel window_kernel_k4(int vb, int G, int nt);
-Kernel window_kernel_k8(int vb, int G, int nt);
-Kernel window_kernel_k16(int vb, int G, int nt);
+// The kernel for (k_bits, v_bits, G): one translation unit for each width of K.
+Kernel window_kernel_k2(int vb, int G, Form f);
+Kernel window_kernel_k4(int vb, int G, Form f);
+Kernel window_kernel_k8(int vb, int G, Form f);
+Kernel window_kernel_k16(int vb, int G, Form f);
 
 }  // namespace win
 }  // namespace kvq

@@ -3,6 +3,6 @@
 
 namespace kvq {
 namespace win {
-Kernel window_kernel_k2(int vb, int G, int nt) { return kernel_of<2>(vb, G, nt); }
+Kernel window_kernel_k2(int vb, int G, Form f) { return kernel_of<2>(vb, G, f); }
 }  // namespace win
 }  // namespace kvq

@@ -3,6 +3,6 @@
 
 namespace kvq {
 namespace win {
-Kernel window_kernel_k4(int vb, int G, int nt) { return kernel_of<4>(vb, G, nt); }
+Kernel window_kernel_k4(int vb, int G, Form f) { return kernel_of<4>(vb, G, f); }
 }  // namespace win
 }  // namespace kvq
