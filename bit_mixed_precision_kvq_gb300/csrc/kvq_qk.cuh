@@ -241,6 +241,12 @@ __device__ __forceinline__ void qk_packed_rows(const uint8_t* kc, const uint8_t*
     h2_to_f2(b.sz.x, z, s1[0]);
   }
   const float kf = pow2i(24 - kLiftQ - k_first_shift<KB>());
+  uint64_t s0p[NG], s1p[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    s0p[g] = pair_of(s0[g] * kf, s0[g] * kf);
+    s1p[g] = pair_of(s1[g] * kf, s1[g] * kf);
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float C[NG][4], S[4];
@@ -255,19 +261,15 @@ __device__ __forceinline__ void qk_packed_rows(const uint8_t* kc, const uint8_t*
     }
     const uint32_t Z[4] = {za, zc, 0u, 0u};
     mma_f16_new(S, Z, sm.zb[t][lane], 0u);
+    uint64_t x0 = pair_of(S[0], S[1]), x1 = pair_of(S[2], S[3]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const float u = s0[g] * kf, v = s1[g] * kf;
-      S[0] = fmaf(u, C[g][0], S[0]);
-      S[1] = fmaf(u, C[g][1], S[1]);
-      S[2] = fmaf(v, C[g][2], S[2]);
-      S[3] = fmaf(v, C[g][3], S[3]);
+      x0 = fma_pair(s0p[g], pair_of(C[g][0], C[g][1]), x0);
+      x1 = fma_pair(s1p[g], pair_of(C[g][2], C[g][3]), x1);
     }
-    const float2 scl = sm.scl[t][tig];
-    S[0] *= scl.x;
-    S[1] *= scl.y;
-    S[2] *= scl.x;
-    S[3] *= scl.y;
+    const uint64_t scl = *reinterpret_cast<const uint64_t*>(&sm.scl[t][tig]);
+    unpair(mul_pair(x0, scl), S[0], S[1]);
+    unpair(mul_pair(x1, scl), S[2], S[3]);
     f(t, S);
   }
 }

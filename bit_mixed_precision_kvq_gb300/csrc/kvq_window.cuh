@@ -91,15 +91,24 @@ __device__ __forceinline__ void cp_async_or_zero(void* dst, const void* src, boo
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(live ? N : 0) : "memory");
 }
 
-// rows [0, n) of `cap` bf16 rows from `src` on into a piece, the others zero.
+// rows [0, n) of 16 bf16 rows from `src` on into a piece, the others zero.
 template <bool kValue>
 __device__ __forceinline__ void copy_bf16(uint8_t* to, const uint8_t* src, int n, int lane) {
+  const int hi = lane >> 4, c = lane & 15;
+  src += lane * 16;
+  auto at = [&](int k) {  // of chunk c of row 2 k + hi
+    const int r = 2 * k + hi;
+    return to + r * kRowBytes + ((c ^ (kValue ? swz_v(r) : swz_k(r))) << 4);
+  };
+  if (n == 16) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int r = 2 * k + (lane >> 4), c = lane & 15;
-    const bool live = r < n;
-    cp_async_or_zero<16>(to + r * kRowBytes + ((c ^ (kValue ? swz_v(r) : swz_k(r))) << 4),
-                         src + (live ? r : 0) * kRowBytes + 16 * c, live);
+    for (int k = 0; k < 8; ++k) cp_async16(at(k), src + k * 2 * kRowBytes);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const bool live = 2 * k + hi < n;
+      cp_async_or_zero<16>(at(k), live ? src + k * 2 * kRowBytes : src - hi * kRowBytes, live);
+    }
   }
 }
 
@@ -107,16 +116,18 @@ __device__ __forceinline__ void copy_bf16(uint8_t* to, const uint8_t* src, int n
 template <int BITS, int G, int RB>
 __device__ __forceinline__ void copy_packed(uint8_t* to, const uint8_t* codes, const uint8_t* sz, int n, int lane) {
   constexpr int kSz = 4 * kD / G;
+  const bool row = lane < n;
+  if (n == RB) {
 #pragma unroll
-  for (int x0 = 0; x0 < RB * BITS; x0 += 32) {
-    const int x = x0 + lane;
-    const bool live = x < n * BITS;
-    cp_async_or_zero<16>(to + 16 * x, codes + 16 * (live ? x : 0), live);
+    for (int x = 0; x < RB * BITS; x += 32) cp_async16(to + 16 * (x + lane), codes + 16 * (x + lane));
+  } else {
+#pragma unroll 1
+    for (int x = lane; x < RB * BITS; x += 32) {
+      const bool live = x < n * BITS;
+      cp_async_or_zero<16>(to + 16 * x, codes + 16 * (live ? x : 0), live);
+    }
   }
-  if (lane < RB) {
-    const bool live = lane < n;
-    cp_async_or_zero<kSz>(to + RB * BITS * 16 + kSz * lane, sz + kSz * (live ? lane : 0), live);
-  }
+  if (lane < RB) cp_async_or_zero<kSz>(to + RB * BITS * 16 + kSz * lane, sz + kSz * (row ? lane : 0), row);
 }
 
 // PV of 16 bf16 rows of a piece: the weights of a column as high and low bf16.
