@@ -564,8 +564,8 @@ kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R, const kvq_
  *   race      device fp32 [B][vocab]: a v whose entry is not above 0 is not picked
  *   temperature  device fp32 [B] or NULL (1 for all); finite, and so is
  *             logit / temperature for the finite logits
- *   tree_len  device int32 [B]: tokens of each tree (only these are read), or
- *             NULL (n_q); an entry outside [1, n_q] marks an inactive sequence
+ *   tree_len  device int32 [B]: tokens of each tree (later ones do not count),
+ *             or NULL (n_q); an entry outside [1, n_q] marks an inactive sequence
  *   path      device int32 [B][n_q]: the tokens on the path, -1 behind the last
  *   path_len  device int32 [B], >= 1
  *   next_token  device int32 [B]
@@ -575,7 +575,8 @@ kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R, const kvq_
  * Logits of -inf are tokens that cannot be.  A sequence whose walk meets a row
  * of logits with NaN, +inf or nothing above -inf is inactive.  Inactive
  * sequences get path and next_token -1, logprob 0 and path_len -1 (which
- * kvq_tree_commit and kvq_attention_mass take as inactive).
+ * kvq_tree_commit and kvq_attention_mass take as inactive).  So does one whose
+ * CTAs waited for one another past kvq_set_wait_limits' tile_polls.
  * The outputs must not share memory with one another or with an input.
  */
 kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, const void* logits, int32_t logits_fp32,
@@ -657,7 +658,8 @@ kvq_status kvq_workspace_status(const void* workspace, uint32_t* status, void* s
  * up.  0 restores the default (2^24 and 2^21).  The defaults are far beyond
  * any healthy wait; shorter limits exist for testing the failure path.
  * tile_polls also limits the waits of kvq_decode_attention_tree inside a CTA,
- * where a limit of 1 asks once without suspending.
+ * where a limit of 1 asks once without suspending, and those of kvq_tree_verify
+ * for the CTAs of a sequence.
  */
 void kvq_set_wait_limits(uint32_t tile_polls, uint32_t peer_polls);
 
