@@ -380,7 +380,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
   // The race row while the walk goes on: its first groups stay in the ring where
   // every row has the same groups (16-byte boundaries at the same places).
   const bool whole_race = good && !greedy && a.lst * sizeof(X) % 16 == 0;
-  if (tid == kVerifyThreads - 1 && good && !greedy) prefetch_share(race, a.V, rank, ranks);
   __syncthreads();
   if (whole_race) row.begin_e(ring, race);
   if (!good) cluster_wait();  // (no exchange comes)
@@ -389,10 +388,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
   while (good) {
     const float* drow = kDraft ? a.draft + b * a.dsb + cur * a.dst : nullptr;
     uint64_t kids = sm.kids[cur];
-    if (kids && tid == kVerifyThreads - 1) {  // what is likely to be read next
+    if (kids && tid == kVerifyThreads - 1)  // what is likely to be read next
       prefetch_share(rows + (__ffsll(kids) - 1) * a.lst, a.V, rank, ranks);
-      if (kDraft && !greedy) prefetch_share(drow, a.V, rank, ranks);
-    }
     float kid_l = -INFINITY, kid_q = 0.f;  // on their way during the pass
     if (tid < 64 && (kids >> tid & 1ull)) {
       const int c = sm.token[tid];
@@ -406,6 +403,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
       sm.kid_l[tid] = kid_l;
       sm.kid_q[tid] = kid_q;
     }
+    if (xc.turn == 0 && !greedy && tid == kVerifyThreads - 1) prefetch_share(race, a.V, rank, ranks);
     const Part p = join_all(sm, mine, xc, JoinRows{sc});
     const float m = p.m, inv_s = 1.f / (1.f + p.s), log_s = log1pf(p.s);
     const int best = p.at;
