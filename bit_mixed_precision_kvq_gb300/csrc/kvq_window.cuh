@@ -34,6 +34,7 @@
 #pragma once
 
 #include <cstddef>
+#include <type_traits>
 
 #include "kvq_split.cuh"
 
@@ -366,134 +367,121 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
     for (int m = 0; m < 8; ++m) acc[t].o[m][0] = acc[t].o[m][1] = acc[t].o[m][2] = acc[t].o[m][3] = 0.f;
     acc[t].zo[0] = acc[t].zo[1] = acc[t].zo[2] = acc[t].zo[3] = 0.f;
   }
-  bool packed_acc = false;
-  float top = kTop;
+  float top = kTop, most_scale = ex2(15.9f - kTop);
   int slot = 0;  // of the block's K piece
+  // The warp's next blocks, up to the first visual one where `text` is set; kK,
+  // kV: their K and V rows are packed.
+  auto blocks_of = [&](bool text, auto k_packed, auto v_packed) {
+    constexpr bool kK = decltype(k_packed)::value, kV = decltype(v_packed)::value;
+    constexpr int RB = kK && kV ? kRB : 16;
 #pragma unroll 1
-  for (; i < blocks; i += step) {
-    const bool more = i + step < blocks;
-    const int slot_v = slot == kSlots - 1 ? 0 : slot + 1, slot_n = slot_v == kSlots - 1 ? 0 : slot_v + 1;
-    cp_async_wait<1>();
-    __syncwarp();
-    if (more) {
-      then = block_of(i + step);
-      issue_k(then, ring + slot_n * kPiece);
-    }
-    cp_async_commit();
-    const uint8_t* kc = ring + slot * kPiece;
-    const bool k_is_packed = KB < 16 && now.visual && kpk, v_is_packed = VB < 16 && now.visual && vpk;
-    const int rb = now.visual ? vrb : 16;
-    float S[NT][kRB / 16][4];
+    for (; i < blocks && !(text && now.visual); i += step) {
+      const bool more = i + step < blocks;
+      const int slot_v = slot == kSlots - 1 ? 0 : slot + 1, slot_n = slot_v == kSlots - 1 ? 0 : slot_v + 1;
+      cp_async_wait<1>();
+      __syncwarp();
+      if (more) {
+        then = block_of(i + step);
+        issue_k(then, ring + slot_n * kPiece);
+      }
+      cp_async_commit();
+      const uint8_t* kc = ring + slot * kPiece;
+      float S[NT][RB / 16][4];
 #pragma unroll
-    for (int hf = 0; hf < kRB / 16; ++hf) {
-      if (16 * hf < rb) {
-        if constexpr (KB < 16) {
-          if (k_is_packed) qk_packed_rows<KB, G, NT>(kc, kc + rb * kKRow, 16 * hf, sm.col, lane, [&](int t, const float (&x)[4]) {
+      for (int hf = 0; hf < RB / 16; ++hf) {
+        auto put_scores = [&](int t, const float (&x)[4]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[t][hf][e] = x[e];
-          });
-        }
-        if (!k_is_packed) {
+          for (int e = 0; e < 4; ++e) S[t][hf][e] = x[e];
+        };
+        if constexpr (kK) {
+          qk_packed_rows<KB, G, NT>(kc, kc + RB * kKRow, 16 * hf, sm.col, lane, put_scores);
+        } else {
           const uint8_t* r0 = kc + gid * kRowBytes;
           qk_bf16_rows<NT>([&](int P, uint4& f0, uint4& f1) {
             const int c = (4 * P + tig) ^ swz_k(gid);
             f0 = *reinterpret_cast<const uint4*>(r0 + (c << 4));
             f1 = *reinterpret_cast<const uint4*>(r0 + 8 * kRowBytes + (c << 4));
-          }, sm.col, a.scale_log2, lane, [&](int t, const float (&x)[4]) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[t][hf][e] = x[e];
-          });
+          }, sm.col, a.scale_log2, lane, put_scores);
         }
-      } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) S[t][hf][0] = S[t][hf][1] = S[t][hf][2] = S[t][hf][3] = -INFINITY;
       }
-    }
-    // What the columns' tokens do not see: rows past the block's last, later
-    // positions, positions between the first ones and a token's window.
-    const int last = now.t + now.n - 1;
-    if (now.n < rb || last > p0 || (last >= a.n_sink && now.t <= len - 1 - a.window) ) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int2 at = *reinterpret_cast<const int2*>(&sm.at[8 * t + 2 * tig]);
-#pragma unroll
-        for (int hf = 0; hf < kRB / 16; ++hf)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = now.t + 16 * hf + gid + (e >> 1) * 8, pos = e & 1 ? at.y : at.x;
-            if (x > last || x > pos || (x >= a.n_sink && x <= pos - a.window)) S[t][hf][e] = -INFINITY;
-          }
-      }
-    }
-    // the softmax of the warp's columns; the reference moves in few blocks
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      Acc& A = acc[t];
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-      for (int hf = 0; hf < kRB / 16; ++hf) {
-        mx0 = fmaxf(mx0, fmaxf(S[t][hf][0], S[t][hf][2]));
-        mx1 = fmaxf(mx1, fmaxf(S[t][hf][1], S[t][hf][3]));
-      }
-      if (__any_sync(0xffffffffu, mx0 > A.m[0] + top || mx1 > A.m[1] + top)) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-        }
-        mx0 = mx0 > A.m[0] + top ? mx0 - (top - kSlack) : A.m[0];
-        mx1 = mx1 > A.m[1] + top ? mx1 - (top - kSlack) : A.m[1];
-        const float c0 = ex2(A.m[0] - (mx0 == -INFINITY ? 0.f : mx0)), c1 = ex2(A.m[1] - (mx1 == -INFINITY ? 0.f : mx1));
-        A.m[0] = mx0;
-        A.m[1] = mx1;
-        A.l[0] *= c0;
-        A.l[1] *= c1;
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          A.o[m][0] *= c0;
-          A.o[m][1] *= c1;
-          A.o[m][2] *= c0;
-          A.o[m][3] *= c1;
-        }
-        A.zo[0] *= c0;
-        A.zo[1] *= c1;
-        A.zo[2] *= c0;
-        A.zo[3] *= c1;
-      }
-      const float r0 = A.m[0] == -INFINITY ? 0.f : A.m[0], r1 = A.m[1] == -INFINITY ? 0.f : A.m[1];
-#pragma unroll
-      for (int hf = 0; hf < kRB / 16; ++hf) {
-        S[t][hf][0] = ex2(S[t][hf][0] - r0);
-        S[t][hf][1] = ex2(S[t][hf][1] - r1);
-        S[t][hf][2] = ex2(S[t][hf][2] - r0);
-        S[t][hf][3] = ex2(S[t][hf][3] - r1);
-        A.l[0] += S[t][hf][0] + S[t][hf][2];
-        A.l[1] += S[t][hf][1] + S[t][hf][3];
-      }
-    }
-    cp_async_wait<1>();
-    __syncwarp();  // V is here; the K piece's slot is free
-    if (more) issue_v(then, ring + slot * kPiece);
-    cp_async_commit();
-    const uint8_t* vc = ring + slot_v * kPiece;
-    if constexpr (VB < 16) {
-      if (v_is_packed != packed_acc) {  // text blocks come first: once a warp
-        packed_acc = v_is_packed;
+      // What the columns' tokens do not see: rows past the block's last, later
+      // positions, positions between the first ones and a token's window.
+      const int last = now.t + now.n - 1;
+      if (now.n < RB || last > p0 || (last >= a.n_sink && now.t <= len - 1 - a.window)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          if (packed_acc) acc_to_packed<VB>(acc[t]);
-          else acc_to_true<VB, G>(acc[t], tig);
+          const int2 at = *reinterpret_cast<const int2*>(&sm.at[8 * t + 2 * tig]);
+#pragma unroll
+          for (int hf = 0; hf < RB / 16; ++hf)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = now.t + 16 * hf + gid + (e >> 1) * 8, pos = e & 1 ? at.y : at.x;
+              if (x > last || x > pos || (x >= a.n_sink && x <= pos - a.window)) S[t][hf][e] = -INFINITY;
+            }
         }
       }
-      if (v_is_packed) {
+      // the softmax of the warp's columns; the reference moves in few blocks
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        Acc& A = acc[t];
+        float mx0 = fmaxf(S[t][0][0], S[t][0][2]), mx1 = fmaxf(S[t][0][1], S[t][0][3]);
+#pragma unroll
+        for (int hf = 1; hf < RB / 16; ++hf) {
+          mx0 = fmaxf(mx0, fmaxf(S[t][hf][0], S[t][hf][2]));
+          mx1 = fmaxf(mx1, fmaxf(S[t][hf][1], S[t][hf][3]));
+        }
+        if (__any_sync(0xffffffffu, mx0 > A.m[0] + top || mx1 > A.m[1] + top)) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+          }
+          mx0 = mx0 > A.m[0] + top ? mx0 - (top - kSlack) : A.m[0];
+          mx1 = mx1 > A.m[1] + top ? mx1 - (top - kSlack) : A.m[1];
+          const float c0 = ex2(A.m[0] - (mx0 == -INFINITY ? 0.f : mx0)), c1 = ex2(A.m[1] - (mx1 == -INFINITY ? 0.f : mx1));
+          A.m[0] = mx0;
+          A.m[1] = mx1;
+          A.l[0] *= c0;
+          A.l[1] *= c1;
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            A.o[m][0] *= c0;
+            A.o[m][1] *= c1;
+            A.o[m][2] *= c0;
+            A.o[m][3] *= c1;
+          }
+          A.zo[0] *= c0;
+          A.zo[1] *= c1;
+          A.zo[2] *= c0;
+          A.zo[3] *= c1;
+        }
+        const uint64_t ref = pair_of(A.m[0] == -INFINITY ? 0.f : -A.m[0], A.m[1] == -INFINITY ? 0.f : -A.m[1]);
+        uint64_t l = pair_of(A.l[0], A.l[1]);
+#pragma unroll
+        for (int hf = 0; hf < RB / 16; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            unpair(add_pair(pair_of(S[t][hf][e], S[t][hf][e + 1]), ref), S[t][hf][e], S[t][hf][e + 1]);
+            S[t][hf][e] = ex2(S[t][hf][e]);
+            S[t][hf][e + 1] = ex2(S[t][hf][e + 1]);
+            l = add_pair(l, pair_of(S[t][hf][e], S[t][hf][e + 1]));
+          }
+        unpair(l, A.l[0], A.l[1]);
+      }
+      cp_async_wait<1>();
+      __syncwarp();  // V is here; the K piece's slot is free
+      if (more) issue_v(then, ring + slot * kPiece);
+      cp_async_commit();
+      const uint8_t* vc = ring + slot_v * kPiece;
+      if constexpr (kV) {
         // a row's largest scale (a lane a row): times a weight it must stay below 2^16
         float big = 0.f;
-        if (lane < rb) {
-          const __half* z = reinterpret_cast<const __half*>(vc + rb * kVRow + kVSz * lane);
+        if (lane < RB) {
+          const __half* z = reinterpret_cast<const __half*>(vc + RB * kVRow + kVSz * lane);
 #pragma unroll
           for (int g = 0; g < kD / G; ++g) big = fmaxf(big, __half2float(z[kD / G + g]));
         }
-        if (__any_sync(0xffffffffu, big >= ex2(15.9f - top))) {  // rare
+        if (__any_sync(0xffffffffu, big >= most_scale)) {  // rare
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
           const float to = floorf(15.9f - log2f(big)), f = ex2(to - top);
@@ -509,30 +497,52 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[t].zo[e] *= f;
 #pragma unroll
-            for (int hf = 0; hf < kRB / 16; ++hf)
+            for (int hf = 0; hf < RB / 16; ++hf)
 #pragma unroll
               for (int e = 0; e < 4; ++e) S[t][hf][e] *= f;
           }
           top = to;
+          most_scale = ex2(15.9f - top);
         }
 #pragma unroll
-        for (int hf = 0; hf < kRB / 16; ++hf)
-          if (16 * hf < rb) {
-            pv_packed_rows<VB, G, NT>(vc, vc + rb * kVRow, 16 * hf, [&](int t) { return S[t][hf]; }, gid, tig, acc);
-          }
+        for (int hf = 0; hf < RB / 16; ++hf)
+          pv_packed_rows<VB, G, NT>(vc, vc + RB * kVRow, 16 * hf, [&](int t) { return S[t][hf]; }, gid, tig, acc);
+      } else {
+        pv_bf16<NT>(vc, [&](int t) { return S[t][0]; }, lane, acc);
+      }
+      now = then;
+      slot = slot_n;
+    }
+  };
+  constexpr std::true_type kYes;
+  constexpr std::false_type kNo;
+  blocks_of(kpk || vpk, kNo, kNo);  // bf16 rows
+  if (i < blocks) {
+    if constexpr (VB < 16) {
+      if (vpk) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc_to_packed<VB>(acc[t]);
       }
     }
-    if (!v_is_packed) pv_bf16<NT>(vc, [&](int t) { return S[t][0]; }, lane, acc);
-    now = then;
-    slot = slot_n;
+    if (kpk && vpk) {
+      if constexpr (KB < 16 && VB < 16) blocks_of(false, kYes, kYes);
+    } else if (vpk) {
+      if constexpr (VB < 16) blocks_of(false, kNo, kYes);
+    } else {
+      if constexpr (KB < 16) blocks_of(false, kYes, kNo);
+    }
+    if constexpr (VB < 16) {
+      if (vpk) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc_to_true<VB, G>(acc[t], tig);
+      }
+    }
   }
   cp_async_wait<0>();
 
   // The warps meet: m and l of every column, then the o rows over the CTA's m.
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if constexpr (VB < 16)
-      if (packed_acc) acc_to_true<VB, G>(acc[t], tig);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float l = acc[t].l[e];
