@@ -300,6 +300,16 @@ extern "C" kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R,
   if (q && k && (kvq::rows_meet(*q_out, H[0], *k, H[1], B, n_tok) || kvq::rows_meet(*q, H[0], *k_out, H[1], B, n_tok) ||
                  kvq::rows_meet(*q_out, H[0], *k_out, H[1], B, n_tok)))
     return KVQ_ERR_INVALID_ARG;
+  // what every row is made with must not lie under the outputs
+  const int64_t n_pos = (R->n_axes - 1) * pos_stride_axis + (B - 1) * pos_stride_b + n_tok;
+  for (int i = 0; i < 2; ++i) {
+    if (!out[i]) continue;
+    const int64_t span = kvq::span_bytes(*out[i], B, H[i], n_tok);
+    if (kvq::ranges_meet(out[i]->data, span, pos, 4 * n_pos) || kvq::ranges_meet(out[i]->data, span, inv_freq, 2 * R->rot_dim) ||
+        kvq::ranges_meet(out[i]->data, span, q_weight, kvq::kRowBytes) ||
+        kvq::ranges_meet(out[i]->data, span, k_weight, kvq::kRowBytes))
+      return KVQ_ERR_INVALID_ARG;
+  }
   if (B * n_tok > 0x7ff00000LL) return KVQ_ERR_UNSUPPORTED;  // (past the last token by a stride of the grid)
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;

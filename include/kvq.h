@@ -506,7 +506,8 @@ kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* 
  *   eps       finite, >= 0
  *   q_out, k_out   as q and k, every row in memory of its own; each may be its
  *             input (same data and strides), else the two must lie apart.
- *             q_out must share no row with k, nor k_out with q or q_out
+ *             q_out must share no row with k, nor k_out with q or q_out, nor
+ *             may pos, inv_freq or a weight lie inside an output's span
  * Arithmetic is fp32 (angles are taken modulo a turn exactly, whatever the
  * position), rounded to bf16 once.  A NaN or infinity in a row stays in it.
  */
@@ -560,7 +561,8 @@ kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R, const kvq_
  *   draft_prob  device fp32, entry (b, i, v) at index b*draft_stride_b +
  *             i*draft_stride_t + v, or NULL; a token id whose entry is NaN
  *             is refused and not picked after a refusal
- *   accept    device fp32 [B][n_q]: u of each token (entry 0 is unread)
+ *   accept    device fp32 [B][n_q]: u of each token (token 0's does not count);
+ *             a NaN refuses it, and a p or r of 0 is refused whatever u is
  *   race      device fp32 [B][vocab]: a v whose entry is not above 0 is not picked
  *   temperature  device fp32 [B] or NULL (1 for all); finite, and so is
  *             logit / temperature for the finite logits

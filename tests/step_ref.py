@@ -84,7 +84,7 @@ def verify_reference(logits, tokens, masks, u, race, draft=None, heat=None, size
                 else:
                     total = p.sum()
                     have, want = p[c], float(u[b, j]) * total * (1.0 if q is None else q[c])
-                    ok = want < have
+                    ok = have > 0 and want < have
                     if c not in gone or q is not None:
                         margin[b] = min(margin[b], abs(have - want) / max(have, want, 1e-300))
                 if ok:

@@ -62,6 +62,7 @@ ROPE_BAD = [
     # outputs over inputs, in place apart
     dict(qo=(FAR + 256, 12288, 128, 2048)), dict(qo=(FAR, 12288, 128, 4096)), dict(ko=FQ), dict(qo=FK), dict(ko=OQ),
     dict(qo=(FAR + 4 * 256, 12288, 128, 2048), q=OQ),
+    dict(pos=2 * FAR + 1024), dict(freq=3 * FAR + 512), dict(wq=2 * FAR), dict(wk=3 * FAR + 16), dict(pos=2 * FAR - 4 * 20),
     dict(R=dict(rot_dim=0)), dict(R=dict(rot_dim=136)), dict(R=dict(rot_dim=12)), dict(R=dict(interleaved=2)), dict(R=dict(n_axes=0)),
     dict(R=dict(n_axes=5)), dict(R=dict(n_axes=2)), dict(R=dict(axis0=3)),
 ]
@@ -88,7 +89,7 @@ def test_rope_too_many_tokens(lib):
     L = _layout(B=64, H_q=1, H_kv=1, protected=[])
     big = 2 ** 31 // 64
     x = (FAR, big * 128, 128, 128)
-    assert _rope(lib, L=L, q=x, k=None, qo=(FAR << 2, big * 128, 128, 128), ko=None, n=big, pa=0, pb=0) == 2
+    assert _rope(lib, L=L, q=x, k=None, qo=(FAR << 2, big * 128, 128, 128), ko=None, n=big, pa=0, pb=0, pos=6 * FAR) == 2
 
 
 def _verify(lib, **bad):

@@ -71,6 +71,8 @@ CASES = [
     (4, 26, 1000, True, False, False), (4, 26, 1001, True, True, False), (2, 64, 4099, False, False, True), (2, 64, 4099, False, True, True),
     (9, 16, 8192, True, True, False), (1, 16, 70001, True, True, False), (1, 16, 152000, True, False, False), (20, 7, 9001, False, False, False),
     (80, 3, 20000, True, False, True), (160, 3, 600, False, True, True),
+    # two CTAs and one a sequence, several groups a thread, rows at every alignment
+    (50, 5, 30001, True, True, False), (80, 4, 20003, False, True, False), (40, 3, 33333, True, False, True),
 ]
 
 
@@ -150,6 +152,31 @@ def test_verify_token_ids_outside_and_twice(cuda_dev, kvq):
     out = run(kvq, cuda_dev, s)
     assert out[1].cpu().tolist()[:2] == [1, 1] and out[2][1] != hot
     check_verify(out, verify_reference(s.x, s.tokens, s.masks, s.u, s.race))
+
+
+@pytest.mark.parametrize("probs", [False, True])
+def test_verify_random_numbers_out_of_range(cuda_dev, kvq, probs):
+    """What has no probability is refused whatever its random number is; a NaN
+    number refuses its token.  (Numbers outside [0, 1) promise no distribution.)"""
+    B, n, V = 4, 3, 100
+    s = Tree(B, n, V, False, probs, 21)
+    s.masks = np.array([[1, 3, 5]], np.uint64)
+    s.x[:, :, 50:] = -np.inf
+    s.t = torch.from_numpy(s.x)
+    s.tokens[0], s.u[0] = [0, 70, -3], [0, -1.0, -5.0]    # p = 0; no such id
+    s.tokens[1], s.u[1] = [0, 10, 11], np.nan
+    s.tokens[2], s.u[2] = [0, 10, 11], [0, 2.0, -1.0]     # the first refused, the second taken
+    if probs:
+        s.draft[:, :, 10:12] = np.float32(0.01)
+        s.draft[2, 0, 10] = 0.999
+        s.x[2, 0, 10] = s.x[2, 0, :10].min()
+        s.t = torch.from_numpy(s.x)
+        s.draft[3, 0, :] = np.nan                         # everything is refused, nothing is left: r stays
+    out = run(kvq, cuda_dev, s)
+    assert out[1].tolist()[:3] == [1, 1, 2] and out[0][2].tolist() == [0, 2, -1]
+    assert all(0 <= int(t) < 50 for t in out[2])
+    if probs:
+        assert out[1][3] == 1
 
 
 def test_verify_race_without_entries(cuda_dev, kvq):
