@@ -26,7 +26,11 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
   if (units > 0x3ffffff || cols > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;  // 16 CTAs a unit at most
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
-  // Units enough for every SM: small CTAs, one a unit; else more warps a CTA.
+  // Two tiles of columns unpack a row once (16 columns x 1280 units: 91 us, 105
+  // as two units of one tile).  Units enough for every SM: CTAs of four warps, one a
+  // unit, several an SM (512 units of 345 positions 16 us, 21 with eight warps);
+  // else eight warps, for more of them a unit (64 units of 8,257 positions 24 us, 41
+  // with four; four units of 2,078 6.4 and 8.0).
   f.warps = f.nt == 2 || units >= 2 * n_sm ? 4 : 8;
   const kvq::win::Kernel k = L->d.k_bits == 2   ? kvq::win::window_kernel_k2(L->d.v_bits, L->d.group_size, f)
                              : L->d.k_bits == 4 ? kvq::win::window_kernel_k4(L->d.v_bits, L->d.group_size, f)
