@@ -11,11 +11,12 @@
 // of the unit's CTAs take in turn: text blocks first, so that a warp's
 // accumulator changes to packed rows once.  A thread-block cluster holds the CTAs
 // of one or more units: units of heads that keep bf16 rows get more of them than
-// those of packed heads.  Every warp streams its blocks
-// through a ring of its own in shared memory (cp.async, K and V rows as separate
-// pieces, so that V and the next K are under way while a block's scores are
-// made), and runs an online softmax of its own.  The warps meet in shared
-// memory, the CTAs in distributed shared memory: one launch, no workspace.
+// those of packed heads.  Every warp streams its blocks through a ring of its own
+// in shared memory (cp.async, K and V rows as separate pieces, so that V and the
+// next K are under way while a block's scores are made), and runs an online softmax
+// of its own.  The warps meet in shared memory, the CTAs in distributed shared
+// memory: one launch, no workspace.  (Asynchronous stores on barriers in place of
+// the cluster barrier there: 0.1 us less of 5.3 and 6.5, not kept.)
 //
 //   QK: S[t][c] = K[t] . q[c]   (mma.sync m16n8k16, positions = M, columns = N)
 //   PV: O[d][c] += V[t][d] P[t][c]   (d = M)
