@@ -143,3 +143,24 @@ def test_rope_feeds_a_decode_step(cuda_dev, kvq):
     torch.cuda.synchronize()
     row = cache[int(L.off[kvq.SEG_TEXT_K]):][:int(L.bytes[kvq.SEG_TEXT_K])].view(torch.bfloat16).view(2, 2, -1, 128)[:, :, 50 - 36]
     assert torch.equal(row, k[:, 0]) and torch.isfinite(out).all()
+
+
+def test_rope_rows_past_32_bits(cuda_dev, kvq):
+    """Sequences and tokens more than 2^32 bytes apart, in and out."""
+    B, n, H, rot = 2, 2, 3, 128
+    x = bf16((B, n, H, 128), 30, cuda_dev)
+    big = torch.empty(2 ** 31 + 2 ** 21, dtype=torch.bfloat16, device=cuda_dev)
+    pos, freq = _pos(3, B, n, 9000, 31), _freq(rot)
+    p, f = torch.from_numpy(pos).to(cuda_dev), torch.from_numpy(freq).to(cuda_dev)
+    L, R = _layout(kvq, B, H, H), kvq.rope_desc(rot, SECTIONS)
+    want = torch.empty_like(x)
+    kvq.norm_rope(L, R, x, None, p, f, want, None)
+    check_rope(want, f64(x), pos, freq.astype(np.float64), SECTIONS, rot, False, None, 0.0)
+    for strides in ((2 ** 31 + 1024, 2 ** 19, 128, 1), (2 ** 19, 2 ** 31 + 4096, 2 ** 10, 1)):
+        far = big.as_strided((B, n, H, 128), strides)
+        far.copy_(x)
+        out = torch.empty_like(x)
+        kvq.norm_rope(L, R, far, None, p, f, out, None)
+        assert torch.equal(out, want)
+        kvq.norm_rope(L, R, far, None, p, f, far, None)
+        assert torch.equal(far, want)

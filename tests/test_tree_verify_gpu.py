@@ -72,7 +72,7 @@ CASES = [
     (9, 16, 8192, True, True, False), (1, 16, 70001, True, True, False), (1, 16, 152000, True, False, False), (20, 7, 9001, False, False, False),
     (80, 3, 20000, True, False, True), (160, 3, 600, False, True, True),
     # two CTAs and one a sequence, several groups a thread, rows at every alignment
-    (50, 5, 30001, True, True, False), (80, 4, 20003, False, True, False), (40, 3, 33333, True, False, True),
+    (1, 2, 1048577, True, True, False), (77, 1, 256000, False, False, False), (50, 5, 30001, True, True, False), (80, 4, 20003, False, True, False), (40, 3, 33333, True, False, True),
 ]
 
 
@@ -238,3 +238,22 @@ def test_verify_is_repeatable(cuda_dev, kvq):
     a, b = run(kvq, cuda_dev, s), run(kvq, cuda_dev, s)
     for x, y in zip(a, b):
         assert torch.equal(x, y)
+
+
+def test_verify_rows_past_32_bits(cuda_dev, kvq):
+    """Rows more than 2^32 bytes apart."""
+    B, n, V = 2, 4, 5003
+    s = Tree(B, n, V, True, True, 22)
+    want = run(kvq, cuda_dev, s)
+    big, far = torch.empty(2 ** 31 + 2 ** 20, dtype=torch.bfloat16, device=cuda_dev), 2 ** 31 + 8192
+    logits = big.as_strided((B, n, V), (far, V + 5, 1))
+    logits.copy_(s.t)
+    got = run(kvq, cuda_dev, s, logits=logits)
+    del logits, big
+    q = torch.empty(2 ** 30 + 2 ** 20, device=cuda_dev).as_strided((B, n, V), (2 ** 30 + 4099, V, 1))
+    q.copy_(torch.from_numpy(s.draft))
+    again = run(kvq, cuda_dev, s, draft=q)
+    # (rows at other 16-byte boundaries are summed in another order)
+    ref = verify_reference(s.x, s.tokens, s.masks, s.u, s.race, s.draft)
+    for out in (want, got, again):
+        check_verify(out, ref)

@@ -209,3 +209,43 @@ def test_window_is_repeatable(cuda_dev, kvq):
     q = bf16((2, 2, 28, 128), 25, cuda_dev)
     a, b = run(kvq, cuda_dev, f, q, 2950, 10, 1024), run(kvq, cuda_dev, f, q, 2950, 10, 1024)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("prot", [[], list(range(8))])
+def test_window_cache_past_32_bits(cuda_dev, kvq, prot):
+    """A cache of 4.9 GB, rows of the last head more than 2^32 bytes in (bf16
+    rows, so that the reference reads them from the buffer)."""
+    T = 1200000
+    c = Case(1, 16, 8, T, 3, T - 7, 16, 16, 32, prot)
+    L = c.layout()
+    assert int(L.total_bytes) > 2 ** 32 + 2 ** 28
+    cache = torch.empty(int(L.total_bytes), dtype=torch.uint8, device=cuda_dev)
+    g = torch.Generator(device=cuda_dev).manual_seed(5)
+    cache.view(torch.bfloat16).normal_(generator=g)
+
+    def rows(vis, text):
+        """[8, T, 128] of the last 8,000 positions and the first 16, fp64."""
+        s = vis[1] if prot else vis[0]
+        n = int(L.Tv) if prot else int(L.Tv_pad)
+        v = cache[int(L.off[s]):int(L.off[s]) + 8 * n * 256].view(torch.bfloat16).view(8, n, 128)
+        t = cache[int(L.off[text]):int(L.off[text]) + 8 * int(L.T_text) * 256].view(torch.bfloat16).view(8, int(L.T_text), 128)
+        first = torch.cat([t[:, :3], v[:, :13]], 1)
+        last = torch.cat([v[:, T - 8000 - 3:T - 10], t[:, 3:]], 1)
+        return f64(first), f64(last)
+
+    q = bf16((1, 2, 16, 128), 40, cuda_dev)
+    out, lse = torch.zeros_like(q), torch.zeros(1, 2, 16, device=cuda_dev)
+    kvq.decode_attention_window(L, cache, q, T, 16, 7000, out, None, lse)
+    (k0, k1), (v0, v1) = rows((kvq.SEG_K_CODES, kvq.SEG_PROT_K), kvq.SEG_TEXT_K), rows((kvq.SEG_V_CODES, kvq.SEG_PROT_V), kvq.SEG_TEXT_V)
+    # the same positions as a short sequence: the first 16, then the last 8,000
+    small = Case(1, 16, 8, 8016, 3, 8009, 16, 16, 32, prot)
+    check_window(small, out, lse, f64(q), np.concatenate([k0, k1], 1)[None], np.concatenate([v0, v1], 1)[None], [8016], 16, 7000)
+
+
+def test_window_of_a_long_context(cuda_dev, kvq):
+    """150,000 positions in the window of one 2-bit head: several turns of every ring."""
+    c = Case(1, 3, 1, 160000, 5, 159000, 2, 2, 128, [])
+    f = Filled(c, 41, cuda_dev)
+    q = bf16((1, 2, 3, 128), 42, cuda_dev)
+    out, lse = run(kvq, cuda_dev, f, q, 159500, 33, 150000)
+    check_window(c, out, lse, f64(q), f.khat, f.vhat, [159500], 33, 150000)
