@@ -22,8 +22,9 @@
 // 128,000, 4.2 rows on average and 8 or more on the longest walk 58 us (the rows
 // that are read take 10 at the rate of a copy).  Rolled loops: unrolled over a
 // thread's groups the code of a pass that runs once a call comes from L2 (130 us
-// became 68).  1,024 threads a CTA, two groups a turn, and a group of draft
-// probabilities ahead of every refusal were no faster.
+// became 68).  1,024 threads a CTA, two groups a turn, draft rows asked for ahead
+// of a refusal, two CTAs an SM with shorter rings (56 us, but 20 in place of 15 for
+// 16 sequences) and every warp's part sent to all ranks (57 and 17) were not kept.
 #include "kvq_geom.cuh"
 
 #include <climits>
