@@ -497,7 +497,8 @@ kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* 
  *             data[b*stride_b + h*stride_h + i*stride_t + d] (strides in elements,
  *             >= 0, multiples of 8; 16-byte aligned).  Either may be NULL with
  *             its output: only the other is made then
- *   n_tok     tokens per sequence, >= 0 (0 is a no-op)
+ *   n_tok     tokens per sequence, >= 0 (0 is a no-op; KVQ_ERR_UNSUPPORTED where
+ *             B * n_tok passes 2^31 - 2^20)
  *   pos       device int32, entry (axis, b, i) at index axis*pos_stride_axis +
  *             b*pos_stride_b + i, any value
  *   inv_freq  device fp32 [rot_dim / 2], finite
