@@ -16,7 +16,7 @@
 // next K are under way while a block's scores are made), and runs an online softmax
 // of its own.  The warps meet in shared memory, the CTAs in distributed shared
 // memory: one launch, no workspace.  (Asynchronous stores on barriers in place of
-// the cluster barrier there: 0.1 us less of 5.3 and 6.5, not kept.)
+// the cluster barrier there: 0.1 us less of 5.3 and of 6.5, not kept.)
 //
 //   QK: S[t][c] = K[t] . q[c]   (mma.sync m16n8k16, positions = M, columns = N)
 //   PV: O[d][c] += V[t][d] P[t][c]   (d = M)
@@ -41,7 +41,8 @@
 // MB, 11.6 GFLOP) 85 us.  Steps: units split by the rows they hold (24 us where
 // equal shares took 31), unpacked codes shared by two column tiles and three CTAs
 // of 168 registers an SM (91 us, before 137 with one of eight warps), a loop for each
-// kind of rows (85, before 88).
+// kind of rows (85, before 88), the first rows asked for while the previous kernel
+// ends (6.1 and 21.6 us, before 6.5 and 22.4).
 #pragma once
 
 #include <cstddef>
@@ -283,8 +284,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
   const int hi = p.B == 1 ? hb : hb / p.B, b = hb - hi * p.B;
   const int h = idle ? 0 : a.head[a.head0[cls] + hi];
   cluster_arrive();  // waited for before the first store to another CTA
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_launch_dependents();  // this kernel writes no cache row
+  if (a.seq_len) pdl_wait();
   int len = a.seq_len ? a.seq_len[b] : a.T;
   if (len < 0 || len > a.T || idle) len = 0;
   const int p0 = len - a.n_q;  // position of token 0
@@ -353,8 +353,21 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
   const int step = ranks * kWarps;
   int i = rank * kWarps + warp;
   Block now = {}, then = {};
+  if (i < blocks) now = block_of(i);
+  if (!a.seq_len) {
+    // Lengths known: the warp's first rows into L2 while the previous kernel ends
+    // (what it still writes of them replaces the lines there).
+    if (i < blocks && lane < 4) {
+      const bool value = lane & 1, packed = now.visual && (value ? vpk : kpk), sz = lane >= 2;
+      const uint8_t* at = value ? (now.visual ? hr.vis_v : hr.text_v) : (now.visual ? hr.vis_k : hr.text_k);
+      int bytes = packed ? (value ? kVRow : kKRow) : kRowBytes;
+      if (sz) at = value ? hr.vis_vsz : hr.vis_ksz, bytes = value ? kVSz : kKSz;
+      if (!sz || packed) prefetch_bytes(at + now.row * bytes, now.n * bytes);
+    }
+    pdl_wait();
+  }
+  if (threadIdx.x == 0) pdl_launch_dependents();  // this kernel writes no cache row
   if (i < blocks) {
-    now = block_of(i);
     issue_k(now, ring);
     cp_async_commit();
     issue_v(now, ring + kPiece);
