@@ -36,6 +36,7 @@ namespace {
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxRanks = 16;  // CTAs of a cluster
+constexpr uint32_t kLeavePolls = 4096;  // of a wait for parts that have been sent (microseconds away), whatever the limit of the others
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 struct VerifyArgs {
@@ -64,6 +65,8 @@ struct VerifySmem {
   Part slot[2][kMaxRanks];  // by exchange parity and rank
   uint64_t bar[2];          // the ranks' parts have come (transaction bytes)
   int late;                 // a wait gave up
+  int any_late;             // so did one in some CTA of the cluster (which stores it here)
+  int sent[kMaxRanks];      // how many exchanges each rank sent its part of (stored by the rank)
   Part warp[kVerifyWarps], joined;
   uint64_t kids[KVQ_MAX_QUERY_TOKENS];  // children of each token
   int32_t token[KVQ_MAX_QUERY_TOKENS];
@@ -118,8 +121,8 @@ struct JoinBest {
 // around plain stores took 1,400 to 1,800 cycles, these about half).  Slots and
 // barriers alternate: a rank sends t + 2 only with every rank's t + 1 in hand,
 // which those send behind arming the barrier for t + 2.  A wait that gives up sets
-// sm.late, the same for the whole CTA: the walk ends there, and the other ranks'
-// waits give up in their turn.
+// sm.late, the same for the whole CTA: the walk ends there, the other ranks'
+// waits give up in their turn, and `leave` sees to the parts still on their way.
 struct Exchange {
   int rank, ranks;
   uint32_t polls, turn;
@@ -135,7 +138,9 @@ __device__ __forceinline__ Part join_all(VerifySmem& sm, Part p, Exchange& x, co
     p = join(lane < kVerifyWarps ? sm.warp[lane] : Join::none());
     if (lane < x.ranks)
       st_async_v4(dsmem_addr(&sm.slot[s][x.rank], lane), make_float4(p.m, p.s, __int_as_float(p.at), 0.f), dsmem_addr(&sm.bar[s], lane));
-    const bool late = __any_sync(0xffffffffu, !mbar_wait_cluster(&sm.bar[s], (x.turn >> 1) & 1, x.polls));
+    const uint32_t parity = (x.turn >> 1) & 1;
+    const bool here = x.polls == 1 ? mbar_test_cluster(&sm.bar[s], parity) : mbar_wait_cluster(&sm.bar[s], parity, x.polls);
+    const bool late = __any_sync(0xffffffffu, !here);
     if (lane == 0 && !late) mbar_arrive_expect_tx(&sm.bar[s], 16 * x.ranks);
     p = join(lane < x.ranks && !late ? sm.slot[s][lane] : Join::none());
     if (lane == 0) {
@@ -146,6 +151,41 @@ __device__ __forceinline__ Part join_all(VerifySmem& sm, Part p, Exchange& x, co
   __syncthreads();
   ++x.turn;
   return sm.joined;
+}
+
+// The last meeting of the cluster's CTAs: no CTA ends while another's part is on
+// its way to it.  A CTA that leaves with all its exchanges done has every part
+// that was sent to it (no rank sends for an exchange that another has not
+// reached).  One that gave up in exchange t = turn - 1 has not: parts of t and, from
+// ranks that saw t complete, of t + 1 may still come, and no barrier between CTAs
+// waits for them.  So the ranks tell one another how many exchanges they sent, and
+// it waits on the barriers of t and t + 1 (both armed) for the bytes that were sent,
+// taking the others off.  Called by every thread with the CTA's turn, behind a
+// __syncthreads that made sm.late known; `between` is work before the meeting ends.
+template <typename F>
+__device__ __forceinline__ void leave(VerifySmem& sm, const Exchange& x, F&& between) {
+  const int tid = threadIdx.x;
+  if (sm.late) {
+    if (tid < x.ranks) st_dsmem(dsmem_addr(&sm.any_late, tid), 1);
+    __syncwarp();
+    cluster_arrive();  // release: the stores come before it
+  } else {
+    cluster_arrive_relaxed();
+  }
+  between();
+  cluster_wait();
+  if (!*reinterpret_cast<volatile int*>(&sm.any_late)) return;  // the same in every CTA
+  if (tid < x.ranks) st_dsmem(dsmem_addr(&sm.sent[x.rank], tid), static_cast<int>(x.turn));
+  __syncwarp();
+  cluster_sync();
+  if (!sm.late || tid != 0) return;
+  const volatile int* sent = sm.sent;
+  for (uint32_t t = x.turn - 1; t <= x.turn; ++t) {
+    uint32_t missing = 0;
+    for (int r = 0; r < x.ranks; ++r) missing += sent[r] <= static_cast<int>(t);
+    if (missing) mbar_complete_tx(&sm.bar[t & 1], 16 * missing);
+    mbar_wait_cluster(&sm.bar[t & 1], (t >> 1) & 1, kLeavePolls);
+  }
 }
 
 // Asks for the CTA's share of a row of V elements of type X, or the first
@@ -356,7 +396,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
     for (int i = 0; i < 2; ++i) mbar_init(&sm.bar[i], 1);
     fence_barrier_init();
     for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.bar[i], 16 * ranks);
-    sm.late = 0;
+    sm.late = sm.any_late = 0;
   }
   __syncwarp();
   cluster_arrive();  // waited for at the first exchange
@@ -536,21 +576,21 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) verify_kernel(const __grid_
     if (tid == 0) sm.logp[count - 1] = log_prob(Share<X>::value(row.row + next));
     break;
   }
-  // No CTA ends while another may still send to it, or with copies under way.
-  cluster_arrive_relaxed();
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-  if (sm.late) good = false;
-  if (rank == 0 && tid == 0) {
-    a.path_len[b] = good ? count : -1;
-    a.next[b] = good ? next : -1;
-  }
-  if (rank == 0 && tid < a.n_q) {
-    const int64_t i = static_cast<int64_t>(b) * a.n_q + tid;
-    a.path[i] = good && tid < count ? sm.path[tid] : -1;
-    if (a.logprob) a.logprob[i] = good && tid < count ? sm.logp[tid] : 0.f;
-  }
-  cluster_wait();
+  // No CTA ends while a part is on its way to it, or with copies under way.
+  leave(sm, xc, [&] {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // what thread 0 wrote of the path
+    if (sm.late) good = false;
+    if (rank == 0 && tid == 0) {
+      a.path_len[b] = good ? count : -1;
+      a.next[b] = good ? next : -1;
+    }
+    if (rank == 0 && tid < a.n_q) {
+      const int64_t i = static_cast<int64_t>(b) * a.n_q + tid;
+      a.path[i] = good && tid < count ? sm.path[tid] : -1;
+      if (a.logprob) a.logprob[i] = good && tid < count ? sm.logp[tid] : 0.f;
+    }
+  });
 }
 
 }  // namespace
