@@ -508,7 +508,8 @@ kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* 
  *   q_out, k_out   as q and k, every row in memory of its own; each may be its
  *             input (same data and strides), else the two must lie apart.
  *             q_out must share no row with k, nor k_out with q or q_out, nor
- *             may pos, inv_freq or a weight lie inside an output's span
+ *             may pos, inv_freq or a weight lie inside an output's span.  Rows
+ *             of k_out may be text rows of a cache (kvq_set_cache_preload)
  * Arithmetic is fp32 (angles are taken modulo a turn exactly, whatever the
  * position), rounded to bf16 once.  A NaN or infinity in a row stays in it.
  */
@@ -683,8 +684,9 @@ void kvq_set_wait_limits(uint32_t tile_polls, uint32_t peer_polls);
  * a memory copy separates it) before the call.  The library's own writers
  * (kvq_quantize_append, kvq_decode_step, kvq_decode_step_ragged) fence
  * their cache writes and let the next kernel launch only after them and
- * after their own dependency wait; kvq_tree_commit and kvq_cache_evict let
- * it launch when they have finished.  So the early copies see every row
+ * after their own dependency wait; kvq_tree_commit, kvq_cache_evict and
+ * kvq_norm_rope (whose outputs may be rows of a cache) let it launch when they
+ * have finished.  So the early copies see every row
  * written before.  Off (0) by default.
  */
 void kvq_set_cache_preload(int32_t enable);
