@@ -27,7 +27,10 @@
 // weight (a long window next to a first position that takes most of the mass)
 // keeps its digits in fp16, the score that sets a column's reference weighs
 // 2^(top - kSlack); the reference moves when a weight would pass 2^top, top = kTop, or
-// less where a V scale s is so large that s 2^top would pass fp16.
+// less where a V scale s is so large that s 2^top would pass fp16.  Sums of bf16 V
+// rows from some 2^100 on may leave fp32 with such weights (and would from 2^128 / T on
+// with any that are not made small for it): output elements where that happened
+// are made again, row by row.
 //
 // mma.sync and not tcgen05: a decode step has few columns, and a unit's rows are
 // a few thousand at most, spread over the SMs; 128 positions take 1.2 us of an SM
@@ -265,6 +268,66 @@ struct Block {
   int64_t row;    // first row among the rows of its kind
   bool visual;
 };
+
+// Elements 4 lane .. 4 lane + 3 of cache row t of K (kKey) or V, in fp32.
+template <bool kKey>
+__device__ __forceinline__ float4 elements_of(const Geom& p, const HeadRows& hr, int t, int lane) {
+  const bool visual = t >= p.vs && t < p.ve;
+  const int64_t at = visual ? t - p.vs : (t < p.vs ? t : t - p.Tv);
+  const uint8_t* row = kKey ? (visual ? hr.vis_k : hr.text_k) : (visual ? hr.vis_v : hr.text_v);
+  if (!visual || !(kKey ? hr.k_packed : hr.v_packed)) {
+    const uint2 w = reinterpret_cast<const uint2*>(row + at * kRowBytes)[lane];
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  }
+  const int bits = kKey ? p.kb : p.vb, szrow = kKey ? p.kszrow : p.vszrow, groups = szrow / 4, g = 4 * lane * groups / kD;
+  row += at * (kKey ? p.krow : p.vrow);
+  const __half* sz = reinterpret_cast<const __half*>((kKey ? hr.vis_ksz : hr.vis_vsz) + at * szrow);
+  const float z = __half2float(sz[g]), s = __half2float(sz[groups + g]);
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int slot;  // (kvq.h)
+    if (kKey) {
+      const int P = lane >> 3, tt = (lane >> 1) & 3, e = lane & 1, odd = i & 1;
+      slot = 32 * tt + (bits == 2   ? 16 * (i >> 1) + 8 * e + (P < 3 ? 4 - P + 3 * odd : odd)
+                        : bits == 4 ? 8 * i + 4 * e + P
+                                    : 4 * (2 * P + (i >> 1)) + 2 * e + odd);
+    } else {
+      const int d = 4 * lane + i;
+      slot = 16 * (d & 7) + 2 * (d >> 4) + ((d >> 3) & 1);
+    }
+    const int bit = bits * slot;
+    x[i] = fmaf(static_cast<float>((row[bit >> 3] >> (bit & 7)) & ((1 << bits) - 1)), s, z);
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// Output elements 4 lane .. 4 lane + 3 of the token at position pos for one query
+// column (of Columns::qb), row by row in fp32: with weights that its lse (`ref`, in
+// log2 units) makes add up to 1/4, no sum of finite values leaves fp32.  Called by a
+// whole warp where a sum of the fast way did.
+static __device__ __noinline__ float4 attend_again(const Args& a, int b, int h, const uint4* column, int pos, float ref) {
+  const int lane = threadIdx.x & 31;
+  const HeadRows hr = head_rows(a.c, b, h);
+  const uint2 w = reinterpret_cast<const uint2*>(column + (lane >> 3) * 32 + ((lane >> 1) & 3))[lane & 1];
+  const float4 q = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  const int first = min(a.n_sink, pos + 1), next = max(first, pos - a.window + 1);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < first + pos + 1 - next; ++i) {
+    const int t = i < first ? i : i - first + next;
+    const float4 k = elements_of<true>(a.c, hr, t, lane), v = elements_of<false>(a.c, hr, t, lane);
+    float x = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    const float p = ex2(fmaf(x, a.scale_log2, -ref) - 2.f);
+    l += p;
+    o.x = fmaf(p, v.x, o.x), o.y = fmaf(p, v.y, o.y), o.z = fmaf(p, v.z, o.z), o.w = fmaf(p, v.w, o.w);
+  }
+  const float inv = 1.f / l;
+  return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
 
 template <int KB, int VB, int G, int NT, int W>
 __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kernel(const __grid_constant__ Args a) {
@@ -588,12 +651,23 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
     for (int w = 0; w < kWarps; ++w) l += sm.ml[w][c][1] * ex2(sm.ml[w][c][0] - (M == -INFINITY ? 0.f : M));
     return make_float2(M, l);
   };
-  auto put = [&](int t, int c, int d4, const float4& o, float M, float l) {
+  // (the warp's lanes all have quads of one column; those that are `mine` write)
+  auto put = [&](int t, int c, int d4, float4 o, float M, float l, bool mine) {
     const int cg = (cb * NT + t) * 8 + c, tok = cg / p.g;
     if (idle || tok >= a.n_q) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing attended: 0 (NaN stays)
     const int64_t row = (static_cast<int64_t>(b) * a.n_q + tok) * p.Hq + h * p.g + (cg - tok * p.g);
-    reinterpret_cast<uint2*>(a.out + row * kD)[d4] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    // bf16 V rows from some 2^100 on may have taken a sum past fp32
+    const bool past = l < INFINITY && !(o.x * 0.f + o.y * 0.f + o.z * 0.f + o.w * 0.f == 0.f);
+    if (__builtin_expect(__any_sync(0xffffffffu, past), 0)) {
+      const float4 x = attend_again(a, b, h, &sm.col.qb[t][0][4 * c], p0 + tok, M + log2f(l));
+      const float4 y = make_float4(__shfl_sync(0xffffffffu, x.x, d4), __shfl_sync(0xffffffffu, x.y, d4), __shfl_sync(0xffffffffu, x.z, d4),
+                                   __shfl_sync(0xffffffffu, x.w, d4));
+      if (past) o = y;
+    }
+    if (!mine) return;
+    reinterpret_cast<uint2*>(a.out + row * kD)[d4] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     if (d4 == 0 && a.lse) a.lse[row] = 0.69314718055994531f * (M + log2f(l));
   };
   const uint32_t base = cluster_ctarank() - rank;  // of the unit's CTAs in the cluster
@@ -631,7 +705,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
       }
       if (ranks == 1) {
         const float2 ml = cta_ml(8 * t + c);
-        put(t, c, d4, s, ml.x, ml.y);
+        put(t, c, d4, s, ml.x, ml.y, true);
       } else {
         // outputs of a tile are shared out over the ranks: 256 / ranks quads each
         if (t == 0 && quad == static_cast<int>(threadIdx.x)) cluster_wait();  // every CTA of the cluster has started
@@ -674,7 +748,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 12 / W) window_kern
         o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
         o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
       }
-      if (src == 0) put(t, c, d4, o, M, l);
+      put(t, c, d4, o, M, l, src == 0);
     }
 }
 

@@ -605,8 +605,10 @@ kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, const void* lo
  *   out_bf16  device bf16 [B][n_q][H_q][D];  lse  fp32 [B][n_q][H_q] or NULL
  * A token that attends nothing (p < 0) gets output zero and lse -inf.  Positions
  * may be visual or text, the tokens' own ones too.  Rows that no token attends
- * may hold anything.  Values: K, V and q as in kvq_decode_attention_tree, with
- * bf16 rows of K and V of any size (they are not passed through fp16).  No
+ * may hold anything, the others are finite.  Values: K, V and q as in
+ * kvq_decode_attention_tree, with bf16 rows of K and V of any size (they are not
+ * passed through fp16; output elements whose sums leave fp32, V from some 2^100 on,
+ * take about 0.4 us a position more).  No
  * workspace: a unit's CTAs meet in a thread-block cluster.
  */
 kvq_status kvq_decode_attention_window(const kvq_layout* L, const void* cache, const void* q_bf16, int32_t n_q,
