@@ -20,10 +20,13 @@
 // integers: inv_freq / 2 pi modulo 1 as a 64-bit binary fraction, times the
 // position modulo 2^64.  Its top 32 bits, rounded to fp32, are the angle to
 // 2^-25 of a turn, and the fast sine and cosine of it are off by 2^-21.  The rest
-// is fp32, in pairs, rounded once to bf16.
+// is fp32, in pairs, rounded once to bf16.  Squares leave fp32 for elements outside
+// some 2^-63 .. 2^63: a row whose mean + eps is not in [2^-100, 2^128) is not stored but
+// made again at the end, scaled by a power of two.
 //
-// Measured (GB300): 8 x 2940 tokens, 40 + 40 heads with norms (963 MB) 162 us, 5.9
-// TB/s, 0.88 of a copy; 16 x 26 tokens, 32 + 32 heads 5.0 us; one token 2.1 us.
+// Measured (GB300): 8 x 2940 tokens, 40 + 40 heads with norms (963 MB) 167 us (162
+// without the look at the means' range), 5.8 TB/s, 0.85 of a copy; 16 x 26 tokens, 32 +
+// 32 heads 5.1 us; one token 2.0 us.
 #include "kvq_geom.cuh"
 
 #include <algorithm>
@@ -95,6 +98,19 @@ __device__ __forceinline__ void join(uint64_t& x0, uint64_t& x1, uint64_t& y0, u
     y0 = pair_of(c, g);
     y1 = pair_of(d, h);
   }
+}
+
+constexpr uint32_t kLeastMean = 27u << 23;  // 2^-100: squares that underflowed are 2^-43 of it at most
+
+// The power of two that takes a row's largest element to [1, 2), or to where its
+// square is far from fp32's ends.  Called by whole warps, 16 lanes a row (the caller
+// takes the rows that want it).
+__device__ __forceinline__ float to_one(uint2 x, uint2 y) {
+  uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu));
+  top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+  for (int o = 1; o < kRowLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return __int_as_float((127 - max(-100, min(100, static_cast<int>(top >> 7) - 127))) << 23);
 }
 
 // f / 2 pi modulo 1 in units of 2^-64, to 2 of them for |f| < 2.
@@ -177,18 +193,27 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 3 : 4) norm_rope_k
   }
   uint16_t* to = s.out + b * s.ob + t * s.ot + h0 * s.oh + e0;
   const int64_t oh = s.oh;
-#pragma unroll
-  for (int k = 0; k < kHeads; ++k) {
+  // A row's two chunks times r to its output: where `mine` is set, and unless its squares
+  // leave fp32 (returns that they do, once r is 1).
+  auto put = [&](uint2 xk, uint2 yk, auto scaled, float r, uint16_t* at, bool mine) {
+    bool far = false;
     uint64_t u0, u1, v0, v1;
-    wide(x[k], u0, u1);
-    wide(y[k], v0, v1);
+    wide(xk, u0, u1);
+    wide(yk, v0, v1);
     if (norm) {
+      if constexpr (decltype(scaled)::value) {
+        const uint64_t rr = pair_of(r, r);
+        u0 = mul_pair(u0, rr), u1 = mul_pair(u1, rr), v0 = mul_pair(v0, rr), v1 = mul_pair(v1, rr);
+      }
       float lo, hi;
       unpair(fma_pair(u0, u0, fma_pair(u1, u1, fma_pair(v0, v0, mul_pair(v1, v1)))), lo, hi);
       float sum = lo + hi;
 #pragma unroll
       for (int o = 1; o < kRowLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float f = rsqrtf(fmaf(sum, 1.f / kD, a.eps));
+      const float mean = fmaf(sum, 1.f / kD, decltype(scaled)::value ? a.eps * r * r : a.eps);
+      if constexpr (!decltype(scaled)::value)  // not in [2^-100, infinity)
+        far = mine && __float_as_uint(mean) - kLeastMean >= 0x7f800000u - kLeastMean;
+      const float f = rsqrtf(mean);
       const uint64_t ff = pair_of(f, f);
       u0 = mul_pair(u0, ff), u1 = mul_pair(u1, ff), v0 = mul_pair(v0, ff), v1 = mul_pair(v1, ff);
     }
@@ -201,11 +226,30 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 3 : 4) norm_rope_k
     } else if (norm) {
       u0 = mul_pair(u0, p0), u1 = mul_pair(u1, p1), v0 = mul_pair(v0, q0), v1 = mul_pair(v1, q1);
     }
-    if (live && k < rows) {
-      *reinterpret_cast<uint2*>(to) = make_uint2(narrow(u0), narrow(u1));
-      *reinterpret_cast<uint2*>(to + gap) = make_uint2(narrow(v0), narrow(v1));
+    if (mine && !far) {
+      *reinterpret_cast<uint2*>(at) = make_uint2(narrow(u0), narrow(u1));
+      *reinterpret_cast<uint2*>(at + gap) = make_uint2(narrow(v0), narrow(v1));
     }
+    return far;
+  };
+  uint32_t again = 0;
+#pragma unroll
+  for (int k = 0; k < kHeads; ++k) {
+    if (put(x[k], y[k], std::false_type(), 1.f, to, live && k < rows)) again |= 1u << k;
     to += oh;
+  }
+  const uint32_t any = __reduce_or_sync(0xffffffffu, again);
+  if (__builtin_expect(any != 0, 0)) {  // those rows' inputs are as they were
+    const uint16_t* const row0 = s.in + b * s.sb + t * s.st + h0 * s.sh + e0;
+    to -= kHeads * oh;
+#pragma unroll 1
+    for (int k = 0; k < kHeads; ++k) {
+      if (!(any >> k & 1)) continue;
+      const bool mine = again >> k & 1;
+      uint2 xk = make_uint2(0u, 0u), yk = xk;
+      if (mine) xk = *reinterpret_cast<const uint2*>(row0 + k * s.sh), yk = *reinterpret_cast<const uint2*>(row0 + k * s.sh + gap);
+      put(xk, yk, std::true_type(), to_one(xk, yk), to + k * oh, mine);
+    }
   }
 }
 

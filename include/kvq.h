@@ -511,7 +511,8 @@ kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* 
  *             may pos, inv_freq or a weight lie inside an output's span.  Rows
  *             of k_out may be text rows of a cache (kvq_set_cache_preload)
  * Arithmetic is fp32 (angles are taken modulo a turn exactly, whatever the
- * position), rounded to bf16 once.  A NaN or infinity in a row stays in it.
+ * position), rounded to bf16 once; finite rows of any size are normed by the formula
+ * (a zero row with eps = 0 is NaN).  A NaN or infinity in a row stays in it.
  */
 typedef struct kvq_rope_desc {
   int32_t rot_dim;     /* elements turned: a multiple of 8, 8..D */
