@@ -113,20 +113,25 @@ __device__ __forceinline__ float to_one(uint2 x, uint2 y) {
   return __int_as_float((127 - max(-100, min(100, static_cast<int>(top >> 7) - 127))) << 23);
 }
 
-// f / 2 pi modulo 1 in units of 2^-64, to 2 of them for |f| < 2.
+// f / 2 pi modulo 1 in units of 2^-64, to 2 of them for every finite f: the 24 bits
+// m of f times the bits of 1 / 2 pi that do not make whole turns (reduction as
+// published by Payne and Hanek, 1983).
 __device__ __forceinline__ uint64_t turn_of(float f) {
+  constexpr uint64_t kInv = 0x28be60db9391054aull;  // 2^64 / 2 pi
   const uint32_t u = __float_as_uint(f), e = (u >> 23) & 0xff;
   uint64_t t;
-  if (e <= 127) {  // m 2^(e - 150) / 2 pi, m the 24 bits of f: one product by the 64 bits of 1 / 2 pi
+  if (e <= 127) {  // m 2^(e - 150) / 2 pi: one product by the first 64 bits of 1 / 2 pi
     const uint32_t m = e ? (u & 0x7fffffu) | 0x800000u : (u & 0x7fffffu) << 1;
-    constexpr uint64_t kInv = 0x28be60db9391054aull;  // 2^64 / 2 pi
     const uint64_t lo = static_cast<uint64_t>(m) * static_cast<uint32_t>(kInv), hi = static_cast<uint64_t>(m) * static_cast<uint32_t>(kInv >> 32) + (lo >> 32);
     const int s = 150 - static_cast<int>(e);  // 23 and more; the product is hi 2^32 + low half of lo
     t = s < 32 ? (hi << (32 - s)) | (static_cast<uint32_t>(lo) >> s) : (s < 96 ? hi >> (s - 32) : 0ull);
-  } else {
-    double d = static_cast<double>(fabsf(f)) * 0.15915494309189533577;
-    d -= floor(d);
-    t = d < 1.0 ? static_cast<uint64_t>(d * 18446744073709551616.0) : 0ull;
+  } else {  // |f| >= 2: m times the 128 bits of 1 / 2 pi behind its first e - 150
+    constexpr uint64_t k1 = 0x7f09d5f47d4d3770ull, k2 = 0x36d8a5664f10e410ull, k3 = 0x7f9458eaf7aef158ull;  // its next bits
+    const uint64_t m = (u & 0x7fffffu) | 0x800000u;
+    const int o = static_cast<int>(e) - 150 + 64, r = o & 63;  // 42 .. 169, from 64 zero bits before the first on
+    const uint64_t x = o < 64 ? 0ull : (o < 128 ? kInv : k1), y = o < 64 ? kInv : (o < 128 ? k1 : k2), z = o < 64 ? k1 : (o < 128 ? k2 : k3);
+    const uint64_t w0 = r ? (x << r) | (y >> (64 - r)) : x, w1 = r ? (y << r) | (z >> (64 - r)) : y;
+    t = m * w0 + __umul64hi(m, w1);
   }
   return u >> 31 ? 0ull - t : t;
 }

@@ -510,8 +510,8 @@ kvq_status kvq_cache_evict(const kvq_layout* L, const void* cache, const float* 
  *             q_out must share no row with k, nor k_out with q or q_out, nor
  *             may pos, inv_freq or a weight lie inside an output's span.  Rows
  *             of k_out may be text rows of a cache (kvq_set_cache_preload)
- * Arithmetic is fp32 (angles are taken modulo a turn exactly, whatever the
- * position), rounded to bf16 once; finite rows of any size are normed by the formula
+ * Arithmetic is fp32 (angles are taken modulo a turn to 2^-25 of it, whatever the
+ * position and the frequency), rounded to bf16 once; finite rows of any size are normed by the formula
  * (a zero row with eps = 0 is NaN).  A NaN or infinity in a row stays in it.
  */
 typedef struct kvq_rope_desc {
