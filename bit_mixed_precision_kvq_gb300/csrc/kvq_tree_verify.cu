@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(X) == 4 ? 2 : 1) verify
   Share<X> row(rows, a.V, rank, ranks);
   row.begin(ring);
   const bool greedy = !(temp > 0.f);
-  const float sc = greedy ? kLog2e : kLog2e / temp;
+  const float sc = greedy ? kLog2e : fminf(kLog2e / temp, 3.4028235e38f);  // (finite for subnormal temperatures, too)
   bool good = n >= 1 && n <= a.n_q;
   __syncthreads();  // kids is zero
   if (tid < KVQ_MAX_QUERY_TOKENS) {

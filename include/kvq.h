@@ -553,6 +553,9 @@ kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R, const kvq_
  * the refused token ids out); greedy, or where no such value is above 0, the
  * token id of the largest logit.  With u uniform in [0, 1) and race exponential
  * the tokens are distributed as the target's samples.  Ties go to the lowest v.
+ * The arithmetic is fp32: p is off by some 2^-20 of itself, so a decision or pick
+ * whose two sides are nearer than 2^-14 of the p and q that they come from may
+ * fall either way, and p, r and race below 2^-126 count as 0 (race: as the smallest).
  *   B         sequences, >= 1 (KVQ_ERR_UNSUPPORTED above 65535)
  *   n_q       tokens of a tree, 1 <= n_q <= KVQ_MAX_QUERY_TOKENS
  *   vocab     1 <= vocab <= 2^30
@@ -564,11 +567,13 @@ kvq_status kvq_norm_rope(const kvq_layout* L, const kvq_rope_desc* R, const kvq_
  *   draft_prob  device fp32, entry (b, i, v) at index b*draft_stride_b +
  *             i*draft_stride_t + v, or NULL; a token id whose entry is NaN
  *             is refused and not picked after a refusal
- *   accept    device fp32 [B][n_q]: u of each token (token 0's does not count);
- *             a NaN refuses it, and a p or r of 0 is refused whatever u is
+ *   accept    device fp32 [B][n_q]: u of each token (token 0's and those of greedy
+ *             sequences do not count); a NaN refuses it, and a p or r of 0 is
+ *             refused whatever u is
  *   race      device fp32 [B][vocab]: a v whose entry is not above 0 is not picked
  *   temperature  device fp32 [B] or NULL (1 for all); finite, and so is
- *             logit / temperature for the finite logits
+ *             logit / temperature for the finite logits (below 2^-127 it counts
+ *             as about that)
  *   tree_len  device int32 [B]: tokens of each tree (later ones do not count),
  *             or NULL (n_q); an entry outside [1, n_q] marks an inactive sequence
  *   path      device int32 [B][n_q]: the tokens on the path, -1 behind the last

@@ -1,5 +1,5 @@
 """kvq_tree_verify where refused siblings hold nearly all of the probability:
-what they leave is held against random numbers next to their borders."""
+what they leave is held against random numbers next to their borders.  Tiny temperatures."""
 import numpy as np
 import pytest
 import torch
@@ -107,3 +107,12 @@ def test_nothing_left(cuda_dev, kvq):
     s.t = torch.from_numpy(s.x)
     out = run(kvq, cuda_dev, s)
     assert out[1].tolist() == [1, 1, 1] and out[2].tolist() == s.tokens[:, 1].tolist()
+
+
+def test_tiny_temperatures(cuda_dev, kvq):
+    """Temperatures whose inverse leaves fp32, with logits that stay finite over them."""
+    s = Rest(4, 3, 3001, False, [0.5], [1], 312)
+    s.x[:] = np.random.default_rng(313).integers(-3, 1, s.x.shape) * np.float32(2.0 ** -4)
+    s.t = torch.from_numpy(s.x)
+    heat = [2e-39, 1e-39, 1e-38, 4e-39]
+    check_verify(run(kvq, cuda_dev, s, heat), verify_reference(s.x, s.tokens, s.masks, s.u, s.race, None, heat))
