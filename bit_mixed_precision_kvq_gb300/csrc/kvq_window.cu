@@ -17,13 +17,22 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
     return KVQ_ERR_INVALID_ARG;
   if (n_q < 1 || n_q > KVQ_MAX_QUERY_TOKENS || T < 1 || T > L->d.T_cap) return KVQ_ERR_INVALID_ARG;
   if (n_sink < 0 || window < 1 || !std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
-  if (T > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;
   const int64_t cols = static_cast<int64_t>(L->g) * n_q;
   kvq::win::Form f;
   f.nt = cols > 8 ? 2 : 1;
   const int64_t nblk = (cols + 8 * f.nt - 1) / (8 * f.nt);
   const int64_t units = static_cast<int64_t>(L->d.B) * L->d.H_kv * nblk;
   if (units > 0x3ffffff || cols > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;  // 16 CTAs a unit at most
+  // The outputs lie apart from one another and from the inputs; out may be q itself
+  // (a unit's CTAs have read their rows of q before any of them writes).
+  const int64_t rows = static_cast<int64_t>(L->d.B) * n_q * L->d.H_q, wide = rows * kvq::kRowBytes;
+  const int64_t total = static_cast<int64_t>(L->total_bytes), lens = 4 * static_cast<int64_t>(L->d.B);
+  if (kvq::ranges_meet(out_bf16, wide, cache, total) || kvq::ranges_meet(out_bf16, wide, seq_len, lens) ||
+      kvq::ranges_meet(out_bf16, wide, lse, 4 * rows) || (out_bf16 != q_bf16 && kvq::ranges_meet(out_bf16, wide, q_bf16, wide)) ||
+      kvq::ranges_meet(lse, 4 * rows, cache, total) || kvq::ranges_meet(lse, 4 * rows, seq_len, lens) ||
+      kvq::ranges_meet(lse, 4 * rows, q_bf16, wide))
+    return KVQ_ERR_INVALID_ARG;
+  if (T > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
   // Two tiles of columns unpack a row once (16 columns x 1280 units: 91 us, 105
@@ -62,9 +71,9 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
   // CTAs a unit: those of the class with the longest share double while one
   // wave holds them all and no CTA is without a block for its warps.  A row costs
   // its bytes and some work (kPosCost); the longest call counts.
-  const int64_t rows = std::min<int64_t>(T, static_cast<int64_t>(a.n_sink) + a.window + n_q - 1);
-  const int64_t vis = std::min<int64_t>(rows, L->Tv), v = L->row_bytes[KVQ_SEG_V_CODES] + L->row_bytes[KVQ_SEG_V_SZ];
-  const int64_t text = (rows - vis) * kvq::kBf16PosCost;
+  const int64_t seen = std::min<int64_t>(T, static_cast<int64_t>(a.n_sink) + a.window + n_q - 1);
+  const int64_t vis = std::min<int64_t>(seen, L->Tv), v = L->row_bytes[KVQ_SEG_V_CODES] + L->row_bytes[KVQ_SEG_V_SZ];
+  const int64_t text = (seen - vis) * kvq::kBf16PosCost;
   const int64_t cost[3] = {text + vis * kvq::kBf16PosCost, text + vis * (kvq::kRowBytes + v + kvq::kPosCost),
                            text + vis * (L->row_bytes[KVQ_SEG_K_CODES] + L->row_bytes[KVQ_SEG_K_SZ] + v + kvq::kPosCost)};
   const int64_t wave = static_cast<int64_t>(n_sm) * (f.warps == 4 ? 3 : 2);
@@ -73,7 +82,7 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
     int worst = -1;
     for (int k = 0; k < 3; ++k)
       if (a.U[k] && (worst < 0 || cost[k] * S[worst] > cost[worst] * S[k])) worst = k;
-    if (worst < 0 || S[worst] >= kvq::win::kMaxRanks || S[worst] * f.warps * 16 >= rows) break;
+    if (worst < 0 || S[worst] >= kvq::win::kMaxRanks || S[worst] * f.warps * 16 >= seen) break;
     int64_t used = 0;
     for (int k = 0; k < 3; ++k) used += static_cast<int64_t>(a.U[k]) * S[k] * (k == worst ? 2 : 1);
     if (used > wave) break;

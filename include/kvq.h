@@ -608,7 +608,9 @@ kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, const void* lo
  *   T         1 <= T <= T_cap: the (largest) length (KVQ_ERR_UNSUPPORTED above
  *             2^31 - 2^16)
  *   n_sink    >= 0;  window  >= 1 (a window of T or more hides nothing)
- *   out_bf16  device bf16 [B][n_q][H_q][D];  lse  fp32 [B][n_q][H_q] or NULL
+ *   out_bf16  device bf16 [B][n_q][H_q][D];  lse  fp32 [B][n_q][H_q] or NULL.
+ *             They must not share memory with one another or with an input, but
+ *             out_bf16 may be q_bf16 itself
  * A token that attends nothing (p < 0) gets output zero and lse -inf.  Positions
  * may be visual or text, the tokens' own ones too.  Rows that no token attends
  * may hold anything, the others are finite.  Values: K, V and q as in
