@@ -17,9 +17,9 @@
 // the memory system: of a row of 32,000 in 8 CTAs the pass takes 1,800 cycles, the
 // exchange and the decision 2,700; of 128,000 in 4 CTAs (a batch of 32) 5,000
 // and 2,500, at about 100 instructions for 8 logits and half of the issue slots.
-// Measured (GB300): 5 drafts, vocabulary 32,000, 1.8 rows on average 7.5 us; 16
+// Measured (GB300): 5 drafts, vocabulary 32,000, 1.8 rows on average 7.9 us; 16
 // sampled drafts, 152,000, 4.2 rows 18 us; 32 sequences of 64 sampled drafts,
-// 128,000, 4.2 rows on average and 8 or more on the longest walk 58 us (the rows
+// 128,000, 4.2 rows on average and 8 or more on the longest walk 58.5 us (the rows
 // that are read take 10 at the rate of a copy).  Rolled loops: unrolled over a
 // thread's groups the code of a pass that runs once a call comes from L2 (130 us
 // became 68).  1,024 threads a CTA, two groups a turn, draft rows asked for ahead
@@ -713,9 +713,12 @@ extern "C" kvq_status kvq_tree_verify(int32_t B, int32_t n_q, int32_t vocab, con
   const int smem = logits_fp32 ? sizeof(kvq::Ring<16>) : sizeof(kvq::Ring<32>);
   const kvq_status st = kvq_allow_clusters(fn, smem);
   if (st != KVQ_OK) return st;
-  // As many CTAs a sequence as one wave holds, but none below 8 bytes a thread
-  // (32,000 logits of one sequence in 8 CTAs: 7.4 us, in 4, the next below 16
-  // bytes, 9.6).
+  // As many CTAs a sequence as the SMs hold, one each, but none below 8 bytes a
+  // thread (32,000 logits of one sequence in 8 CTAs: 7.4 us when this was chosen, in 4, the
+  // next below 16 bytes, 9.6).  A cluster lies within one GPC, which this does not look at:
+  // with bf16 logits, whose CTAs fill an SM, the last clusters of 8 and 9, 16 to
+  // 19 or 38 sequences wait for the first (two rows of 64,000: 14.2 us where 10
+  // sequences take 8.3, 16.1 where 20 take 10.3, 20.0 where 39 take 14.1).
   int ranks = 1;
   while (ranks < kvq::kMaxRanks && 2 * ranks * static_cast<int64_t>(B) <= n_sm &&
          ranks * 16 * kvq::kVerifyThreads <= static_cast<int64_t>(vocab) * elt)

@@ -35,11 +35,11 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
   if (T > kvq::kMaxLen) return KVQ_ERR_UNSUPPORTED;
   int n_sm = 0;
   if (kvq_device_sm_count(&n_sm) != 0) return KVQ_ERR_CUDA;
-  // Two tiles of columns unpack a row once (16 columns x 1280 units: 91 us, 105
+  // Two tiles of columns unpack a row once (16 columns x 1280 units: 85 us, 104
   // as two units of one tile).  Units enough for every SM: CTAs of four warps, one a
-  // unit, several an SM (512 units of 345 positions 16 us, 21 with eight warps);
-  // else eight warps, for more of them a unit (64 units of 8,257 positions 24 us, 41
-  // with four; four units of 2,078 6.4 and 8.0).
+  // unit, several an SM (512 units of 345 positions 15.3 us, 20.0 with eight warps);
+  // else eight warps, for more of them a unit (64 units of 8,257 positions 21.6 us, 36
+  // with four; four units of 2,078 6.2 and 7.3).
   f.warps = f.nt == 2 || units >= 2 * n_sm ? 4 : 8;
   const kvq::win::Kernel k = L->d.k_bits == 2   ? kvq::win::window_kernel_k2(L->d.v_bits, L->d.group_size, f)
                              : L->d.k_bits == 4 ? kvq::win::window_kernel_k4(L->d.v_bits, L->d.group_size, f)
@@ -70,7 +70,9 @@ extern "C" kvq_status kvq_decode_attention_window(const kvq_layout* L, const voi
   }
   // CTAs a unit: those of the class with the longest share double while one
   // wave holds them all and no CTA is without a block for its warps.  A row costs
-  // its bytes and some work (kPosCost); the longest call counts.
+  // its bytes and some work (kPosCost); the longest call counts.  (Of four warps, three
+  // an SM: what two column tiles leave room for.  One tile's CTAs would fit four
+  // times, and GPCs that a cluster does not fill are not looked at.)
   const int64_t seen = std::min<int64_t>(T, static_cast<int64_t>(a.n_sink) + a.window + n_q - 1);
   const int64_t vis = std::min<int64_t>(seen, L->Tv), v = L->row_bytes[KVQ_SEG_V_CODES] + L->row_bytes[KVQ_SEG_V_SZ];
   const int64_t text = (seen - vis) * kvq::kBf16PosCost;

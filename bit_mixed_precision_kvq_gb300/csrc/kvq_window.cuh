@@ -39,13 +39,14 @@
 // Bound by instruction issue and latency (530 instructions a block of 32 packed
 // rows and 8 columns, half of the issue slots used at 12 to 16 warps an SM), small
 // calls by their start, a block and the two meetings.  Measured (GB300): 2,078
-// positions of a LLaVA-OneVision layer 6.1 us; a window of 8K of 32K x 8 in 2 bits
+// positions of a LLaVA-OneVision layer 6.2 us; a window of 8K of 32K x 8 in 2 bits
 // (80 MB) 21.6 us, 3.7 TB/s; 16 tokens over 1,103 positions x 32 x 40 heads (281
 // MB, 11.6 GFLOP) 85 us.  Steps: units split by the rows they hold (24 us where
 // equal shares took 31), unpacked codes shared by two column tiles and three CTAs
 // of 168 registers an SM (91 us, before 137 with one of eight warps), a loop for
 // each kind of rows (85, before 88), the first rows asked for while the previous
-// kernel ends (6.1 and 21.6 us, before 6.5 and 22.4).
+// kernel ends (6.1 and 21.6 us, before 6.5 and 22.4), the check for sums past fp32 (6.2,
+// 21.6 and 85.1 us, before 6.1, 21.5 and 84.5).
 #pragma once
 
 #include <cstddef>
